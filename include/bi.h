@@ -257,6 +257,90 @@ bi_status bi_kv_append(const bi_bf16* k_new, const bi_bf16* v_new, int64_t ld_ne
                        int Hkv, int D, void* stream);
 
 /*
+ * The 8-bit paged KV store. No page describes it; it is the unified paged store above at
+ * half the bytes per token, with the same page tables, and every operation on it keeps the
+ * same promise (a row's bits depend on that row's inputs only).
+ * k_cache, v_cache: [num_pages, Hkv, 16, D] 8-bit values (16-byte aligned), of the kind
+ * BI_KV_INT8 (signed integers) or BI_KV_E4M3 (fp8 e4m3, finite-only form: no infinities);
+ * k_scale, v_scale: [num_pages, Hkv, 16] fp32 (16-byte aligned). A slot's row of D values v
+ * with scale s stands for v * s.
+ *
+ * bi_kv_append_q8: bi_kv_append's rows and slots; row x with a = max |x| is stored as
+ *   BI_KV_INT8: s = a / 127 (rounded to fp32), v = the integer nearest to 127 x / a (exact
+ *     quotient, ties to even);
+ *   BI_KV_E4M3: s = 2^e, the least power of two with a <= 448 s, v = x / s rounded to e4m3
+ *     (nearest, ties to even);
+ *   a < 2^-100: v = 0, s = 1; a row with a NaN or an infinity: v = 0, s = NaN (the row reads
+ *     back as NaN, and so does attention that sees it).
+ *   Out-of-range ids set the device error word and skip the token. The slots of one call must
+ *   be distinct: two rows for one slot leave an unspecified mix of both in it.
+ * bi_kv_read_q8: row t of k_out / v_out (at t * ld_out, [Hkv, D] bf16) = bf16(v s) of slot
+ *   (q_seq[t], q_pos[t]), the product in fp32; zeros (and the device error word) where an id is
+ *   out of range. Rows may repeat. The outputs overlap neither each other nor the store.
+ * D in {64, 128}. ld_new, ld_out >= Hkv * D and % 8 == 0. T == 0 is a no-op.
+ */
+#define BI_KV_INT8 0
+#define BI_KV_E4M3 1
+bi_status bi_kv_append_q8(const bi_bf16* k_new, const bi_bf16* v_new, int64_t ld_new, const int32_t* q_seq,
+                          const int32_t* q_pos, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                          int kind, int64_t num_pages, const int32_t* page_table, int num_seqs,
+                          int max_pages_per_seq, int T, int Hkv, int D, void* stream);
+bi_status bi_kv_read_q8(bi_bf16* k_out, bi_bf16* v_out, int64_t ld_out, const int32_t* q_seq, const int32_t* q_pos,
+                        const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                        int kind, int64_t num_pages, const int32_t* page_table, int num_seqs,
+                        int max_pages_per_seq, int T, int Hkv, int D, void* stream);
+
+/*
+ * Attention over the 8-bit store: bi_attention_decode and bi_attention_prefill with the store
+ * above in place of the bf16 one. Keys and values are the exact v * s; with
+ * z_t = scale log2(e) q.(k_t sk_t) + log2 sv_t and w_t = 2^(z_t - max z),
+ *   out = sum_t w_t v_t / sum_t (w_t / sv_t)    (= softmax(scale q.k) v),
+ * the products on tensor cores in f16 with fp32 sums (8-bit values are exact in f16; a query
+ * row is scaled by a power of two; 2^14 w_t is rounded to f16), everything else in fp32, one
+ * rounding to bf16. Splits of 256 tokens at absolute positions, pages in order, splits folded
+ * in ascending order: a row's bits depend on its own length and slots only, and a prefill row
+ * equals the decode row at its position bit for bit (they are not the bits of the bf16 store's
+ * calls). Slots past a row's length are never folded in, whatever bytes and scales they hold;
+ * a row that sees nothing (length 0, q_pos -1) yields zeros; a page id outside the store sets
+ * the device error word and its tokens are not seen. Every slot that a row sees was written by
+ * bi_kv_append_q8 (its scale is a positive normal number, or NaN, which gives NaN).
+ * Hq % Hkv == 0 and Hq / Hkv in 1..16; D in {64, 128}. out must not overlap q.
+ * bi_attention_decode_q8: workspace >= bi_attention_workspace_size(B, Hq, D, max_pages).
+ * bi_attention_prefill_q8: q's rows ldq apart; rows of one sequence that follow one another
+ *   in the batch (a chunk) are taken together, which costs nothing in bits and is what makes
+ *   a chunk fast; workspace >= bi_attention_prefill_q8_workspace_size(T).
+ */
+bi_status bi_attention_decode_q8(const bi_bf16* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                 const float* v_scale, int kind, int64_t num_pages, const int32_t* page_table,
+                                 int max_pages_per_seq, const int32_t* seq_lens, bi_bf16* out, int B, int Hq,
+                                 int Hkv, int D, float scale, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+size_t bi_attention_prefill_q8_workspace_size(int64_t T);
+bi_status bi_attention_prefill_q8(const bi_bf16* q, int64_t ldq, const int32_t* q_seq, const int32_t* q_pos,
+                                  const void* k_cache, const void* v_cache, const float* k_scale,
+                                  const float* v_scale, int kind, int64_t num_pages, const int32_t* page_table,
+                                  int num_seqs, int max_pages_per_seq, bi_bf16* out, int T, int Hq, int Hkv, int D,
+                                  float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * RMSNorm of every query and key head with the rotary embedding in the same pass (models that
+ * norm each head before the rotation). Row t of q holds [Hq, D] bf16 at t * ldq, of k [Hkv, D]
+ * at t * ldk (e.g. parts of a fused QKV row); each head row x at position p = pos[t] becomes
+ *   n_i = (x_i r) w_i, r = rsqrt(mean_i x_i^2 + eps), with w = q_weight or k_weight [D],
+ *   y_i = n_i c - n_{i+D/2} s,  y_{i+D/2} = n_{i+D/2} c + n_i s,  i < D/2,
+ * (c, s) as for bi_rope, all in fp32 and rounded to bf16 once (bi_rmsnorm then bi_rope would
+ * round n as well). y goes to q_out / k_out (rows ldq_out / ldk_out apart), which may be q / k
+ * themselves with the same row stride and otherwise overlap neither them nor each other. A
+ * position outside [0, max_pos) sets the device error word and leaves that row's outputs
+ * unwritten. One fixed reduction order per head row. D in {64, 128, 256}; cos_sin
+ * [max_pos][D/2][2] fp32, 16-byte aligned. T == 0 is a no-op.
+ */
+bi_status bi_qk_norm_rope(const bi_bf16* q, int64_t ldq, const bi_bf16* k, int64_t ldk, const bi_bf16* q_weight,
+                          const bi_bf16* k_weight, const int32_t* pos, const float* cos_sin, int max_pos, float eps,
+                          bi_bf16* q_out, int64_t ldq_out, bi_bf16* k_out, int64_t ldk_out, int64_t T, int Hq,
+                          int Hkv, int D, void* stream);
+
+/*
  * Glue of a Llama-style decoder step. Each output element depends only on its own
  * row's inputs (copies and elementwise fp32 math), so these are batch-invariant by
  * construction; they keep a whole decoder step inside this library between the

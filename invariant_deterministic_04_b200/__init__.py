@@ -8,7 +8,9 @@ libbi.so is missing or fails to load, every call raises ``BIError``.
 Operations (see include/bi.h for the exact contracts):
   rmsnorm, matmul, matmul_multi, matmul_tile_n, matmul_tile_m, attention_decode, attention_decode_static, attention_prefill,
   kv_append, lmhead_argmax, gather_rows, rope, swiglu, add, log_softmax,
-  token_logprob, row_mean, sampling_uniforms, sample, get_device_error.
+  token_logprob, row_mean, sampling_uniforms, sample, get_device_error; with the
+  8-bit paged KV store: kv_append_q8, kv_read_q8, attention_decode_q8,
+  attention_prefill_q8; for models that norm each head: qk_norm_rope.
 """
 from __future__ import annotations
 
@@ -54,6 +56,15 @@ _SIGNATURES = {
     "bi_attention_prefill_tc": ([_P, _I64, _I32, _I32, _I32, _P, _P, _I64, _P, _I32, _I32, _P, _I32, _I32, _I32, _F,
                                  _P], _I32),
     "bi_kv_append": ([_P, _P, _I64, _P, _P, _P, _P, _I64, _P, _I32, _I32, _I32, _I32, _I32, _P], _I32),
+    "bi_kv_append_q8": ([_P, _P, _I64, _P, _P, _P, _P, _P, _P, _I32, _I64, _P, _I32, _I32, _I32, _I32, _I32, _P], _I32),
+    "bi_kv_read_q8": ([_P, _P, _I64, _P, _P, _P, _P, _P, _P, _I32, _I64, _P, _I32, _I32, _I32, _I32, _I32, _P], _I32),
+    "bi_attention_decode_q8": ([_P, _P, _P, _P, _P, _I32, _I64, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _F, _P, _SZ,
+                                _P], _I32),
+    "bi_attention_prefill_q8_workspace_size": ([_I64], _SZ),
+    "bi_attention_prefill_q8": ([_P, _I64, _P, _P, _P, _P, _P, _P, _I32, _I64, _P, _I32, _I32, _P, _I32, _I32, _I32,
+                                 _I32, _F, _P, _SZ, _P], _I32),
+    "bi_qk_norm_rope": ([_P, _I64, _P, _I64, _P, _P, _P, _P, _I32, _F, _P, _I64, _P, _I64, _I64, _I32, _I32, _I32, _P],
+                        _I32),
     "bi_gather_rows": ([_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P], _I32),
     "bi_rope": ([_P, _I64, _I64, _I32, _I32, _P, _P, _I32, _P], _I32),
     "bi_swiglu": ([_P, _I64, _P, _I64, _I64, _I64, _P], _I32),
@@ -445,6 +456,199 @@ def kv_append(k_new, v_new, q_seq, q_pos, k_cache, v_cache, page_table, stream=N
         _check("bi_kv_append", lib().bi_kv_append(
             _ptr(k_new), _ptr(v_new), ld, _ptr(q_seq), _ptr(q_pos), _ptr(k_cache), _ptr(v_cache), k_cache.shape[0],
             _ptr(page_table), num_seqs, maxp, T, Hkv, D, _stream()))
+
+
+_KV_KINDS = {torch.int8: 0, torch.float8_e4m3fn: 1}
+
+
+def _store_q8(k_cache, v_cache, k_scale, v_scale, page_table):
+    """Check an 8-bit store; returns (num_pages, Hkv, D, kind)."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dtype not in _KV_KINDS:
+        raise TypeError("k_cache must be a CUDA tensor of torch.int8 or torch.float8_e4m3fn")
+    _req(k_cache, k_cache.dtype, "k_cache", 4)
+    _req(v_cache, k_cache.dtype, "v_cache", 4)
+    _req(k_scale, torch.float32, "k_scale", 3)
+    _req(v_scale, torch.float32, "v_scale", 3)
+    _req(page_table, torch.int32, "page_table", 2)
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale"),
+                 (page_table, "page_table")):
+        _contig(t, n)
+    num_pages, Hkv, P, D = k_cache.shape
+    if v_cache.shape != k_cache.shape or P != PAGE_TOKENS:
+        raise ValueError("k_cache/v_cache must be [num_pages, Hkv, 16, D]")
+    if k_scale.shape != (num_pages, Hkv, P) or v_scale.shape != k_scale.shape:
+        raise ValueError("k_scale/v_scale must be [num_pages, Hkv, 16]")
+    return num_pages, Hkv, D, _KV_KINDS[k_cache.dtype]
+
+
+def _row_ids(q_seq, q_pos, T: int):
+    for t, n in ((q_seq, "q_seq"), (q_pos, "q_pos")):
+        _req(t, torch.int32, n, 1)
+        _contig(t, n)
+        if t.shape[0] != T:
+            raise ValueError("q_seq and q_pos need one entry per row")
+
+
+def kv_append_q8(k_new, v_new, q_seq, q_pos, k_cache, v_cache, k_scale, v_scale, page_table, stream=None):
+    """Quantise k_new/v_new [T, Hkv, D] (rows may be strided) into the 8-bit store at (q_seq[t], q_pos[t]).
+
+    k_cache/v_cache [num_pages, Hkv, 16, D] int8 or float8_e4m3fn, k_scale/v_scale
+    [num_pages, Hkv, 16] fp32: a slot's row stands for value * scale. The slots of one
+    call must be distinct."""
+    num_pages, Hkv, D, kind = _store_q8(k_cache, v_cache, k_scale, v_scale, page_table)
+    _req(k_new, torch.bfloat16, "k_new", 3)
+    _req(v_new, torch.bfloat16, "v_new", 3)
+    ld = _rows3(k_new, "k_new")
+    T = k_new.shape[0]
+    if _rows3(v_new, "v_new") != ld or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must have the same shape and row stride")
+    if k_new.shape[1:] != (Hkv, D):
+        raise ValueError(f"k_new must be [T, {Hkv}, {D}] to match the store, got {tuple(k_new.shape)}")
+    _row_ids(q_seq, q_pos, T)
+    device = _same_device(k_new, v_new, q_seq, q_pos, k_cache, v_cache, k_scale, v_scale, page_table)
+    if T == 0:  # empty tensors have no address to pass on
+        return
+    with _on(device, stream):
+        _check("bi_kv_append_q8", lib().bi_kv_append_q8(
+            _ptr(k_new), _ptr(v_new), ld, _ptr(q_seq), _ptr(q_pos), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+            _ptr(v_scale), kind, num_pages, _ptr(page_table), page_table.shape[0], page_table.shape[1], T, Hkv, D,
+            _stream()))
+
+
+def kv_read_q8(q_seq, q_pos, k_cache, v_cache, k_scale, v_scale, page_table, k_out=None, v_out=None, stream=None):
+    """The bf16 keys and values [T, Hkv, D] that the 8-bit store holds at (q_seq[t], q_pos[t])."""
+    num_pages, Hkv, D, kind = _store_q8(k_cache, v_cache, k_scale, v_scale, page_table)
+    _req(q_seq, torch.int32, "q_seq", 1)
+    T = q_seq.shape[0]
+    _row_ids(q_seq, q_pos, T)
+    ld = Hkv * D
+    if (k_out is None) != (v_out is None):
+        raise ValueError("give both k_out and v_out, or neither")
+    if k_out is not None:
+        for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+            _req(t, torch.bfloat16, n, 3)
+            if tuple(t.shape) != (T, Hkv, D):
+                raise ValueError(f"{n} must have shape {(T, Hkv, D)}, got {tuple(t.shape)}")
+        ld = _rows3(k_out, "k_out")
+        if _rows3(v_out, "v_out") != ld:
+            raise ValueError("k_out and v_out must have the same row stride")
+    device = _same_device(k_cache, v_cache, k_scale, v_scale, page_table, q_seq, q_pos, k_out, v_out)
+    with _on(device, stream):
+        if k_out is None:
+            k_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=device)
+            v_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=device)
+        if T == 0:
+            return k_out, v_out
+        _check("bi_kv_read_q8", lib().bi_kv_read_q8(
+            _ptr(k_out), _ptr(v_out), ld, _ptr(q_seq), _ptr(q_pos), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+            _ptr(v_scale), kind, num_pages, _ptr(page_table), page_table.shape[0], page_table.shape[1], T, Hkv, D,
+            _stream()))
+    return k_out, v_out
+
+
+def attention_decode_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, scale: float | None = None,
+                        out=None, workspace=None, stream=None):
+    """Decode attention over the 8-bit paged store; q [B, Hq, D] -> out [B, Hq, D] (Hq / Hkv up to 16).
+
+    workspace: at least attention_workspace_size(B, Hq, D, page_table.shape[1]) bytes."""
+    num_pages, Hkv, Dc, kind = _store_q8(k_cache, v_cache, k_scale, v_scale, page_table)
+    _req(q, torch.bfloat16, "q", 3)
+    _req(seq_lens, torch.int32, "seq_lens", 1)
+    _contig(q, "q")
+    _contig(seq_lens, "seq_lens")
+    B, Hq, D = q.shape
+    if D != Dc:
+        raise ValueError(f"q has heads of {D} dims, the store of {Dc}")
+    if page_table.shape[0] < B or seq_lens.shape[0] < B:
+        raise ValueError("page_table and seq_lens need a row per sequence")
+    maxp = page_table.shape[1]
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    device = _same_device(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, out, workspace)
+    if out is not None:
+        _out(out, torch.bfloat16, (B, Hq, D), "out")
+    _check_workspace(workspace)
+    with _on(device, stream):
+        out = torch.empty_like(q) if out is None else out
+        if B == 0:
+            return out
+        ws, nbytes = _workspace(attention_workspace_size(B, Hq, D, maxp), device, workspace)
+        _check("bi_attention_decode_q8", lib().bi_attention_decode_q8(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kind, num_pages, _ptr(page_table),
+            maxp, _ptr(seq_lens), _ptr(out), B, Hq, Hkv, D, scale, _ptr(ws), nbytes, _stream()))
+    return out
+
+
+def attention_prefill_q8_workspace_size(T: int) -> int:
+    return int(lib().bi_attention_prefill_q8_workspace_size(T))
+
+
+def attention_prefill_q8(q, q_seq, q_pos, k_cache, v_cache, k_scale, v_scale, page_table, scale: float | None = None,
+                         out=None, workspace=None, stream=None):
+    """Causal prefill over the 8-bit store; row t of q [T, Hq, D] (rows may be strided) sees keys
+    0..q_pos[t] of sequence q_seq[t], with the bits of the decode row there. Prompt chunks and
+    decode tokens may share a call; a chunk's rows are fastest next to one another.
+
+    workspace: at least attention_prefill_q8_workspace_size(T) bytes."""
+    num_pages, Hkv, Dc, kind = _store_q8(k_cache, v_cache, k_scale, v_scale, page_table)
+    _req(q, torch.bfloat16, "q", 3)
+    ldq = _rows3(q, "q")
+    T, Hq, D = q.shape
+    if D != Dc:
+        raise ValueError(f"q has heads of {D} dims, the store of {Dc}")
+    _row_ids(q_seq, q_pos, T)
+    num_seqs, maxp = page_table.shape
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    device = _same_device(q, q_seq, q_pos, k_cache, v_cache, k_scale, v_scale, page_table, out, workspace)
+    if out is not None:
+        _out(out, torch.bfloat16, (T, Hq, D), "out")
+    _check_workspace(workspace)
+    with _on(device, stream):
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=device) if out is None else out
+        if T == 0:
+            return out
+        ws, nbytes = _workspace(attention_prefill_q8_workspace_size(T), device, workspace)
+        _check("bi_attention_prefill_q8", lib().bi_attention_prefill_q8(
+            _ptr(q), ldq, _ptr(q_seq), _ptr(q_pos), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kind,
+            num_pages, _ptr(page_table), num_seqs, maxp, _ptr(out), T, Hq, Hkv, D, scale, _ptr(ws), nbytes,
+            _stream()))
+    return out
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, pos, cos_sin, eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """RMSNorm of every head of q [T, Hq, D] and k [T, Hkv, D] (rows may be strided), then the rotary
+    embedding at pos[t], in one pass and one rounding; in place unless q_out / k_out are given.
+    q_weight, k_weight bf16 [D]; cos_sin fp32 [max_pos, D/2, 2]. Returns (q, k) as written."""
+    _req(q, torch.bfloat16, "q", 3)
+    _req(k, torch.bfloat16, "k", 3)
+    _req(pos, torch.int32, "pos", 1)
+    _req(cos_sin, torch.float32, "cos_sin", 3)
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if k.shape[0] != T or k.shape[2] != D:
+        raise ValueError("q and k must be [T, Hq, D] and [T, Hkv, D]")
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        _out(t, torch.bfloat16, (D,), n)
+    _contig(pos, "pos")
+    _contig(cos_sin, "cos_sin")
+    if cos_sin.shape[1:] != (D // 2, 2):
+        raise ValueError("cos_sin must be [max_pos, D/2, 2]")
+    if pos.shape != (T,):
+        raise ValueError("pos needs one entry per row of q")
+    q_out = q if q_out is None else q_out
+    k_out = k if k_out is None else k_out
+    for t, like, n in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        _req(t, torch.bfloat16, n, 3)
+        if t.shape != like.shape:
+            raise ValueError(f"{n} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    device = _same_device(q, k, q_weight, k_weight, pos, cos_sin, q_out, k_out)
+    if T == 0:
+        return q_out, k_out
+    with _on(device, stream):
+        _check("bi_qk_norm_rope", lib().bi_qk_norm_rope(
+            _ptr(q), _rows3(q, "q"), _ptr(k), _rows3(k, "k"), _ptr(q_weight), _ptr(k_weight), _ptr(pos),
+            _ptr(cos_sin), cos_sin.shape[0], eps, _ptr(q_out), _rows3(q_out, "q_out"), _ptr(k_out),
+            _rows3(k_out, "k_out"), T, Hq, Hkv, D, _stream()))
+    return q_out, k_out
 
 
 def gather_rows(src, idx, out=None, stream=None):

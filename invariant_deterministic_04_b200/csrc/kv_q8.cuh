@@ -1,0 +1,180 @@
+// The 8-bit paged KV store: rows quantised as they are written, and read back.
+//
+// A store row (page slot of one kv-head, D values) holds 8-bit values v and one fp32 scale
+// s; it stands for v * s. From a bf16 row x with a = max |x|:
+//   int8: s = a / 127 (one fp32 rounding), v = the integer nearest to 127 x / a, ties to even.
+//     127 x has at most 15 significant bits, so it is exact in fp32 and v takes one rounded
+//     division and one rounding to an integer. Together they are exact: with x = mx 2^(j-d)
+//     and a = ma 2^j (mx, ma < 2^8, ma >= 2^7) a quotient q >= 2^n that is no half-integer is
+//     at least 2^-d / 255 > 2^(n-16) from the nearest one, and the division is off by 2^(n-24)
+//     at most; a half-integer is representable, so the division gives it and the tie goes to even.
+//   e4m3: s = 2^e, the least power of two with a <= 448 s; v = e4m3(x / s), nearest even. The
+//     division by a power of two is exact.
+//   a < 2^-100 (a row of zeros too): v = 0, s = 1. A row with a NaN or an infinity: v = 0,
+//     s = NaN, so that it reads back, and enters attention, as NaN.
+// Each element depends on its own row only.
+//
+// Bound: HBM. A row of D bf16 is read once (2 D bytes) and D + 4 bytes are written.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "attention.cuh"
+#include "device.cuh"
+
+namespace bi {
+namespace kvq8 {
+
+constexpr int PAGE = BI_PAGE_TOKENS;
+constexpr int kThreads = 256;
+constexpr uint32_t kEmptyBits = 0x0D80u;     // bf16 bits of 2^-100
+constexpr uint32_t kLoudBits = 0x5F80u;      // bf16 bits of 2^64
+constexpr uint32_t kNonFiniteBits = 0x7F80u; // bf16 bits of infinity
+
+struct Store {
+  uint8_t* k;
+  uint8_t* v;
+  float* ks;
+  float* vs;
+  int64_t num_pages;
+  const int32_t* pt;
+  int num_seqs, max_pages;
+};
+
+// Store row of (seq, pos) for kv-head g, or -1 (error recorded) if an id is out of range.
+__device__ __forceinline__ int64_t slot_row(const Store& S, int seq, int pos, int g, int Hkv, bool report) {
+  int pg = -1;
+  if (seq >= 0 && seq < S.num_seqs && pos >= 0 && pos < S.max_pages * PAGE)
+    pg = S.pt[(int64_t)seq * S.max_pages + pos / PAGE];
+  if (pg < 0 || pg >= S.num_pages) {
+    if (report) record_error(BI_ERR_DEVICE_INDEX);
+    return -1;
+  }
+  return ((int64_t)pg * Hkv + g) * PAGE + pos % PAGE;
+}
+
+// D/8 lanes hold a row, 8 values each: the largest bit pattern of |x| over the row (bf16
+// magnitudes order like integers, NaN above infinity above the finite ones).
+template <int LANES>
+__device__ __forceinline__ uint32_t row_max_bits(const uint4& x) {
+  uint32_t m = 0;
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+#pragma unroll
+  for (int off = LANES / 2; off >= 1; off >>= 1) m = max(m, __shfl_xor_sync(kFullMask, m, off));
+  return m;
+}
+
+template <int KIND>
+__device__ __forceinline__ uint2 quantise8(const uint4& x, uint32_t amax_bits, float& scale) {
+  float f[8];
+  unpack8(x, f);
+  const float a = __uint_as_float(amax_bits << 16);
+  if (amax_bits < kEmptyBits || amax_bits >= kNonFiniteBits) {
+    scale = amax_bits < kEmptyBits ? 1.f : __uint_as_float(0x7FC00000u);
+    return make_uint2(0, 0);
+  }
+  uint32_t b[8];
+  if constexpr (KIND == BI_KV_INT8) {
+    scale = __fdiv_rn(a, 127.f);
+    // rows from 2^64 on are divided at 2^-64 of their size, where 127 x cannot overflow (elements
+    // that this takes below the normal numbers are far below half a step)
+    const bool loud = amax_bits >= kLoudBits;
+    const float num = loud ? 127.f * 0x1p-64f : 127.f, den = loud ? __fmul_rn(a, 0x1p-64f) : a;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = (uint32_t)__float2int_rn(__fdiv_rn(__fmul_rn(num, f[i]), den)) & 0xFFu;
+    return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
+  } else {
+    // a = (1 + m / 128) 2^n: 448 = 1.75 * 2^8, so e = n - 8, one more where 1 + m / 128 > 1.75
+    const int e = (int)(amax_bits >> 7) - 127 - 8 + ((amax_bits & 0x7Fu) > 0x60u ? 1 : 0);
+    scale = __uint_as_float((uint32_t)(e + 127) << 23);
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+    uint16_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      h[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(f[2 * i], inv), __fmul_rn(f[2 * i + 1], inv)),
+                                      __NV_SATFINITE, __NV_E4M3);
+    return make_uint2((uint32_t)h[0] | (uint32_t)h[1] << 16, (uint32_t)h[2] | (uint32_t)h[3] << 16);
+  }
+}
+
+// D/8 lanes per (row, kv-head) and side; side 0 is K, side 1 is V.
+template <int KIND, int D>
+__global__ void __launch_bounds__(kThreads) kv_append_q8_kernel(const uint16_t* __restrict__ kn,
+                                                                const uint16_t* __restrict__ vn, int64_t ld_new,
+                                                                const int32_t* __restrict__ q_seq,
+                                                                const int32_t* __restrict__ q_pos, Store S, int T,
+                                                                int Hkv) {
+  constexpr int LANES = D / 8;
+  const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t item = e / LANES;
+  const int j = (int)(e % LANES);
+  pdl_wait();  // inputs written by the previous kernel on the stream are complete from here on
+  pdl_trigger();
+  const bool live = item < (int64_t)2 * T * Hkv;
+  const int64_t it = live ? item : 0;
+  const int side = (int)(it & 1);
+  const int64_t tg = it >> 1;
+  const int t = (int)(tg / Hkv), g = (int)(tg - (int64_t)t * Hkv);
+  const uint4 x = __ldg(reinterpret_cast<const uint4*>((side ? vn : kn) + (int64_t)t * ld_new + (int64_t)g * D) + j);
+  const uint32_t amax = row_max_bits<LANES>(x);
+  if (!live) return;
+  const int64_t row = slot_row(S, q_seq[t], q_pos[t], g, Hkv, j == 0);
+  if (row < 0) return;
+  float s;
+  const uint2 v = quantise8<KIND>(x, amax, s);
+  reinterpret_cast<uint2*>((side ? S.v : S.k) + row * D)[j] = v;
+  if (j == 0) (side ? S.vs : S.ks)[row] = s;
+}
+
+template <int KIND>
+__device__ __forceinline__ void widen4(uint32_t w, float (&f)[4]) {
+  if constexpr (KIND == BI_KV_INT8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = (float)(int8_t)(w >> (8 * i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3);
+      const float2 p = __half22float2(__half2(h));
+      f[2 * i] = p.x;
+      f[2 * i + 1] = p.y;
+    }
+  }
+}
+
+// The inverse: bf16(v * s) of the store rows at (q_seq[t], q_pos[t]); zeros where an id is bad.
+template <int KIND, int D>
+__global__ void __launch_bounds__(kThreads) kv_read_q8_kernel(uint16_t* __restrict__ ko, uint16_t* __restrict__ vo,
+                                                              int64_t ld_out, const int32_t* __restrict__ q_seq,
+                                                              const int32_t* __restrict__ q_pos, Store S, int T,
+                                                              int Hkv) {
+  constexpr int LANES = D / 8;
+  const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t it = e / LANES;
+  const int j = (int)(e % LANES);
+  pdl_wait();  // the store is complete from here on
+  pdl_trigger();
+  if (it >= (int64_t)2 * T * Hkv) return;
+  const int side = (int)(it & 1);
+  const int64_t tg = it >> 1;
+  const int t = (int)(tg / Hkv), g = (int)(tg - (int64_t)t * Hkv);
+  const int64_t row = slot_row(S, q_seq[t], q_pos[t], g, Hkv, j == 0);
+  uint4 o = make_uint4(0, 0, 0, 0);
+  if (row >= 0) {
+    const uint2 v = reinterpret_cast<const uint2*>((side ? S.v : S.k) + row * D)[j];
+    const float s = (side ? S.vs : S.ks)[row];
+    float f[4], h[4];
+    widen4<KIND>(v.x, f);
+    widen4<KIND>(v.y, h);
+    o = make_uint4(pack_bf16x2(__fmul_rn(f[0], s), __fmul_rn(f[1], s)),
+                   pack_bf16x2(__fmul_rn(f[2], s), __fmul_rn(f[3], s)),
+                   pack_bf16x2(__fmul_rn(h[0], s), __fmul_rn(h[1], s)),
+                   pack_bf16x2(__fmul_rn(h[2], s), __fmul_rn(h[3], s)));
+  }
+  reinterpret_cast<uint4*>((side ? vo : ko) + (int64_t)t * ld_out + (int64_t)g * D)[j] = o;
+}
+
+}  // namespace kvq8
+}  // namespace bi

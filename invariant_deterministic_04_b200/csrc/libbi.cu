@@ -14,6 +14,9 @@
 #include "lmhead.cuh"
 #include "glue.cuh"
 #include "attention_tc.cuh"
+#include "attention_q8.cuh"
+#include "kv_q8.cuh"
+#include "qknorm.cuh"
 #include "reduce.cuh"
 
 namespace {
@@ -181,6 +184,60 @@ bi_status attention_common(const uint16_t* q, int64_t ldq, const uint16_t* kc, c
                      (const float2*)lay.pml, (const int32_t*)lay.off, nrows, Hq, out);
   }
   return e == cudaSuccess ? BI_OK : BI_ERR_CUDA;
+}
+
+// ---- 8-bit store
+
+// Host checks shared by the calls on the 8-bit store.
+bi_status store_check(const void* kc, const void* vc, const float* ks, const float* vs, int kind, int64_t num_pages,
+                      int max_pages, int Hkv, int D) {
+  if (num_pages <= 0 || max_pages <= 0 || Hkv <= 0 || D <= 0) return BI_ERR_SHAPE;
+  if (num_pages > (int64_t(1) << 31) || max_pages > INT_MAX / BI_PAGE_TOKENS) return BI_ERR_SHAPE;
+  if ((kind != BI_KV_INT8 && kind != BI_KV_E4M3) || (D != 64 && D != 128)) return BI_ERR_UNSUPPORTED;
+  if (!aligned16(kc) || !aligned16(vc) || !aligned16(ks) || !aligned16(vs)) return BI_ERR_ALIGN;
+  return BI_OK;
+}
+
+bi_status attention_q8_check(const uint16_t* q, int64_t ldq, int nrows, const uint16_t* out, int Hq, int Hkv, int D,
+                             int max_pages, float scale) {
+  if (Hq <= 0 || Hq % Hkv != 0) return BI_ERR_SHAPE;
+  if (Hq / Hkv > 16) return BI_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || ldq < (int64_t)Hq * D) return BI_ERR_SHAPE;
+  if (ldq % 8 || !aligned16(q) || !aligned16(out)) return BI_ERR_ALIGN;
+  // index arithmetic of the work lists is 32-bit
+  if ((int64_t)nrows * max_splits(max_pages) * Hkv >= INT_MAX / 2 || (int64_t)nrows * Hq >= INT_MAX / 16)
+    return BI_ERR_SHAPE;
+  if (ranges_overlap(q, span_bytes(nrows, (int64_t)Hq * D, ldq, 2), out, span_bytes(nrows, (int64_t)Hq * D, (int64_t)Hq * D, 2)))
+    return BI_ERR_SHAPE;
+  return BI_OK;
+}
+
+template <int KIND, int D>
+cudaError_t q8_decode(const uint16_t* q, int Hq, int Hkv, const bi::attnq8::Cache& C, bi::attn::Rows R, int nrows,
+                      const AttnWs& ws, uint16_t* out, float c, int sms, cudaStream_t st) {
+  namespace a8 = bi::attnq8;
+  cudaError_t e = bi::launch_pdl(bi::attn::split_offsets_kernel, dim3(1), dim3(1024), 0, st, R, nrows, ws.off);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)(sms * 4)), block(a8::kWarps * 32);
+  e = Hq / Hkv <= 8 ? bi::launch_pdl(a8::split_kernel<KIND, D, 1>, grid, block, 0, st, q, Hq, Hkv, C, R, nrows,
+                                     (const int32_t*)ws.off, ws.po, ws.pml, c)
+                    : bi::launch_pdl(a8::split_kernel<KIND, D, 2>, grid, block, 0, st, q, Hq, Hkv, C, R, nrows,
+                                     (const int32_t*)ws.off, ws.po, ws.pml, c);
+  if (e != cudaSuccess) return e;
+  return bi::launch_pdl(a8::combine_kernel<D>, dim3((unsigned)((nrows * Hq + 7) / 8)), dim3(256), 0, st,
+                        (const float*)ws.po, (const float2*)ws.pml, (const int32_t*)ws.off, nrows, Hq, out);
+}
+
+template <int KIND, int D>
+cudaError_t q8_prefill(const uint16_t* q, int64_t ldq, int Hq, int Hkv, const bi::attnq8::Cache& C, bi::attn::Rows R,
+                       int T, bi::attnq8::Tile* tiles, int32_t* count, uint16_t* out, float c, int sms,
+                       cudaStream_t st) {
+  namespace a8 = bi::attnq8;
+  cudaError_t e = bi::launch_pdl(a8::plan_kernel, dim3(1), dim3(1024), 0, st, R, T, 16 / (Hq / Hkv), tiles, count);
+  if (e != cudaSuccess) return e;
+  return bi::launch_pdl(a8::tile_kernel<KIND, D>, dim3((unsigned)(sms * 3)), dim3(a8::kTileWarps * 32),
+                        (size_t)a8::tile_smem_bytes<D>(), st, q, ldq, Hq, Hkv, C, R, (const a8::Tile*)tiles,
+                        (const int32_t*)count, out, c);
 }
 
 // ---- LM head workspace: bf16 logits [M, V], fp32 logits [M, V], flagged list [M + 1],
@@ -455,6 +512,143 @@ bi_status bi_kv_append(const bi_bf16* k_new, const bi_bf16* v_new, int64_t ld_ne
   return bi::launch_pdl(bi::attn::kv_append_kernel, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, as_stream(stream),
                         k_new, v_new, ld_new, q_seq, q_pos, k_cache, v_cache, num_pages, page_table, num_seqs,
                         max_pages_per_seq, T, Hkv, D) == cudaSuccess
+             ? BI_OK
+             : BI_ERR_CUDA;
+}
+
+bi_status bi_kv_append_q8(const bi_bf16* k_new, const bi_bf16* v_new, int64_t ld_new, const int32_t* q_seq,
+                          const int32_t* q_pos, void* k_cache, void* v_cache, float* k_scale, float* v_scale, int kind,
+                          int64_t num_pages, const int32_t* page_table, int num_seqs, int max_pages_per_seq, int T,
+                          int Hkv, int D, void* stream) {
+  if (!k_new || !v_new || !q_seq || !q_pos || !k_cache || !v_cache || !k_scale || !v_scale || !page_table)
+    return BI_ERR_NULL;
+  if (T < 0 || num_seqs <= 0) return BI_ERR_SHAPE;
+  if (bi_status e = store_check(k_cache, v_cache, k_scale, v_scale, kind, num_pages, max_pages_per_seq, Hkv, D)) return e;
+  if (ld_new < (int64_t)Hkv * D) return BI_ERR_SHAPE;
+  if (!aligned16(k_new) || !aligned16(v_new) || ld_new % 8) return BI_ERR_ALIGN;
+  const int64_t grid = ((int64_t)2 * T * Hkv * (D / 8) + bi::kvq8::kThreads - 1) / bi::kvq8::kThreads;
+  if (grid > INT_MAX) return BI_ERR_SHAPE;
+  if (T == 0) return BI_OK;
+  const bi::kvq8::Store S{(uint8_t*)k_cache, (uint8_t*)v_cache, k_scale, v_scale, num_pages, page_table, num_seqs,
+                          max_pages_per_seq};
+  auto kernel = kind == BI_KV_INT8 ? (D == 128 ? bi::kvq8::kv_append_q8_kernel<BI_KV_INT8, 128>
+                                               : bi::kvq8::kv_append_q8_kernel<BI_KV_INT8, 64>)
+                                   : (D == 128 ? bi::kvq8::kv_append_q8_kernel<BI_KV_E4M3, 128>
+                                               : bi::kvq8::kv_append_q8_kernel<BI_KV_E4M3, 64>);
+  return bi::launch_pdl(kernel, dim3((unsigned)grid), dim3(bi::kvq8::kThreads), 0, as_stream(stream), k_new, v_new,
+                        ld_new, q_seq, q_pos, S, T, Hkv) == cudaSuccess
+             ? BI_OK
+             : BI_ERR_CUDA;
+}
+
+bi_status bi_kv_read_q8(bi_bf16* k_out, bi_bf16* v_out, int64_t ld_out, const int32_t* q_seq, const int32_t* q_pos,
+                        const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale, int kind,
+                        int64_t num_pages, const int32_t* page_table, int num_seqs, int max_pages_per_seq, int T,
+                        int Hkv, int D, void* stream) {
+  if (!k_out || !v_out || !q_seq || !q_pos || !k_cache || !v_cache || !k_scale || !v_scale || !page_table)
+    return BI_ERR_NULL;
+  if (T < 0 || num_seqs <= 0) return BI_ERR_SHAPE;
+  if (bi_status e = store_check(k_cache, v_cache, k_scale, v_scale, kind, num_pages, max_pages_per_seq, Hkv, D)) return e;
+  if (ld_out < (int64_t)Hkv * D) return BI_ERR_SHAPE;
+  if (!aligned16(k_out) || !aligned16(v_out) || ld_out % 8) return BI_ERR_ALIGN;
+  const int64_t grid = ((int64_t)2 * T * Hkv * (D / 8) + bi::kvq8::kThreads - 1) / bi::kvq8::kThreads;
+  if (grid > INT_MAX) return BI_ERR_SHAPE;
+  if (T == 0) return BI_OK;
+  const int64_t width = (int64_t)Hkv * D, rows = num_pages * Hkv * BI_PAGE_TOKENS;
+  if (blocks_overlap(k_out, ld_out, width, v_out, ld_out, width, T)) return BI_ERR_SHAPE;
+  const size_t ob = span_bytes(T, width, ld_out, 2);
+  for (const void* o : {(const void*)k_out, (const void*)v_out})
+    if (ranges_overlap(o, ob, k_cache, rows * D) || ranges_overlap(o, ob, v_cache, rows * D) ||
+        ranges_overlap(o, ob, k_scale, rows * 4) || ranges_overlap(o, ob, v_scale, rows * 4))
+      return BI_ERR_SHAPE;
+  const bi::kvq8::Store S{(uint8_t*)k_cache, (uint8_t*)v_cache, (float*)k_scale, (float*)v_scale, num_pages, page_table,
+                          num_seqs, max_pages_per_seq};
+  auto kernel = kind == BI_KV_INT8 ? (D == 128 ? bi::kvq8::kv_read_q8_kernel<BI_KV_INT8, 128>
+                                               : bi::kvq8::kv_read_q8_kernel<BI_KV_INT8, 64>)
+                                   : (D == 128 ? bi::kvq8::kv_read_q8_kernel<BI_KV_E4M3, 128>
+                                               : bi::kvq8::kv_read_q8_kernel<BI_KV_E4M3, 64>);
+  return bi::launch_pdl(kernel, dim3((unsigned)grid), dim3(bi::kvq8::kThreads), 0, as_stream(stream), k_out, v_out,
+                        ld_out, q_seq, q_pos, S, T, Hkv) == cudaSuccess
+             ? BI_OK
+             : BI_ERR_CUDA;
+}
+
+bi_status bi_attention_decode_q8(const bi_bf16* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                 const float* v_scale, int kind, int64_t num_pages, const int32_t* page_table,
+                                 int max_pages_per_seq, const int32_t* seq_lens, bi_bf16* out, int B, int Hq, int Hkv,
+                                 int D, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !page_table || !seq_lens || !out) return BI_ERR_NULL;
+  if (B < 0) return BI_ERR_SHAPE;
+  if (bi_status e = store_check(k_cache, v_cache, k_scale, v_scale, kind, num_pages, max_pages_per_seq, Hkv, D)) return e;
+  if (bi_status e = attention_q8_check(q, (int64_t)Hq * D, B, out, Hq, Hkv, D, max_pages_per_seq, scale)) return e;
+  if (B == 0) return BI_OK;
+  if (!workspace) return BI_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return BI_ERR_ALIGN;
+  AttnWs lay{};
+  if (workspace_bytes < attn_ws_size(B, Hq, D, max_pages_per_seq, &lay, workspace)) return BI_ERR_WORKSPACE;
+  const int sms = device_sms();
+  if (sms <= 0) return BI_ERR_CUDA;
+  const bi::attnq8::Cache C{(const uint8_t*)k_cache, (const uint8_t*)v_cache, k_scale, v_scale, num_pages, page_table};
+  const bi::attn::Rows R{seq_lens, nullptr, nullptr, B, max_pages_per_seq};
+  const float c = (float)((double)scale * 1.4426950408889634);  // scale * log2(e)
+  auto call = kind == BI_KV_INT8 ? (D == 128 ? q8_decode<BI_KV_INT8, 128> : q8_decode<BI_KV_INT8, 64>)
+                                 : (D == 128 ? q8_decode<BI_KV_E4M3, 128> : q8_decode<BI_KV_E4M3, 64>);
+  return call(q, Hq, Hkv, C, R, B, lay, out, c, sms, as_stream(stream)) == cudaSuccess ? BI_OK : BI_ERR_CUDA;
+}
+
+size_t bi_attention_prefill_q8_workspace_size(int64_t T) {
+  return T < 0 ? 0 : 256 + align256((size_t)T * sizeof(bi::attnq8::Tile));
+}
+
+bi_status bi_attention_prefill_q8(const bi_bf16* q, int64_t ldq, const int32_t* q_seq, const int32_t* q_pos,
+                                  const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                                  int kind, int64_t num_pages, const int32_t* page_table, int num_seqs,
+                                  int max_pages_per_seq, bi_bf16* out, int T, int Hq, int Hkv, int D, float scale,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !q_seq || !q_pos || !k_cache || !v_cache || !k_scale || !v_scale || !page_table || !out) return BI_ERR_NULL;
+  if (T < 0 || num_seqs <= 0) return BI_ERR_SHAPE;
+  if (bi_status e = store_check(k_cache, v_cache, k_scale, v_scale, kind, num_pages, max_pages_per_seq, Hkv, D)) return e;
+  if (bi_status e = attention_q8_check(q, ldq, T, out, Hq, Hkv, D, max_pages_per_seq, scale)) return e;
+  if (T == 0) return BI_OK;
+  if (!workspace || workspace_bytes < bi_attention_prefill_q8_workspace_size(T)) return BI_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return BI_ERR_ALIGN;
+  const int sms = device_sms();
+  if (sms <= 0) return BI_ERR_CUDA;
+  const bi::attnq8::Cache C{(const uint8_t*)k_cache, (const uint8_t*)v_cache, k_scale, v_scale, num_pages, page_table};
+  const bi::attn::Rows R{nullptr, q_seq, q_pos, num_seqs, max_pages_per_seq};
+  const float c = (float)((double)scale * 1.4426950408889634);  // scale * log2(e)
+  int32_t* count = static_cast<int32_t*>(workspace);
+  auto* tiles = reinterpret_cast<bi::attnq8::Tile*>(static_cast<uint8_t*>(workspace) + 256);
+  auto call = kind == BI_KV_INT8 ? (D == 128 ? q8_prefill<BI_KV_INT8, 128> : q8_prefill<BI_KV_INT8, 64>)
+                                 : (D == 128 ? q8_prefill<BI_KV_E4M3, 128> : q8_prefill<BI_KV_E4M3, 64>);
+  return call(q, ldq, Hq, Hkv, C, R, T, tiles, count, out, c, sms, as_stream(stream)) == cudaSuccess ? BI_OK
+                                                                                                   : BI_ERR_CUDA;
+}
+
+bi_status bi_qk_norm_rope(const bi_bf16* q, int64_t ldq, const bi_bf16* k, int64_t ldk, const bi_bf16* q_weight,
+                          const bi_bf16* k_weight, const int32_t* pos, const float* cos_sin, int max_pos, float eps,
+                          bi_bf16* q_out, int64_t ldq_out, bi_bf16* k_out, int64_t ldk_out, int64_t T, int Hq, int Hkv,
+                          int D, void* stream) {
+  if (!q || !k || !q_weight || !k_weight || !pos || !cos_sin || !q_out || !k_out) return BI_ERR_NULL;
+  if (T < 0 || T > INT_MAX || Hq <= 0 || Hkv <= 0 || Hq > (1 << 20) || Hkv > (1 << 20) || D <= 0 || max_pos <= 0 ||
+      !std::isfinite(eps) || eps < 0)
+    return BI_ERR_SHAPE;
+  if (D != 64 && D != 128 && D != 256) return BI_ERR_UNSUPPORTED;
+  const int64_t nq = (int64_t)Hq * D, nk = (int64_t)Hkv * D;
+  if (ldq < nq || ldk < nk || ldq_out < nq || ldk_out < nk) return BI_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(cos_sin) ||
+      !aligned16(q_out) || !aligned16(k_out) || ldq % 8 || ldk % 8 || ldq_out % 8 || ldk_out % 8)
+    return BI_ERR_ALIGN;
+  if ((T * (Hq + Hkv) * (D / 16) + bi::qknorm::kThreads - 1) / bi::qknorm::kThreads > INT_MAX) return BI_ERR_SHAPE;
+  if (T == 0) return BI_OK;
+  // in place only row for row; otherwise no output may share an element with an input or the other output
+  if (q_out == q ? ldq_out != ldq : blocks_overlap(q, ldq, nq, q_out, ldq_out, nq, T)) return BI_ERR_SHAPE;
+  if (k_out == k ? ldk_out != ldk : blocks_overlap(k, ldk, nk, k_out, ldk_out, nk, T)) return BI_ERR_SHAPE;
+  if (blocks_overlap(q, ldq, nq, k_out, ldk_out, nk, T) || blocks_overlap(k, ldk, nk, q_out, ldq_out, nq, T) ||
+      blocks_overlap(q_out, ldq_out, nq, k_out, ldk_out, nk, T))
+    return BI_ERR_SHAPE;
+  return bi::qknorm::launch({q, ldq, q_weight, q_out, ldq_out}, {k, ldk, k_weight, k_out, ldk_out}, T, Hq, Hkv, D, pos,
+                            reinterpret_cast<const float2*>(cos_sin), max_pos, eps, as_stream(stream)) == cudaSuccess
              ? BI_OK
              : BI_ERR_CUDA;
 }
