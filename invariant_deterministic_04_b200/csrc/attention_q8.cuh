@@ -351,63 +351,218 @@ __device__ __forceinline__ void join(float& M, float m, float& a, float& b) {
 
 // ---------------------------------------------------------------------------
 // Decode: one warp per (row, kv-head, split); the split's partial result goes to the workspace.
+//
+// Bound: HBM (4 (2 D + 8) L Hkv flops-free bytes per row against 4 L Hq D flops). Each lane
+// copies the bytes that it will itself widen into its own places of a ring in shared memory
+// (cp.async, 16 bytes each), kStages pages ahead across item boundaries, so that nothing but
+// the 32 scales of a page crosses lanes and no barrier beyond the warp's is needed; a warp's
+// reads back are contiguous, without bank conflicts.
 
 constexpr int kWarps = 4;
+constexpr int kStages = 4;
+constexpr int kCoarse = 1024;  // entries of the split-count prefix that a CTA keeps
+
+template <int D>
+struct Ring {
+  static constexpr int K_BYTES = PAGE * D;         // [n-tile][64-dim part][lane] 16 bytes
+  static constexpr int V_BYTES = PAGE * D;         // [token of the lane's four][lane] D/8 bytes
+  static constexpr int STAGE = K_BYTES + V_BYTES + 2 * PAGE * 4;  // and the page's scales
+  static constexpr int WARP = kStages * STAGE;
+  static constexpr int SMEM = kWarps * WARP + (kCoarse + 1) * 4;
+};
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Starts the copies of one page (store rows row0 .. row0 + 15) into a ring stage.
+template <int D>
+__device__ __forceinline__ void copy_page(uint32_t stage, const Cache& C, int64_t row0, int lane) {
+  using T = Ring<D>;
+  const int g = lane >> 2, c = lane & 3;
+  const uint8_t* kp = C.k + (row0 + g) * D + 16 * c;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int v = 0; v < D / 64; ++v)
+      cp_async<16>(stage + ((i * (D / 64) + v) * 32 + lane) * 16, kp + i * 8 * D + 64 * v);
+  const uint8_t* vp = C.v + (row0 + 2 * c) * D + (D / 8) * g;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    cp_async<D / 8>(stage + T::K_BYTES + (i * 32 + lane) * (D / 8), vp + ((i & 1) + (i >> 1) * 8) * D);
+  if (lane < 8)
+    cp_async<16>(stage + T::K_BYTES + T::V_BYTES + 16 * lane, (lane < 4 ? C.ks + row0 : C.vs + row0 - 16) + 4 * lane);
+}
+
+// The lane's part of a page from its ring stage.
+template <int D>
+__device__ __forceinline__ void read_page(Page<D>& P, uint32_t stage, int lane) {
+  using T = Ring<D>;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int v = 0; v < D / 64; ++v) P.k[i][v] = ld_shared_v4(stage + ((i * (D / 64) + v) * 32 + lane) * 16);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = stage + T::K_BYTES + (i * 32 + lane) * (D / 8);
+    if constexpr (D == 128) {
+      const uint4 x = ld_shared_v4(a);
+      P.v[i][0] = x.x; P.v[i][1] = x.y; P.v[i][2] = x.z; P.v[i][3] = x.w;
+    } else {
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(P.v[i][0]), "=r"(P.v[i][1]) : "r"(a));
+    }
+  }
+  const uint32_t sc = stage + T::K_BYTES + T::V_BYTES + 8 * (lane & 3);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(P.ks[2 * i]), "=f"(P.ks[2 * i + 1]) : "r"(sc + 32 * i));
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(P.vs[2 * i]), "=f"(P.vs[2 * i + 1]) : "r"(sc + 64 + 32 * i));
+  }
+}
+
+// A work item: split s of row r for one kv-head; `page` is page `lane` of it (-1: unusable).
+struct Item {
+  int r, s, kh, seen, page;
+};
 
 template <int KIND, int D, int RH>
-__global__ void __launch_bounds__(kWarps * 32) split_kernel(const uint16_t* __restrict__ q, int Hq, int Hkv, Cache C, Rows R,
-                                                            int nrows, const int32_t* __restrict__ off,
-                                                            float* __restrict__ po, float2* __restrict__ pml,
-                                                            float scale_log2) {
+__global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4)
+    split_kernel(const uint16_t* __restrict__ q, int Hq, int Hkv, Cache C, Rows R, int nrows, int max_splits,
+                 float* __restrict__ po, float2* __restrict__ pml, float scale_log2) {
+  using T = Ring<D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int32_t warp_sum[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int G = Hq / Hkv;
-  pdl_wait();  // the offsets (and the caller's q and store) are complete from here on
+  int32_t* pre = reinterpret_cast<int32_t*>(smem + kWarps * T::WARP);  // pre[i]: splits of rows below i * per
+  pdl_wait();  // the caller's inputs are complete from here on
   pdl_trigger();
-  const int total = off[nrows] * Hkv;
-  for (int item = warp * gridDim.x + blockIdx.x; item < total; item += gridDim.x * kWarps) {
-    const int f = item / Hkv, kh = item - f * Hkv;
-    int lo = 0, hi = nrows;  // off[lo] <= f < off[hi]
+
+  // the prefix of split counts, `per` rows an entry (1 up to kCoarse rows)
+  const int per = (nrows + kCoarse - 1) / kCoarse, entries = (nrows + per - 1) / per;
+  int base = 0;
+  for (int e0 = 0; e0 < entries; e0 += kWarps * 32) {
+    const int e = e0 + (int)threadIdx.x;
+    int n = 0;
+    if (e < entries)
+      for (int r = e * per; r < min(nrows, (e + 1) * per); ++r) n += attn::num_splits(R, r);
+    int x = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(kFullMask, x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int before = base;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += warp_sum[w];
+      base += warp_sum[w];
+    }
+    if (e < entries) pre[e] = before + x - n;
+    __syncthreads();
+  }
+  const int total = base * Hkv;
+  const int step = (int)gridDim.x * kWarps;
+
+  auto fetch = [&](int item) {
+    Item I;
+    const int f = item / Hkv;
+    I.kh = item - f * Hkv;
+    int lo = 0, hi = entries;  // pre[lo] <= f < pre[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (off[mid] <= f) lo = mid;
+      if (pre[mid] <= f) lo = mid;
       else hi = mid;
     }
-    const int r = lo, s = f - off[lo];
+    I.s = f - pre[lo];
+    I.r = lo * per;
+    while (per > 1) {
+      const int n = attn::num_splits(R, I.r);
+      if (I.s < n) break;
+      I.s -= n;
+      ++I.r;
+    }
     int pt_row;
-    const int len = attn::row_len(R, r, pt_row);
-    const int t0 = s * SPLIT, t1 = min(t0 + SPLIT, len);
-    const int np = (t1 - t0 + PAGE - 1) / PAGE;
-    const int32_t* prow = C.pt + (int64_t)pt_row * R.max_pages + s * PAGES_PER_SPLIT;
-    const int my_page = lane < np ? prow[lane] : 0;
+    const int len = attn::row_len(R, I.r, pt_row);
+    I.seen = min(SPLIT, len - I.s * SPLIT);
+    I.page = -1;
+    if (lane * PAGE < I.seen) {
+      const int pg = C.pt[(int64_t)pt_row * R.max_pages + I.s * PAGES_PER_SPLIT + lane];
+      if (pg >= 0 && pg < C.num_pages) I.page = pg;
+      else record_error(BI_ERR_DEVICE_INDEX);
+    }
+    return I;
+  };
 
+  const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * T::WARP);
+  int item = warp * (int)gridDim.x + (int)blockIdx.x;
+  if (item >= total) return;
+  Item cur = fetch(item), nxt = cur;
+  bool ahead = false;            // the copies have gone on to nxt
+  int pj = 0, issued = 0, used = 0;
+  // starts the copy of the next page of the item stream, if it is known by now
+  auto issue = [&] {
+    if (!ahead && pj * PAGE >= cur.seen && item + step < total) {
+      nxt = fetch(item + step);
+      ahead = true;
+      pj = 0;
+    }
+    const Item& I = ahead ? nxt : cur;
+    if (pj * PAGE < I.seen) {
+      const int pg = __shfl_sync(kFullMask, I.page, pj);
+      if (pg >= 0) copy_page<D>(ring + (uint32_t)(issued % kStages) * T::STAGE, C, ((int64_t)pg * Hkv + I.kh) * PAGE, lane);
+      ++pj;
+      ++issued;
+    }
+    cp_commit();
+  };
+  for (int i = 0; i < kStages; ++i) issue();
+
+  while (true) {
     Query<D, RH> Q;
 #pragma unroll
     for (int h = 0; h < RH; ++h) {
       const int head = g + 8 * h;
-      load_query<D, RH>(Q, h, head < G ? q + ((int64_t)r * Hq + kh * G + head) * D : nullptr, c, scale_log2);
+      load_query<D, RH>(Q, h, head < G ? q + ((int64_t)cur.r * Hq + cur.kh * G + head) * D : nullptr, c, scale_log2);
     }
     State<D, RH> S;
     S.clear();
-    for (int j = 0; j < np; ++j) {
-      const int pg = __shfl_sync(kFullMask, my_page, j);
-      if (pg < 0 || pg >= C.num_pages) {  // an unusable page: its tokens are not seen
-        if (lane == 0) record_error(BI_ERR_DEVICE_INDEX);
-        continue;
-      }
-      Page<D> P;
-      load_page<D>(P, C, ((int64_t)pg * Hkv + kh) * PAGE, g, c);
-      int nv[RH];
+    for (int j = 0; j * PAGE < cur.seen; ++j) {
+      // with the ring full the oldest copy group is the page wanted; otherwise (the stream's end,
+      // or an item of few pages) wait for all of them
+      if (issued - used == kStages) cp_wait<kStages - 1>();
+      else cp_wait<0>();
+      __syncwarp();
+      if (__shfl_sync(kFullMask, cur.page, j) >= 0) {  // the tokens of an unusable page are not seen
+        Page<D> P;
+        read_page<D>(P, ring + (uint32_t)(used % kStages) * T::STAGE, lane);
+        int nv[RH];
 #pragma unroll
-      for (int h = 0; h < RH; ++h) nv[h] = t1 - t0 - j * PAGE;
-      fold_page<KIND, D, RH>(Q, P, nv, nv[0], c, S);
+        for (int h = 0; h < RH; ++h) nv[h] = cur.seen - j * PAGE;
+        fold_page<KIND, D, RH>(Q, P, nv, nv[0], c, S);
+      }
+      ++used;
+      __syncwarp();  // every lane has read this page's scales: its stage may be refilled
+      issue();
     }
 #pragma unroll
     for (int h = 0; h < RH; ++h) {
       const float l = row_sum(S.l[h]);
       const int head = g + 8 * h;
       if (head >= G) continue;
-      const int64_t slot = (int64_t)f * Hq + kh * G + head;
+      const int64_t slot = ((int64_t)cur.r * max_splits + cur.s) * Hq + cur.kh * G + head;
       float* dst = po + slot * D + (D / 4) * c;
 #pragma unroll
       for (int i = 0; i < D / 8; i += 4) {
@@ -418,40 +573,96 @@ __global__ void __launch_bounds__(kWarps * 32) split_kernel(const uint16_t* __re
       }
       if (c == 0) pml[slot] = make_float2(S.m[h], l);
     }
+    if (item + step >= total) break;
+    item += step;
+    if (!ahead) {  // nothing of the next item has been asked for yet
+      cur = fetch(item);
+      pj = 0;
+    } else {
+      cur = nxt;
+      ahead = false;
+    }
+    for (int i = issued - used; i < kStages; ++i) issue();  // short items left the ring less than full
   }
 }
 
-// Folds a row's splits in ascending order; one warp per (row, query head).
-template <int D>
+// Folds a row's splits in ascending order; one warp per (row, query head, 32 * DPL output dims).
+// The lanes take the splits' maxima 32 at a time: the running maximum before and after each
+// split (a maximum is exact in any order) gives the weights of both sides of its fold step, and
+// the fold itself is one chain per output dim in split order whatever DPL is. Partials are
+// loaded U at a time.
+template <int D, int DPL>
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ po, const float2* __restrict__ pml,
-                                                      const int32_t* __restrict__ off, int nrows, int Hq,
+                                                      Rows R, int nrows, int max_splits, int Hq,
                                                       uint16_t* __restrict__ out) {
-  constexpr int DPL = D / 32;
-  const int w = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  constexpr int NG = D / (32 * DPL);  // warps per (row, head)
+  constexpr int U = DPL == 1 ? 16 : 8;
+  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
   pdl_wait();  // the split partials are complete from here on
   pdl_trigger();
-  if (w >= nrows * Hq) return;
-  const int r = w / Hq, h = w - r * Hq;
-  const int f0 = off[r], n = off[r + 1] - f0;
+  if (w >= (int64_t)nrows * Hq * NG) return;
+  const int64_t rh = w / NG;
+  const int r = (int)(rh / Hq), h = (int)(rh - (int64_t)r * Hq);
+  const int d0 = ((int)(w - rh * NG) * 32 + lane) * DPL;
+  const int n = attn::num_splits(R, r);
+  const int64_t slot0 = (int64_t)r * max_splits * Hq + h;
+  const float* src = po + slot0 * D + d0;
   float M = -INFINITY, L = 0.f, O[DPL];
 #pragma unroll
   for (int d = 0; d < DPL; ++d) O[d] = 0.f;
-  for (int s = 0; s < n; ++s) {
-    const int64_t slot = (int64_t)(f0 + s) * Hq + h;
-    const float2 ml = pml[slot];
-    float a, b;
-    join(M, ml.x, a, b);
-    L = __fmaf_rn(ml.y, b, __fmul_rn(L, a));
-    const float* src = po + slot * D + lane * DPL;
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    const float2 ml = s0 + lane < n ? pml[slot0 + (int64_t)(s0 + lane) * Hq] : make_float2(-INFINITY, 0.f);
+    float top = ml.x;  // the running maximum up to and with this lane's split
 #pragma unroll
-    for (int d = 0; d < DPL; ++d) O[d] = __fmaf_rn(src[d], b, __fmul_rn(O[d], a));
+    for (int d = 1; d < 32; d <<= 1) {
+      const float y = __shfl_up_sync(kFullMask, top, d);
+      if (lane >= d) top = fmaxf(top, y);
+    }
+    top = fmaxf(top, M);
+    float prev = __shfl_up_sync(kFullMask, top, 1);
+    if (lane == 0) prev = M;
+    float a, b;
+    join(prev, ml.x, a, b);
+    M = __shfl_sync(kFullMask, top, 31);
+    const int cnt = min(32, n - s0);
+    for (int u0 = 0; u0 < cnt; u0 += U) {
+      float v[U][DPL];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float* p = src + (int64_t)(s0 + min(u0 + u, cnt - 1)) * Hq * D;
+        if constexpr (DPL == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(p);
+          v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+        } else if constexpr (DPL == 2) {
+          const float2 x = *reinterpret_cast<const float2*>(p);
+          v[u][0] = x.x; v[u][1] = x.y;
+        } else {
+          v[u][0] = *p;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float ak = __shfl_sync(kFullMask, a, (u0 + u) & 31), bk = __shfl_sync(kFullMask, b, (u0 + u) & 31);
+        const float lk = __shfl_sync(kFullMask, ml.y, (u0 + u) & 31);
+        if (u0 + u < cnt) {
+          L = __fmaf_rn(lk, bk, __fmul_rn(L, ak));
+#pragma unroll
+          for (int d = 0; d < DPL; ++d) O[d] = __fmaf_rn(v[u][d], bk, __fmul_rn(O[d], ak));
+        }
+      }
+    }
   }
   float y[DPL];
 #pragma unroll
   for (int d = 0; d < DPL; ++d) y[d] = L == 0.f ? 0.f : __fdiv_rn(O[d], L);
-  uint32_t* dst = reinterpret_cast<uint32_t*>(out + (int64_t)w * D + lane * DPL);
+  uint16_t* dst = out + rh * D + d0;
+  if constexpr (DPL == 1) {
+    *dst = to_bf16_bits(y[0]);
+  } else {
 #pragma unroll
-  for (int d = 0; d < DPL; d += 2) dst[d / 2] = pack_bf16x2(y[d], y[d + 1]);
+    for (int d = 0; d < DPL; d += 2) reinterpret_cast<uint32_t*>(dst)[d / 2] = pack_bf16x2(y[d], y[d + 1]);
+  }
 }
 
 // ---------------------------------------------------------------------------

@@ -212,32 +212,74 @@ bi_status attention_q8_check(const uint16_t* q, int64_t ldq, int nrows, const ui
   return BI_OK;
 }
 
-template <int KIND, int D>
-cudaError_t q8_decode(const uint16_t* q, int Hq, int Hkv, const bi::attnq8::Cache& C, bi::attn::Rows R, int nrows,
-                      const AttnWs& ws, uint16_t* out, float c, int sms, cudaStream_t st) {
+// Shared-memory limit and resident CTAs per SM of a persistent kernel, found once per device.
+template <typename Tag, typename Kernel>
+cudaError_t resident_ctas(Kernel kernel, int threads, int smem, int dev, int* per_sm) {
+  static std::once_flag once[64];
+  static cudaError_t result[64];
+  static int found[64];
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::call_once(once[dev], [&] {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&found[dev], kernel, threads, smem);
+    if (e == cudaSuccess && found[dev] <= 0) e = cudaErrorInvalidConfiguration;
+    result[dev] = e;
+  });
+  *per_sm = found[dev];
+  return result[dev];
+}
+
+struct Q8Call {
+  const uint16_t* q;
+  int64_t ldq;
+  int Hq, Hkv;
+  bi::attnq8::Cache C;
+  bi::attn::Rows R;
+  int rows;
+  uint16_t* out;
+  float c;  // scale * log2(e)
+  int sms, dev;
+  cudaStream_t st;
+};
+
+template <int KIND, int D, int RH>
+cudaError_t q8_split(const Q8Call& a, const AttnWs& ws) {
   namespace a8 = bi::attnq8;
-  cudaError_t e = bi::launch_pdl(bi::attn::split_offsets_kernel, dim3(1), dim3(1024), 0, st, R, nrows, ws.off);
+  auto kernel = a8::split_kernel<KIND, D, RH>;
+  struct Tag {};  // one set of once-flags per instantiation
+  int per_sm = 0;
+  const cudaError_t e = resident_ctas<Tag>(kernel, a8::kWarps * 32, a8::Ring<D>::SMEM, a.dev, &per_sm);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(sms * 4)), block(a8::kWarps * 32);
-  e = Hq / Hkv <= 8 ? bi::launch_pdl(a8::split_kernel<KIND, D, 1>, grid, block, 0, st, q, Hq, Hkv, C, R, nrows,
-                                     (const int32_t*)ws.off, ws.po, ws.pml, c)
-                    : bi::launch_pdl(a8::split_kernel<KIND, D, 2>, grid, block, 0, st, q, Hq, Hkv, C, R, nrows,
-                                     (const int32_t*)ws.off, ws.po, ws.pml, c);
-  if (e != cudaSuccess) return e;
-  return bi::launch_pdl(a8::combine_kernel<D>, dim3((unsigned)((nrows * Hq + 7) / 8)), dim3(256), 0, st,
-                        (const float*)ws.po, (const float2*)ws.pml, (const int32_t*)ws.off, nrows, Hq, out);
+  // no more CTAs than there can be items
+  const int ms = max_splits(a.R.max_pages);
+  const int64_t ctas = ((int64_t)a.rows * ms * a.Hkv + a8::kWarps - 1) / a8::kWarps;
+  const int64_t full = (int64_t)a.sms * per_sm;
+  return bi::launch_pdl(kernel, dim3((unsigned)(ctas < full ? ctas : full)), dim3(a8::kWarps * 32),
+                        (size_t)a8::Ring<D>::SMEM, a.st, a.q, a.Hq, a.Hkv, a.C, a.R, a.rows, ms, ws.po, ws.pml, a.c);
 }
 
 template <int KIND, int D>
-cudaError_t q8_prefill(const uint16_t* q, int64_t ldq, int Hq, int Hkv, const bi::attnq8::Cache& C, bi::attn::Rows R,
-                       int T, bi::attnq8::Tile* tiles, int32_t* count, uint16_t* out, float c, int sms,
-                       cudaStream_t st) {
+cudaError_t q8_decode(const Q8Call& a, const AttnWs& ws) {
   namespace a8 = bi::attnq8;
-  cudaError_t e = bi::launch_pdl(a8::plan_kernel, dim3(1), dim3(1024), 0, st, R, T, 16 / (Hq / Hkv), tiles, count);
+  const cudaError_t e = a.Hq / a.Hkv <= 8 ? q8_split<KIND, D, 1>(a, ws) : q8_split<KIND, D, 2>(a, ws);
   if (e != cudaSuccess) return e;
-  return bi::launch_pdl(a8::tile_kernel<KIND, D>, dim3((unsigned)(sms * 3)), dim3(a8::kTileWarps * 32),
-                        (size_t)a8::tile_smem_bytes<D>(), st, q, ldq, Hq, Hkv, C, R, (const a8::Tile*)tiles,
-                        (const int32_t*)count, out, c);
+  // one dim per lane while that leaves at most 32 warps per SM, else D / 32 (fewer, wider loads)
+  const int64_t heads = (int64_t)a.rows * a.Hq;
+  const bool narrow = heads * (D / 32) <= (int64_t)a.sms * 32;
+  auto kernel = narrow ? a8::combine_kernel<D, 1> : a8::combine_kernel<D, D / 32>;
+  return bi::launch_pdl(kernel, dim3((unsigned)((heads * (narrow ? D / 32 : 1) + 7) / 8)), dim3(256), 0, a.st,
+                        (const float*)ws.po, (const float2*)ws.pml, a.R, a.rows, max_splits(a.R.max_pages), a.Hq, a.out);
+}
+
+template <int KIND, int D>
+cudaError_t q8_prefill(const Q8Call& a, bi::attnq8::Tile* tiles, int32_t* count) {
+  namespace a8 = bi::attnq8;
+  cudaError_t e = bi::launch_pdl(a8::plan_kernel, dim3(1), dim3(1024), 0, a.st, a.R, a.rows, 16 / (a.Hq / a.Hkv), tiles,
+                                 count);
+  if (e != cudaSuccess) return e;
+  return bi::launch_pdl(a8::tile_kernel<KIND, D>, dim3((unsigned)(a.sms * 3)), dim3(a8::kTileWarps * 32),
+                        (size_t)a8::tile_smem_bytes<D>(), a.st, a.q, a.ldq, a.Hq, a.Hkv, a.C, a.R,
+                        (const a8::Tile*)tiles, (const int32_t*)count, a.out, a.c);
 }
 
 // ---- LM head workspace: bf16 logits [M, V], fp32 logits [M, V], flagged list [M + 1],
@@ -586,14 +628,17 @@ bi_status bi_attention_decode_q8(const bi_bf16* q, const void* k_cache, const vo
   if (!aligned16(workspace)) return BI_ERR_ALIGN;
   AttnWs lay{};
   if (workspace_bytes < attn_ws_size(B, Hq, D, max_pages_per_seq, &lay, workspace)) return BI_ERR_WORKSPACE;
-  const int sms = device_sms();
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BI_ERR_CUDA;
+  const int sms = bi::gemm::device_sms(dev);
   if (sms <= 0) return BI_ERR_CUDA;
   const bi::attnq8::Cache C{(const uint8_t*)k_cache, (const uint8_t*)v_cache, k_scale, v_scale, num_pages, page_table};
   const bi::attn::Rows R{seq_lens, nullptr, nullptr, B, max_pages_per_seq};
   const float c = (float)((double)scale * 1.4426950408889634);  // scale * log2(e)
   auto call = kind == BI_KV_INT8 ? (D == 128 ? q8_decode<BI_KV_INT8, 128> : q8_decode<BI_KV_INT8, 64>)
                                  : (D == 128 ? q8_decode<BI_KV_E4M3, 128> : q8_decode<BI_KV_E4M3, 64>);
-  return call(q, Hq, Hkv, C, R, B, lay, out, c, sms, as_stream(stream)) == cudaSuccess ? BI_OK : BI_ERR_CUDA;
+  const Q8Call a{q, (int64_t)Hq * D, Hq, Hkv, C, R, B, out, c, sms, dev, as_stream(stream)};
+  return call(a, lay) == cudaSuccess ? BI_OK : BI_ERR_CUDA;
 }
 
 size_t bi_attention_prefill_q8_workspace_size(int64_t T) {
@@ -612,7 +657,9 @@ bi_status bi_attention_prefill_q8(const bi_bf16* q, int64_t ldq, const int32_t* 
   if (T == 0) return BI_OK;
   if (!workspace || workspace_bytes < bi_attention_prefill_q8_workspace_size(T)) return BI_ERR_WORKSPACE;
   if (!aligned16(workspace)) return BI_ERR_ALIGN;
-  const int sms = device_sms();
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BI_ERR_CUDA;
+  const int sms = bi::gemm::device_sms(dev);
   if (sms <= 0) return BI_ERR_CUDA;
   const bi::attnq8::Cache C{(const uint8_t*)k_cache, (const uint8_t*)v_cache, k_scale, v_scale, num_pages, page_table};
   const bi::attn::Rows R{nullptr, q_seq, q_pos, num_seqs, max_pages_per_seq};
@@ -621,8 +668,8 @@ bi_status bi_attention_prefill_q8(const bi_bf16* q, int64_t ldq, const int32_t* 
   auto* tiles = reinterpret_cast<bi::attnq8::Tile*>(static_cast<uint8_t*>(workspace) + 256);
   auto call = kind == BI_KV_INT8 ? (D == 128 ? q8_prefill<BI_KV_INT8, 128> : q8_prefill<BI_KV_INT8, 64>)
                                  : (D == 128 ? q8_prefill<BI_KV_E4M3, 128> : q8_prefill<BI_KV_E4M3, 64>);
-  return call(q, ldq, Hq, Hkv, C, R, T, tiles, count, out, c, sms, as_stream(stream)) == cudaSuccess ? BI_OK
-                                                                                                   : BI_ERR_CUDA;
+  const Q8Call a{q, ldq, Hq, Hkv, C, R, T, out, c, sms, dev, as_stream(stream)};
+  return call(a, tiles, count) == cudaSuccess ? BI_OK : BI_ERR_CUDA;
 }
 
 bi_status bi_qk_norm_rope(const bi_bf16* q, int64_t ldq, const bi_bf16* k, int64_t ldk, const bi_bf16* q_weight,
