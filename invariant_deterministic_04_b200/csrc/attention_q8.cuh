@@ -2,31 +2,34 @@
 //
 // For a query row (one token, one head) with visible keys 0 .. L-1 of its sequence:
 //   s_t = scale q . (k_t sk_t),  out = sum_t e^(s_t) v_t sv_t / sum_t e^(s_t).
-// In the base-2 domain with z_t = s_t log2 e + log2 sv_t and w_t = 2^(z_t - max z):
+// In the base-2 domain with z_t = s_t log2 e + log2 sv_t, any m and w_t = 2^(z_t - m):
 //   out = sum_t w_t v_t / sum_t (w_t / sv_t),
-// so the value scale rides in the exponent, w_t lies in [0, 1] however far apart the rows'
-// scales are, and both sums use the same w_t (an error of log2 sv_t is a common factor of a
-// token's two terms).
+// so the value scale rides in the exponent, the weights share one range however far apart the
+// rows' scales are, and both sums use the same w_t (an error of log2 sv_t is a common factor of
+// a token's two terms). m follows the running maximum of z lazily: it moves, to the maximum,
+// when that has risen by more than kSlack = 8, so w_t <= 2^8 and most pages need neither a
+// reduction over lanes nor a rescaling of the sums.
 //
-// The products run on mma.sync m16n8k16 (f16 operands, fp32 sums). 8-bit keys and values are
-// exact in f16. A query row is brought to |q| < 2^15 by a power of two (exact but for dims
-// 2^28 below the row's largest, which lose bits below 2^-39 of it); 2^14 w_t is rounded to f16
-// (half a step 2^-12 relative, and 2^-39 of the largest weight below 2^-28 of it), a finer
-// rounding than the bf16 output's 2^-9. All sums and the softmax statistics are fp32.
-// mma.sync takes its operands from registers, which is what this read pattern needs: decode
-// has 1 to 16 query rows per kv-head, one MMA tile, and the 8-bit bytes go from HBM into the
-// lane that widens them without a stop in shared memory.
+// The products run on mma.sync m16n8k16 (f16 operands, fp32 sums), keys and values as the
+// 16-row operand, 8 query rows as the other: scores^T = K Q^T, out^T = V^T W^T. Decode has 1 to
+// 16 query rows per kv-head, so this wastes the least of the MMA, and the operands come from
+// registers: the 8-bit bytes go from HBM to the lane that widens them. 8-bit keys and values
+// are exact in f16. A query row is brought to |q| < 2^15 by a power of two (exact but for dims
+// 2^28 below the row's largest, which lose bits below 2^-39 of it). 2^7 w_t <= 2^15 is rounded
+// to f16: half a step 2^-12 relative (finer than the bf16 output's 2^-9), and 2^-32 of the
+// largest weight for weights 2^-21 below it. All sums and the softmax statistics are fp32.
 //
 // Per-row schedule (a function of the row's own L only, so decode, whole and chunked prefill,
 // and any batch give the same bits):
 //   * keys are cut into splits at absolute positions 0, 256, 512, ...; a split is folded page
-//     by page (16 tokens, one MMA k-step of weights x values) with a running maximum;
-//   * s_t is one chain of D/16 MMAs, dims in a fixed order; a lane sums its 4 tokens' w / sv of
-//     each page in order, and the 4 lanes of a row are added by an xor tree at the split's end;
+//     by page (16 tokens, one MMA k-step of weights x values);
+//   * s_t is one chain of D/16 MMAs, dims in a fixed order; lane t mod 8 sums w / sv over its two
+//     tokens of each page in order, and the 8 lanes are added by an xor tree at the split's end;
+//   * whether m moves at a page depends on the row's own scores;
 //   * splits are folded in ascending order: M' = max(M, m_s), X = X 2^(M-M') + x_s 2^(m_s-M').
-// An MMA's output row depends on its own A row only, so it does not matter which rows share
-// a tile. Tokens a row does not see get w = 0 exactly and stale value bytes are replaced by
-// zeros; rows that see nothing give zeros.
+// An MMA's output column depends on its own column of query rows only, so it does not matter
+// which rows share a tile. Tokens a row does not see get w = 0 exactly and stale value bytes are
+// replaced by zeros; rows that see nothing give zeros.
 #pragma once
 
 #include "attention.cuh"
@@ -75,17 +78,24 @@ __device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
   return v;
 }
 
-// d += A B with A 16 x 16 (rows = query rows), B 16 x 8, f16 operands.
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// d += A B with A 16 x 16 (keys or values), B 16 x 8 (columns = query rows), f16 operands.
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
       "%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Transposes an 8 x 8 matrix of 16-bit elements held two to a lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 
@@ -109,57 +119,45 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 
 // Lane layout (g = lane / 4, c = lane % 4, as in an MMA fragment):
-//   queries: MMA rows g and g + 8; MMA step j covers dims 64 (j/4) + 16 c + 4 (j%4) + 0..3 of lane c;
-//   keys: MMA column g of n-tile i is token 8 i + g; the lane loads dims 64 v + 16 c .. + 15;
-//   scores: the lane holds tokens 2c, 2c+1, 2c+8, 2c+9 of rows g and g + 8, which is the A
-//     fragment of weights x values as it stands;
-//   values: the lane loads those four tokens' dims (D/8) g .. + D/8 - 1; MMA column g of n-tile i
-//     is dim (D/8) g + i, so it holds output dims (D/4) c .. + D/4 - 1 of rows g and g + 8.
-template <int D>
-struct Page {
-  uint4 k[2][D / 64];
-  uint32_t v[4][D / 32];
-  float ks[4], vs[4];  // of tokens 2c, 2c+1, 2c+8, 2c+9
-};
+//   keys: MMA rows g and g + 8 are tokens g and g + 8 of the page; step j covers dims
+//     64 (j/4) + 16 c + 4 (j%4) + 0..3 of lane c, so the lane loads dims 64 v + 16 c .. + 15;
+//   queries: column g of tile n is query row 8 n + g, same dims;
+//   scores: the lane holds tokens g and g + 8 of query rows 8 n + 2c and + 1; transposed in 8 x 8
+//     blocks they are the weights' operand, tokens 2c, 2c+1 (and + 8) of query row 8 n + g;
+//   values: the lane loads tokens 2c, 2c+1, 2c+8, 2c+9, dims (D/8) g .. + D/8 - 1; rows g and g + 8
+//     of tile i are dims (D/8) g + 2 i and + 1, so the lane ends with output dims
+//     (D/8) g .. + D/8 - 1 of query rows 8 n + 2c and + 1.
 
-template <int D>
-__device__ __forceinline__ void load_page(Page<D>& P, const Cache& C, int64_t row0, int g, int c) {
-  const uint8_t* kp = C.k + (row0 + g) * D + 16 * c;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int v = 0; v < D / 64; ++v) P.k[i][v] = ldg16(kp + i * 8 * D + 64 * v);
-  const uint8_t* vp = C.v + (row0 + 2 * c) * D + (D / 8) * g;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint8_t* p = vp + ((i & 1) + (i >> 1) * 8) * D;
-    if constexpr (D == 128) {
-      const uint4 x = ldg16(p);
-      P.v[i][0] = x.x; P.v[i][1] = x.y; P.v[i][2] = x.z; P.v[i][3] = x.w;
-    } else {
-      const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-      P.v[i][0] = x.x; P.v[i][1] = x.y;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float2 a = __ldg(reinterpret_cast<const float2*>(C.ks + row0 + 8 * i + 2 * c));
-    const float2 b = __ldg(reinterpret_cast<const float2*>(C.vs + row0 + 8 * i + 2 * c));
-    P.ks[2 * i] = a.x; P.ks[2 * i + 1] = a.y;
-    P.vs[2 * i] = b.x; P.vs[2 * i + 1] = b.y;
-  }
+// Four dims (one MMA step) of the keys of tokens g (x) and g + 8 (y).
+template <int KIND>
+__device__ __forceinline__ uint4 key_operand(uint32_t x, uint32_t y) {
+  uint4 a;
+  widen<KIND>(x, a.x, a.z);
+  widen<KIND>(y, a.y, a.w);
+  return a;
 }
 
-// Query rows in A-fragment order. RH = 1: MMA rows 8 .. 15 are empty (groups of up to 8 heads).
-template <int D, int RH>
+// Four dims (two tiles) of the values of tokens 2c, 2c+1, 2c+8, 2c+9.
+template <int KIND>
+__device__ __forceinline__ void value_operands(const uint32_t (&x)[4], uint4& a, uint4& b) {
+  // bytes (token 2c, token 2c+1) of dims 0, 1 | 2, 3, and the same of tokens 2c+8, 2c+9
+  widen<KIND>(__byte_perm(x[0], x[1], 0x5140), a.x, a.y);
+  widen<KIND>(__byte_perm(x[2], x[3], 0x5140), a.z, a.w);
+  widen<KIND>(__byte_perm(x[0], x[1], 0x7362), b.x, b.y);
+  widen<KIND>(__byte_perm(x[2], x[3], 0x7362), b.z, b.w);
+}
+
+// NT tiles of 8 query rows.
+template <int D, int NT>
 struct Query {
-  uint32_t a[D / 16][2 * RH];  // step j: (row g: dims +0,1 | +2,3), then row g + 8
-  float c[RH];                 // scale log2(e) / the row's power of two; NaN if the row is not finite
+  uint32_t b[NT][D / 16][2];
+  float c[NT][2];  // of rows 8 n + 2c, + 1: scale log2(e) / the row's power of two; NaN if the row is not finite
 };
 
-// Loads one query row (nullptr: zeros) into half `r` of the fragment. All lanes of the warp call it.
-template <int D, int RH>
-__device__ __forceinline__ void load_query(Query<D, RH>& Q, int r, const uint16_t* row, int c, float scale_log2) {
+// Loads query row g of tile n (nullptr: zeros). All lanes of the warp call it.
+template <int D, int NT>
+__device__ __forceinline__ void load_query(Query<D, NT>& Q, int n, const uint16_t* row, int lane, float scale_log2) {
+  const int c = lane & 3;
   uint4 x[D / 64][2];
   uint32_t m = 0;
 #pragma unroll
@@ -177,170 +175,123 @@ __device__ __forceinline__ void load_query(Query<D, RH>& Q, int r, const uint16_
   const bool finite = m < kvq8::kNonFiniteBits;
   const float up = __uint_as_float((uint32_t)(127 + 14 - (finite ? e : 14)) << 23);
   const float down = __uint_as_float((uint32_t)(127 - 14 + (finite ? e : 14)) << 23);
-  Q.c[r] = finite ? __fmul_rn(scale_log2, down) : __uint_as_float(0x7FC00000u);
+  const float mine = finite ? __fmul_rn(scale_log2, down) : __uint_as_float(0x7FC00000u);
+  Q.c[n][0] = __shfl_sync(kFullMask, mine, 8 * c);
+  Q.c[n][1] = __shfl_sync(kFullMask, mine, 8 * c + 4);
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) {
     // 4 dims: elements 4 (j%4) .. + 3 of the 16 in x[j/4]
     const uint4 q = x[j / 4][(j % 4) / 2];
     const uint32_t w0 = (j & 1) ? q.z : q.x, w1 = (j & 1) ? q.w : q.y;
-    Q.a[j][2 * r] = pack_f16x2(__fmul_rn(bf16lo(w0), up), __fmul_rn(bf16hi(w0), up));
-    Q.a[j][2 * r + 1] = pack_f16x2(__fmul_rn(bf16lo(w1), up), __fmul_rn(bf16hi(w1), up));
+    Q.b[n][j][0] = pack_f16x2(__fmul_rn(bf16lo(w0), up), __fmul_rn(bf16hi(w0), up));
+    Q.b[n][j][1] = pack_f16x2(__fmul_rn(bf16lo(w1), up), __fmul_rn(bf16hi(w1), up));
   }
 }
 
-// Running state of a split: per row the maximum z, 2^14 sum w / sv over the lane's tokens,
-// and 2^14 sum w v over the lane's output dims (pairs of rows g, g + 8 as the MMA gives them).
-template <int D, int RH>
+// Running state of a split: per query row the reference m, 2^7 sum w / sv over the lane's
+// tokens, and 2^7 sum w v over the lane's output dims (o[n][i]: dims 2i | 2i + 1 of rows 2c, 2c+1).
+template <int D, int NT>
 struct State {
-  float m[RH], l[RH];
-  float o[D / 8][2 * RH];
+  float m[NT][2], l[NT][2];
+  float o[NT][D / 16][4];
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int r = 0; r < RH; ++r) m[r] = -INFINITY, l[r] = 0.f;
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+      for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-      for (int e = 0; e < 2 * RH; ++e) o[i][e] = 0.f;
+        for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+    }
   }
 };
 
-template <int RH>
-__device__ __forceinline__ void mma_rows(float (&d)[2 * RH], const uint32_t (&a)[2 * RH], uint32_t b0, uint32_t b1) {
-  if constexpr (RH == 2) {
-    const uint32_t A[4] = {a[0], a[2], a[1], a[3]};
-    mma16816(d, A, b0, b1);
-  } else {
-    const uint32_t A[4] = {a[0], 0u, a[1], 0u};
-    float t[4] = {d[0], d[1], 0.f, 0.f};
-    mma16816(t, A, b0, b1);
-    d[0] = t[0];
-    d[1] = t[1];
-  }
-}
+// What the fold needs of the lane's tokens g and g + 8.
+struct Tokens {
+  float ks[2], lg[2], ri[2];  // key scale; log2 and reciprocal of the value scale
+};
 
-// Scores of one page: s[i] covers tokens 8 i + 2c, + 1 of row g (then of row g + 8).
-template <int KIND, int D, int RH>
-__device__ __forceinline__ void page_scores(const Query<D, RH>& Q, const Page<D>& P, float (&s)[2][2 * RH]) {
+constexpr float kSlack = 8.f;
+
+// Weights of one page from its scores: moves m (and l and o with it) where it must, adds to l,
+// and gives 2^7 w as the operand of the value product. MASKED: query row (n, e) sees the
+// first nv[n][e] tokens only; otherwise all 16. live: tiles that hold query rows.
+template <int D, int NT, bool MASKED>
+__device__ __forceinline__ void page_weights(const Query<D, NT>& Q, const float (&s)[NT][4], const Tokens& T,
+                                             const int (&nv)[NT][2], int g, int live, State<D, NT>& S,
+                                             uint32_t (&w)[NT][2]) {
+  float z[NT][4];
+  bool over = false;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int n = 0; n < NT; ++n) {
+    if (NT > 1 && n >= live) break;
 #pragma unroll
-    for (int e = 0; e < 2 * RH; ++e) s[i][e] = 0.f;
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-      const uint4 x = P.k[i][j / 4];
-      const uint32_t w = (j % 4) == 0 ? x.x : (j % 4) == 1 ? x.y : (j % 4) == 2 ? x.z : x.w;
-      uint32_t b0, b1;
-      widen<KIND>(w, b0, b1);
-      mma_rows<RH>(s[i], Q.a[j], b0, b1);
+    for (int e = 0; e < 4; ++e) {
+      const int tok = e >> 1, r = e & 1;
+      z[n][e] = __fmaf_rn(s[n][e], __fmul_rn(T.ks[tok], Q.c[n][r]), T.lg[tok]);
+      if (MASKED && g + 8 * tok >= nv[n][r]) z[n][e] = -INFINITY;
+      over |= z[n][e] > __fadd_rn(S.m[n][r], kSlack);
     }
   }
-}
-
-// Weights of one page from its scores: updates m, l and o's scaling, and gives 2^14 w as the
-// A fragment of the value product. lg, ri: log2 and reciprocal of the lane's four tokens'
-// value scales. MASKED: row half r sees the first nv[r] tokens only; otherwise all 16.
-template <int D, int RH, bool MASKED>
-__device__ __forceinline__ void page_weights(const Query<D, RH>& Q, const float (&s)[2][2 * RH], const float (&ks)[4],
-                                             const float (&lg)[4], const float (&ri)[4], const int (&nv)[RH], int c,
-                                             State<D, RH>& S, uint32_t (&w)[2 * RH]) {
-  float z[RH][4];
-  float alpha[RH];
-  bool moved = false;
+  if (__any_sync(kFullMask, over)) {
 #pragma unroll
-  for (int r = 0; r < RH; ++r) {
+    for (int n = 0; n < NT; ++n) {
+      if (NT > 1 && n >= live) break;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      z[r][i] = __fmaf_rn(s[i >> 1][2 * r + (i & 1)], __fmul_rn(ks[i], Q.c[r]), lg[i]);
-      if (MASKED && 8 * (i >> 1) + 2 * c + (i & 1) >= nv[r]) z[r][i] = -INFINITY;
-    }
-    float mx = fmaxf(fmaxf(z[r][0], z[r][1]), fmaxf(z[r][2], z[r][3]));
-    mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 2));
-    const float mn = fmaxf(S.m[r], mx);
-    alpha[r] = mn == S.m[r] ? 1.f : ex2(__fsub_rn(S.m[r], mn));
-    moved |= mn != S.m[r];
-    S.m[r] = mn;
-  }
-  if (__any_sync(kFullMask, moved)) {  // x * 1 == x, so rows whose maximum stayed keep their bits
+      for (int r = 0; r < 2; ++r) {
+        float mx = fmaxf(z[n][r], z[n][2 + r]);
 #pragma unroll
-    for (int r = 0; r < RH; ++r) {
-      S.l[r] = __fmul_rn(S.l[r], alpha[r]);
+        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, d));
+        const bool up = mx > __fadd_rn(S.m[n][r], kSlack);
+        const float alpha = up ? ex2(__fsub_rn(S.m[n][r], mx)) : 1.f;  // x * 1 == x: the other rows keep their bits
+        if (up) S.m[n][r] = mx;
+        S.l[n][r] = __fmul_rn(S.l[n][r], alpha);
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        S.o[i][2 * r] = __fmul_rn(S.o[i][2 * r], alpha[r]);
-        S.o[i][2 * r + 1] = __fmul_rn(S.o[i][2 * r + 1], alpha[r]);
+        for (int i = 0; i < D / 16; ++i) {
+          S.o[n][i][r] = __fmul_rn(S.o[n][i][r], alpha);
+          S.o[n][i][2 + r] = __fmul_rn(S.o[n][i][2 + r], alpha);
+        }
       }
     }
   }
 #pragma unroll
-  for (int r = 0; r < RH; ++r) {
-    const float ref = S.m[r] == -INFINITY ? 0.f : __fsub_rn(S.m[r], 14.f);
+  for (int n = 0; n < NT; ++n) {
+    if (NT > 1 && n >= live) break;
     float p[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      p[i] = ex2(__fsub_rn(z[r][i], ref));
-      if (!MASKED || 8 * (i >> 1) + 2 * c + (i & 1) < nv[r]) S.l[r] = __fmaf_rn(p[i], ri[i], S.l[r]);
+    for (int r = 0; r < 2; ++r) {
+      const float ref = S.m[n][r] == -INFINITY ? 0.f : __fsub_rn(S.m[n][r], 7.f);
+#pragma unroll
+      for (int tok = 0; tok < 2; ++tok) {
+        p[2 * tok + r] = ex2(__fsub_rn(z[n][2 * tok + r], ref));
+        if (!MASKED || g + 8 * tok < nv[n][r]) S.l[n][r] = __fmaf_rn(p[2 * tok + r], T.ri[tok], S.l[n][r]);
+      }
     }
-    w[2 * r] = pack_f16x2(p[0], p[1]);
-    w[2 * r + 1] = pack_f16x2(p[2], p[3]);
+    w[n][0] = transpose8x8(pack_f16x2(p[0], p[1]));
+    w[n][1] = transpose8x8(pack_f16x2(p[2], p[3]));
   }
 }
 
-// o += weights x values of one page. `seen`: tokens from there on are replaced by zeros.
-template <int KIND, int D, int RH, bool MASKED>
-__device__ __forceinline__ void page_values(const Page<D>& P, const uint32_t (&w)[2 * RH], int seen, int c,
-                                            State<D, RH>& S) {
-#pragma unroll
-  for (int u = 0; u < D / 32; ++u) {
-    uint32_t x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = P.v[i][u];
-      if (MASKED && 8 * (i >> 1) + 2 * c + (i & 1) >= seen) x[i] = 0;
-    }
-    // bytes (token 2c, token 2c+1) of dims 4u, 4u+1 | 4u+2, 4u+3, and the same of tokens 2c+8, 2c+9
-    const uint32_t a0 = __byte_perm(x[0], x[1], 0x5140), a1 = __byte_perm(x[0], x[1], 0x7362);
-    const uint32_t b0 = __byte_perm(x[2], x[3], 0x5140), b1 = __byte_perm(x[2], x[3], 0x7362);
-    uint32_t f0, f1, f2, f3, h0, h1, h2, h3;
-    widen<KIND>(a0, f0, f1);
-    widen<KIND>(a1, f2, f3);
-    widen<KIND>(b0, h0, h1);
-    widen<KIND>(b1, h2, h3);
-    mma_rows<RH>(S.o[4 * u], w, f0, h0);
-    mma_rows<RH>(S.o[4 * u + 1], w, f1, h1);
-    mma_rows<RH>(S.o[4 * u + 2], w, f2, h2);
-    mma_rows<RH>(S.o[4 * u + 3], w, f3, h3);
-  }
-}
-
-// Folds one page of which `seen` tokens exist for the tile and nv[r] for row half r.
-template <int KIND, int D, int RH>
-__device__ __forceinline__ void fold_page(const Query<D, RH>& Q, const Page<D>& P, const int (&nv)[RH], int seen, int c,
-                                          State<D, RH>& S) {
-  float s[2][2 * RH], lg[4], ri[4];
-  uint32_t w[2 * RH];
-  page_scores<KIND, D, RH>(Q, P, s);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) lg[i] = lg2(P.vs[i]), ri[i] = rcp(P.vs[i]);
+template <int D, int NT>
+__device__ __forceinline__ void weights(const Query<D, NT>& Q, const float (&s)[NT][4], const Tokens& T,
+                                        const int (&nv)[NT][2], int g, int live, State<D, NT>& S,
+                                        uint32_t (&w)[NT][2]) {
   bool all = true;
 #pragma unroll
-  for (int r = 0; r < RH; ++r) all &= nv[r] >= PAGE;
-  if (__all_sync(kFullMask, all)) {
-    page_weights<D, RH, false>(Q, s, P.ks, lg, ri, nv, c, S, w);
-    page_values<KIND, D, RH, false>(P, w, seen, c, S);
-  } else {
-    page_weights<D, RH, true>(Q, s, P.ks, lg, ri, nv, c, S, w);
-    page_values<KIND, D, RH, true>(P, w, seen, c, S);
-  }
+  for (int n = 0; n < NT; ++n) all &= nv[n][0] >= PAGE && nv[n][1] >= PAGE;
+  if (__all_sync(kFullMask, all)) page_weights<D, NT, false>(Q, s, T, nv, g, live, S, w);
+  else page_weights<D, NT, true>(Q, s, T, nv, g, live, S, w);
 }
 
-// The xor tree over a row's 4 lanes that ends a split.
+// The xor tree over a query row's 8 lanes that ends a split.
 __device__ __forceinline__ float row_sum(float l) {
-  l = __fadd_rn(l, __shfl_xor_sync(kFullMask, l, 1));
-  return __fadd_rn(l, __shfl_xor_sync(kFullMask, l, 2));
+#pragma unroll
+  for (int d = 4; d < 32; d <<= 1) l = __fadd_rn(l, __shfl_xor_sync(kFullMask, l, d));
+  return l;
 }
 
-// One step of the fold over splits: (M, L, O) and split (m, l, o) -> weights of both.
+// One step of the fold over splits: M and a split's m -> the factors of both sides.
 __device__ __forceinline__ void join(float& M, float m, float& a, float& b) {
   const float mn = fmaxf(M, m);
   const float ref = mn == -INFINITY ? 0.f : mn;
@@ -364,7 +315,7 @@ constexpr int kCoarse = 1024;  // entries of the split-count prefix that a CTA k
 
 template <int D>
 struct Ring {
-  static constexpr int K_BYTES = PAGE * D;         // [n-tile][64-dim part][lane] 16 bytes
+  static constexpr int K_BYTES = PAGE * D;         // [token g | g + 8][64-dim part][lane] 16 bytes
   static constexpr int V_BYTES = PAGE * D;         // [token of the lane's four][lane] D/8 bytes
   static constexpr int STAGE = K_BYTES + V_BYTES + 2 * PAGE * 4;  // and the page's scales
   static constexpr int WARP = kStages * STAGE;
@@ -403,29 +354,70 @@ __device__ __forceinline__ void copy_page(uint32_t stage, const Cache& C, int64_
     cp_async<16>(stage + T::K_BYTES + T::V_BYTES + 16 * lane, (lane < 4 ? C.ks + row0 : C.vs + row0 - 16) + 4 * lane);
 }
 
-// The lane's part of a page from its ring stage.
-template <int D>
-__device__ __forceinline__ void read_page(Page<D>& P, uint32_t stage, int lane) {
-  using T = Ring<D>;
+// Folds the page in a ring stage; `seen` of its tokens exist, query row (n, e) sees nv[n][e].
+template <int KIND, int D, int NT>
+__device__ __forceinline__ void fold_page(const Query<D, NT>& Q, uint32_t stage, const int (&nv)[NT][2], int seen,
+                                          int live, int lane, State<D, NT>& S) {
+  using R = Ring<D>;
+  const int g = lane >> 2, c = lane & 3;
+  float s[NT][4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int v = 0; v < D / 64; ++v) P.k[i][v] = ld_shared_v4(stage + ((i * (D / 64) + v) * 32 + lane) * 16);
+    for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a = stage + T::K_BYTES + (i * 32 + lane) * (D / 8);
-    if constexpr (D == 128) {
-      const uint4 x = ld_shared_v4(a);
-      P.v[i][0] = x.x; P.v[i][1] = x.y; P.v[i][2] = x.z; P.v[i][3] = x.w;
-    } else {
-      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(P.v[i][0]), "=r"(P.v[i][1]) : "r"(a));
+  for (int v = 0; v < D / 64; ++v) {
+    const uint4 x = ld_shared_v4(stage + (v * 32 + lane) * 16);
+    const uint4 y = ld_shared_v4(stage + ((D / 64 + v) * 32 + lane) * 16);
+    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const uint4 a = key_operand<KIND>(xw[b], yw[b]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (NT == 1 || n < live) mma16816(s[n], a, Q.b[n][4 * v + b][0], Q.b[n][4 * v + b][1]);
     }
   }
-  const uint32_t sc = stage + T::K_BYTES + T::V_BYTES + 8 * (lane & 3);
+  Tokens T;
+  const uint32_t sc = stage + R::K_BYTES + R::V_BYTES + 4 * g;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(P.ks[2 * i]), "=f"(P.ks[2 * i + 1]) : "r"(sc + 32 * i));
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(P.vs[2 * i]), "=f"(P.vs[2 * i + 1]) : "r"(sc + 64 + 32 * i));
+  for (int t = 0; t < 2; ++t) {
+    const float vs = ld_shared_f32(sc + 64 + 32 * t);
+    T.ks[t] = ld_shared_f32(sc + 32 * t);
+    T.lg[t] = lg2(vs);
+    T.ri[t] = rcp(vs);
+  }
+  uint32_t w[NT][2];
+  weights<D, NT>(Q, s, T, nv, g, live, S, w);
+  uint32_t x[4][D / 32];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t at = stage + R::K_BYTES + (i * 32 + lane) * (D / 8);
+    if constexpr (D == 128) {
+      const uint4 t = ld_shared_v4(at);
+      x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
+    } else {
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[i][0]), "=r"(x[i][1]) : "r"(at));
+    }
+  }
+  if (seen < PAGE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (2 * c + (i & 1) + 8 * (i >> 1) >= seen)
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) x[i][u] = 0;
+  }
+#pragma unroll
+  for (int u = 0; u < D / 32; ++u) {
+    uint4 a, b;
+    const uint32_t xu[4] = {x[0][u], x[1][u], x[2][u], x[3][u]};
+    value_operands<KIND>(xu, a, b);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (NT > 1 && n >= live) break;
+      mma16816(S.o[n][2 * u], a, w[n][0], w[n][1]);
+      mma16816(S.o[n][2 * u + 1], b, w[n][0], w[n][1]);
+    }
   }
 }
 
@@ -434,7 +426,7 @@ struct Item {
   int r, s, kh, seen, page;
 };
 
-template <int KIND, int D, int RH>
+template <int KIND, int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4)
     split_kernel(const uint16_t* __restrict__ q, int Hq, int Hkv, Cache C, Rows R, int nrows, int max_splits,
                  float* __restrict__ po, float2* __restrict__ pml, float scale_log2) {
@@ -531,13 +523,13 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4)
   for (int i = 0; i < kStages; ++i) issue();
 
   while (true) {
-    Query<D, RH> Q;
+    Query<D, NT> Q;
 #pragma unroll
-    for (int h = 0; h < RH; ++h) {
-      const int head = g + 8 * h;
-      load_query<D, RH>(Q, h, head < G ? q + ((int64_t)cur.r * Hq + cur.kh * G + head) * D : nullptr, c, scale_log2);
+    for (int n = 0; n < NT; ++n) {
+      const int head = g + 8 * n;
+      load_query<D, NT>(Q, n, head < G ? q + ((int64_t)cur.r * Hq + cur.kh * G + head) * D : nullptr, lane, scale_log2);
     }
-    State<D, RH> S;
+    State<D, NT> S;
     S.clear();
     for (int j = 0; j * PAGE < cur.seen; ++j) {
       // with the ring full the oldest copy group is the page wanted; otherwise (the stream's end,
@@ -546,33 +538,31 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4)
       else cp_wait<0>();
       __syncwarp();
       if (__shfl_sync(kFullMask, cur.page, j) >= 0) {  // the tokens of an unusable page are not seen
-        Page<D> P;
-        read_page<D>(P, ring + (uint32_t)(used % kStages) * T::STAGE, lane);
-        int nv[RH];
+        const int seen = cur.seen - j * PAGE;
+        int nv[NT][2];
 #pragma unroll
-        for (int h = 0; h < RH; ++h) nv[h] = cur.seen - j * PAGE;
-        fold_page<KIND, D, RH>(Q, P, nv, nv[0], c, S);
+        for (int n = 0; n < NT; ++n) nv[n][0] = nv[n][1] = seen;
+        fold_page<KIND, D, NT>(Q, ring + (uint32_t)(used % kStages) * T::STAGE, nv, seen, NT, lane, S);
       }
       ++used;
       __syncwarp();  // every lane has read this page's scales: its stage may be refilled
       issue();
     }
 #pragma unroll
-    for (int h = 0; h < RH; ++h) {
-      const float l = row_sum(S.l[h]);
-      const int head = g + 8 * h;
-      if (head >= G) continue;
-      const int64_t slot = ((int64_t)cur.r * max_splits + cur.s) * Hq + cur.kh * G + head;
-      float* dst = po + slot * D + (D / 4) * c;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < D / 8; i += 4) {
-        *reinterpret_cast<float4*>(dst + i) =
-            make_float4(S.o[i][2 * h], S.o[i + 1][2 * h], S.o[i + 2][2 * h], S.o[i + 3][2 * h]);
-        *reinterpret_cast<float4*>(dst + D / 8 + i) =
-            make_float4(S.o[i][2 * h + 1], S.o[i + 1][2 * h + 1], S.o[i + 2][2 * h + 1], S.o[i + 3][2 * h + 1]);
+      for (int r = 0; r < 2; ++r) {
+        const float l = row_sum(S.l[n][r]);
+        const int head = 8 * n + 2 * c + r;
+        if (head >= G) continue;
+        const int64_t slot = ((int64_t)cur.r * max_splits + cur.s) * Hq + cur.kh * G + head;
+        float* dst = po + slot * D + (D / 8) * g;
+#pragma unroll
+        for (int i = 0; i < D / 16; i += 2)
+          *reinterpret_cast<float4*>(dst + 2 * i) =
+              make_float4(S.o[n][i][r], S.o[n][i][2 + r], S.o[n][i + 1][r], S.o[n][i + 1][2 + r]);
+        if (g == 0) pml[slot] = make_float2(S.m[n][r], l);
       }
-      if (c == 0) pml[slot] = make_float2(S.m[h], l);
-    }
     if (item + step >= total) break;
     item += step;
     if (!ahead) {  // nothing of the next item has been asked for yet
@@ -666,7 +656,17 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
 }
 
 // ---------------------------------------------------------------------------
-// Prefill: query rows of one sequence are taken in tiles of up to 16 MMA rows.
+// Prefill: rows of one sequence that follow one another in the batch are taken in tiles.
+//
+// A tile has up to kTileRows query rows (row i is query head i % G of token i / G) and one kv-head,
+// and runs on one CTA of four warps:
+//   * more than kWarpRows query rows: each warp takes kWarpRows of them, and the CTA widens a chunk of pages
+//     once into f16 operands in shared memory (in fragment order, so every access is a contiguous
+//     16 bytes a lane), double buffered, the next chunk's bytes on their way in registers;
+//   * fewer (decode rows in a mixed batch, ends of chunks): every warp takes all the rows and
+//     every fourth split with its own ring, as in decode, and the CTA folds four splits at a time.
+// Either way a split is folded by one warp in the order above, and splits in ascending order.
+// Bound: the tensor cores' mma.sync rate and the softmax's arithmetic between the MMAs.
 
 // A tile: rows first .. first + n - 1 (one sequence), the longest of their visible lengths.
 struct Tile {
@@ -727,95 +727,341 @@ __global__ void __launch_bounds__(1024) plan_kernel(Rows R, int T, int per, Tile
 }
 
 constexpr int kTileWarps = 4;
+constexpr int kNT = 2;  // tiles of 8 query rows per warp
+constexpr int kWarpRows = 8 * kNT;
+constexpr int kTileRows = kTileWarps * kWarpRows;
 
 template <int D>
-constexpr int tile_smem_bytes() {
-  return kTileWarps * 16 * D * 4;
+struct TileSmem {
+  static constexpr int PAGES = 256 / D;                   // pages a chunk: one item of each kind per warp
+  static constexpr int OPERANDS = PAGES * 2 * PAGE * D * 2;  // f16 keys and values
+  static constexpr int BUFFER = OPERANDS + PAGES * PAGE * 16;  // and {ks, log2 vs, 1 / vs, -} per token
+  static constexpr int TOTALS = kTileRows * D * 4;
+  // few rows: the rings, over which the four splits' partial results go, and the totals
+  static constexpr int RINGS = kTileWarps * Ring<D>::WARP;
+  static constexpr int PARTIALS = kTileWarps * kWarpRows * D * 4;
+  static constexpr int SMALL = (RINGS > PARTIALS ? RINGS : PARTIALS) + kTileWarps * kWarpRows * 8 + kWarpRows * D * 4;
+  static constexpr int LARGE = 2 * BUFFER + TOTALS;
+  static constexpr int BYTES = SMALL > LARGE ? SMALL : LARGE;
+};
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
 }
 
-// One warp per (tile, kv-head): MMA row i is query head i % G of token i / G. Splits are folded
-// into running totals in shared memory (one float per lane, row half and output dim).
+// One lane's bytes of a chunk: key bytes of tokens g, g + 8 and value bytes of four tokens of
+// the page and part that its warp widens, and a token's scales.
+struct Raw {
+  uint4 k[2];
+  uint2 v[4];
+  float ks, vs;
+};
+
+template <int D>
+__device__ __forceinline__ int64_t tile_row0(const Cache& C, const int32_t* prow, int tp, int len, int Hkv, int kh) {
+  if (tp >= len) return -1;
+  const int pg = prow[tp / PAGE];
+  if (pg < 0 || pg >= C.num_pages) {
+    record_error(BI_ERR_DEVICE_INDEX);
+    return -1;
+  }
+  return ((int64_t)pg * Hkv + kh) * PAGE;
+}
+
+// Loads chunk tp .. of a tile; bytes of unusable pages and of tokens from len on are zeros.
+template <int D>
+__device__ __forceinline__ void load_chunk(Raw& X, const Cache& C, const int32_t* prow, int tp, int len, int Hkv, int kh,
+                                           int warp, int lane) {
+  const int g = lane >> 2, c = lane & 3;
+  static_assert(TileSmem<D>::PAGES * (D / 64) == kTileWarps, "one page part a warp");
+  const int page = warp / (D / 64), part = warp % (D / 64);
+  const int t0 = tp + page * PAGE;
+  const int64_t row0 = tile_row0<D>(C, prow, t0, len, Hkv, kh);
+  const uint8_t* kp = C.k + (row0 + g) * D + 64 * part + 16 * c;
+  X.k[0] = row0 >= 0 ? ldg16(kp) : make_uint4(0, 0, 0, 0);
+  X.k[1] = row0 >= 0 ? ldg16(kp + 8 * D) : make_uint4(0, 0, 0, 0);
+  const uint8_t* vp = C.v + (row0 + 2 * c) * D + (D / 8) * g + 8 * part;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = (i & 1) + 8 * (i >> 1);
+    X.v[i] = row0 >= 0 && t0 + 2 * c + t < len ? __ldg(reinterpret_cast<const uint2*>(vp + t * D)) : make_uint2(0, 0);
+  }
+  const int tok = warp * 32 + lane;
+  X.ks = 0.f;
+  X.vs = 0.f;  // log2 is -infinity: the token has no weight
+  if (tok < TileSmem<D>::PAGES * PAGE) {
+    const int64_t r = tile_row0<D>(C, prow, tp + tok / PAGE * PAGE, len, Hkv, kh);
+    if (r >= 0 && tp + tok < len) {
+      X.ks = __ldg(C.ks + r + tok % PAGE);
+      X.vs = __ldg(C.vs + r + tok % PAGE);
+    }
+  }
+}
+
+// Widens the loaded chunk into a buffer: keys [page][step][lane], values [page][tile][lane], tokens.
 template <int KIND, int D>
-__global__ void __launch_bounds__(kTileWarps * 32) tile_kernel(const uint16_t* __restrict__ q, int64_t ldq, int Hq, int Hkv, Cache C,
-                                                               Rows R, const Tile* __restrict__ tiles,
-                                                               const int32_t* __restrict__ count,
-                                                               uint16_t* __restrict__ out, float scale_log2) {
-  extern __shared__ float totals[];
+__device__ __forceinline__ void store_chunk(const Raw& X, uint32_t buf, int warp, int lane) {
+  using M = TileSmem<D>;
+  const int page = warp / (D / 64), part = warp % (D / 64);
+  const uint32_t kb = buf + ((page * (D / 16) + 4 * part) * 32 + lane) * 16;
+  const uint32_t xw[4] = {X.k[0].x, X.k[0].y, X.k[0].z, X.k[0].w}, yw[4] = {X.k[1].x, X.k[1].y, X.k[1].z, X.k[1].w};
+#pragma unroll
+  for (int b = 0; b < 4; ++b) st_shared_v4(kb + b * 512, key_operand<KIND>(xw[b], yw[b]));
+  const uint32_t vb = buf + M::OPERANDS / 2 + ((page * (D / 16) + 4 * part) * 32 + lane) * 16;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    uint32_t x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = u ? X.v[i].y : X.v[i].x;
+    uint4 a, b;
+    value_operands<KIND>(x, a, b);
+    st_shared_v4(vb + (2 * u) * 512, a);
+    st_shared_v4(vb + (2 * u + 1) * 512, b);
+  }
+  const int tok = warp * 32 + lane;
+  if (tok < M::PAGES * PAGE) {
+    const float4 t = make_float4(X.ks, lg2(X.vs), X.vs == 0.f ? 0.f : rcp(X.vs), 0.f);
+    st_shared_v4(buf + M::OPERANDS + tok * 16, *reinterpret_cast<const uint4*>(&t));
+  }
+}
+
+// Folds one page of a buffer.
+template <int D>
+__device__ __forceinline__ void fold_wide(const Query<D, kNT>& Q, uint32_t buf, int page, const int (&nv)[kNT][2],
+                                          int live, int lane, State<D, kNT>& S) {
+  using M = TileSmem<D>;
+  const int g = lane >> 2;
+  float s[kNT][4];
+#pragma unroll
+  for (int n = 0; n < kNT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+  const uint32_t kb = buf + (page * (D / 16) * 32 + lane) * 16, vb = kb + M::OPERANDS / 2;
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) {
+    const uint4 a = ld_shared_v4(kb + j * 512);
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+      if (n < live) mma16816(s[n], a, Q.b[n][j][0], Q.b[n][j][1]);
+  }
+  Tokens T;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const uint4 x = ld_shared_v4(buf + M::OPERANDS + (page * PAGE + g + 8 * t) * 16);
+    T.ks[t] = __uint_as_float(x.x);
+    T.lg[t] = __uint_as_float(x.y);
+    T.ri[t] = __uint_as_float(x.z);
+  }
+  uint32_t w[kNT][2];
+  weights<D, kNT>(Q, s, T, nv, g, live, S, w);
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const uint4 a = ld_shared_v4(vb + i * 512);
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+      if (n < live) mma16816(S.o[n][i], a, w[n][0], w[n][1]);
+  }
+}
+
+// Writes a query row's dims (D/8) g .. + D/8 - 1.
+template <int D>
+__device__ __forceinline__ void store_row(uint16_t* dst, const float (&x)[D / 8], float L) {
+#pragma unroll
+  for (int i = 0; i < D / 8; i += 8) {
+    float y[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) y[u] = L == 0.f ? 0.f : __fdiv_rn(x[i + u], L);
+    *reinterpret_cast<uint4*>(dst + i) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                                    pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+  }
+}
+
+template <int KIND, int D>
+__global__ void __launch_bounds__(kTileWarps * 32, 2)
+    tile_kernel(const uint16_t* __restrict__ q, int64_t ldq, int Hq, int Hkv, Cache C, Rows R,
+                const Tile* __restrict__ tiles, const int32_t* __restrict__ count, uint16_t* __restrict__ out,
+                float scale_log2) {
+  using M = TileSmem<D>;
+  extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int G = Hq / Hkv;
-  float* tot = totals + warp * 16 * D + lane;  // entry i at tot[32 i]
+  const uint32_t base = smem_u32(smem);
   pdl_wait();  // the plan (and the caller's q and store) are complete from here on
   pdl_trigger();
   const int64_t total = (int64_t)*count * Hkv;
-  for (int64_t item = total - 1 - ((int64_t)warp * gridDim.x + blockIdx.x); item >= 0;
-       item -= (int64_t)gridDim.x * kTileWarps) {
+  // later rows of a prompt see more keys: longest first
+  for (int64_t item = total - 1 - blockIdx.x; item >= 0; item -= gridDim.x) {
     const Tile t = tiles[item / Hkv];
     const int kh = (int)(item % Hkv);
-    Query<D, 2> Q;
-    int len[2];
-    int64_t orow[2];
+    const int rows = t.n * G;
+    const bool small = rows <= kWarpRows;
+    const int i0 = small ? 0 : warp * kWarpRows;                    // the warp's first query row
+    const int live = min(kNT, (rows - i0 + 7) / 8);               // its tiles that hold rows (<= 0: none)
+    Query<D, kNT> Q;
+    int len[kNT][2];
+    int longest = 0;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = g + 8 * h, tok = i / G, head = kh * G + i % G;
-      const bool live = tok < t.n;
-      int pt_row;
-      len[h] = live ? attn::row_len(R, t.first + tok, pt_row) : 0;
-      orow[h] = live ? ((int64_t)(t.first + tok) * Hq + head) * D : -1;
-      load_query<D, 2>(Q, h, live ? q + (int64_t)(t.first + tok) * ldq + (int64_t)head * D : nullptr, c, scale_log2);
+    for (int n = 0; n < kNT; ++n) {
+      const int i = i0 + 8 * n + g;
+      load_query<D, kNT>(Q, n, i < rows ? q + (int64_t)(t.first + i / G) * ldq + (int64_t)(kh * G + i % G) * D : nullptr,
+                         lane, scale_log2);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int k = i0 + 8 * n + 2 * c + r;
+        int pt_row;
+        len[n][r] = k < rows ? attn::row_len(R, t.first + k / G, pt_row) : INT_MAX / 2;  // no row: nothing to mask
+        if (k < rows) longest = max(longest, len[n][r]);
+      }
     }
-    float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < D / 2; ++i) tot[32 * i] = 0.f;
+    longest = __reduce_max_sync(kFullMask, longest);
     const int32_t* prow = C.pt + (int64_t)t.pt_row * R.max_pages;
-    for (int t0 = 0; t0 < t.len; t0 += SPLIT) {
-      State<D, 2> S;
-      S.clear();
-      const int t1 = min(t0 + SPLIT, t.len);
-      for (int tp = t0; tp < t1; tp += PAGE) {
-        const int pg = prow[tp / PAGE];
-        if (pg < 0 || pg >= C.num_pages) {
-          if (lane == 0) record_error(BI_ERR_DEVICE_INDEX);
-          continue;
+    float Mx[kNT][2], L[kNT][2];
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+      Mx[n][0] = Mx[n][1] = -INFINITY;
+      L[n][0] = L[n][1] = 0.f;
+    }
+    if (!small) {
+      float* tot = reinterpret_cast<float*>(smem + 2 * M::BUFFER) + warp * kWarpRows * D + lane;  // entry i at tot[32 i]
+      for (int i = 0; i < kWarpRows * D / 32; ++i) tot[32 * i] = 0.f;
+      constexpr int CHUNK = M::PAGES * PAGE;
+      Raw X;
+      if (t.len > 0) load_chunk<D>(X, C, prow, 0, t.len, Hkv, kh, warp, lane);
+      int b = 0;
+      for (int t0 = 0; t0 < t.len; t0 += SPLIT) {
+        State<D, kNT> S;
+        S.clear();
+        for (int tp = t0; tp < min(t0 + SPLIT, t.len); tp += CHUNK, b ^= 1) {
+          const uint32_t buf = base + b * M::BUFFER;
+          store_chunk<KIND, D>(X, buf, warp, lane);
+          if (tp + CHUNK < t.len) load_chunk<D>(X, C, prow, tp + CHUNK, t.len, Hkv, kh, warp, lane);
+          __syncthreads();  // the buffer is complete, and every warp is done with the other one
+          for (int p = 0; p < M::PAGES; ++p) {
+            if (tp + p * PAGE >= longest) break;
+            int nv[kNT][2];
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) nv[n][r] = len[n][r] - tp - p * PAGE;
+            fold_wide<D>(Q, buf, p, nv, live, lane, S);
+          }
         }
-        Page<D> P;
-        load_page<D>(P, C, ((int64_t)pg * Hkv + kh) * PAGE, g, c);
-        const int nv[2] = {len[0] - tp, len[1] - tp};
-        fold_page<KIND, D, 2>(Q, P, nv, t.len - tp, c, S);
-      }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float a, b;
-        const float l = row_sum(S.l[h]);
-        join(M[h], S.m[h], a, b);
-        L[h] = __fmaf_rn(l, b, __fmul_rn(L[h], a));
+        for (int n = 0; n < kNT; ++n)
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
+          for (int r = 0; r < 2; ++r) {
+            float fa, fb;
+            const float l = row_sum(S.l[n][r]);
+            join(Mx[n][r], S.m[n][r], fa, fb);
+            L[n][r] = __fmaf_rn(l, fb, __fmul_rn(L[n][r], fa));
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float* x = tot + 32 * (4 * i + 2 * h + e);
-            *x = __fmaf_rn(S.o[i][2 * h + e], b, __fmul_rn(*x, a));
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float* x = tot + 32 * ((n * 2 + r) * (D / 8) + 2 * i + e);
+                *x = __fmaf_rn(S.o[n][i][2 * e + r], fb, __fmul_rn(*x, fa));
+              }
           }
       }
-    }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (orow[h] < 0) continue;
+      for (int n = 0; n < kNT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+        for (int r = 0; r < 2; ++r) {
+          const int k = i0 + 8 * n + 2 * c + r;
+          if (k >= rows) continue;
+          float x[D / 8];
 #pragma unroll
-        for (int i = 0; i < D / 8; i += 8) {
-          float y[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const float x = tot[32 * (4 * (i + u) + 2 * h + e)];
-            y[u] = L[h] == 0.f ? 0.f : __fdiv_rn(x, L[h]);
-          }
-          *reinterpret_cast<uint4*>(out + orow[h] + (D / 4) * c + e * (D / 8) + i) =
-              make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                         pack_bf16x2(y[6], y[7]));
+          for (int i = 0; i < D / 8; ++i) x[i] = tot[32 * ((n * 2 + r) * (D / 8) + i)];
+          store_row<D>(out + ((int64_t)(t.first + k / G) * Hq + kh * G + k % G) * D + (D / 8) * g, x, L[n][r]);
         }
+    } else {
+      // four splits at a time, one a warp; then row k's thread group folds them in order
+      const uint32_t ring = base + (uint32_t)(warp * Ring<D>::WARP);
+      float* part = reinterpret_cast<float*>(smem);                                  // [warp][row][D]
+      constexpr int OVER = M::RINGS > M::PARTIALS ? M::RINGS : M::PARTIALS;
+      float2* pml = reinterpret_cast<float2*>(smem + OVER);                          // [warp][row]
+      float* tot = reinterpret_cast<float*>(smem + OVER + kTileWarps * kWarpRows * 8);      // [row][D]
+      for (int i = threadIdx.x; i < rows * D; i += kTileWarps * 32) tot[i] = 0.f;
+      // thread -> (row, quarter of D) for the folds
+      const int frow = threadIdx.x >> 2, fd = (threadIdx.x & 3) * (D / 4);
+      float FM = -INFINITY, FL = 0.f;
+      for (int r0 = 0; r0 < t.len; r0 += kTileWarps * SPLIT) {
+        const int t0 = r0 + warp * SPLIT, seen = min(SPLIT, t.len - t0);
+        State<D, kNT> S;
+        S.clear();
+        const int np = seen > 0 ? (seen + PAGE - 1) / PAGE : 0;
+        int page = -1;
+        if (lane < np) {
+          const int64_t row0 = tile_row0<D>(C, prow, t0 + lane * PAGE, t.len, Hkv, kh);
+          page = row0 < 0 ? -1 : (int)(row0 / (Hkv * PAGE));
+        }
+        auto issue = [&](int j) {
+          if (j < np) {
+            const int pg = __shfl_sync(kFullMask, page, j);
+            if (pg >= 0) copy_page<D>(ring + (uint32_t)(j % kStages) * Ring<D>::STAGE, C, ((int64_t)pg * Hkv + kh) * PAGE, lane);
+          }
+          cp_commit();
+        };
+        for (int j = 0; j < kStages; ++j) issue(j);
+        for (int j = 0; j < np; ++j) {
+          cp_wait<kStages - 1>();
+          __syncwarp();
+          if (__shfl_sync(kFullMask, page, j) >= 0) {
+            const int tp = t0 + j * PAGE;
+            int nv[kNT][2];
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) nv[n][r] = len[n][r] - tp;
+            fold_page<KIND, D, kNT>(Q, ring + (uint32_t)(j % kStages) * Ring<D>::STAGE, nv, t.len - tp, live, lane, S);
+          }
+          __syncwarp();
+          issue(j + kStages);
+        }
+        cp_wait<0>();
+        __syncthreads();  // the rings are free (and the totals cleared, or the last fold done)
+        if (np > 0) {
+#pragma unroll
+          for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float l = row_sum(S.l[n][r]);
+              const int k = 8 * n + 2 * c + r;
+              if (k >= rows) continue;
+              float* dst = part + (warp * kWarpRows + k) * D + (D / 8) * g;
+#pragma unroll
+              for (int i = 0; i < D / 16; i += 2)
+                *reinterpret_cast<float4*>(dst + 2 * i) =
+                    make_float4(S.o[n][i][r], S.o[n][i][2 + r], S.o[n][i + 1][r], S.o[n][i + 1][2 + r]);
+              if (g == 0) pml[warp * kWarpRows + k] = make_float2(S.m[n][r], l);
+            }
+        }
+        __syncthreads();
+        if (frow < rows)
+          for (int w = 0; w < kTileWarps && r0 + w * SPLIT < t.len; ++w) {
+            const float2 ml = pml[w * kWarpRows + frow];
+            float fa, fb;
+            join(FM, ml.x, fa, fb);
+            FL = __fmaf_rn(ml.y, fb, __fmul_rn(FL, fa));
+            for (int d = fd; d < fd + D / 4; ++d)
+              tot[frow * D + d] = __fmaf_rn(part[(w * kWarpRows + frow) * D + d], fb, __fmul_rn(tot[frow * D + d], fa));
+          }
+        __syncthreads();  // the partial results are read: the rings may be refilled
+      }
+      __syncthreads();
+      if (frow < rows) {
+        uint16_t* dst = out + ((int64_t)(t.first + frow / G) * Hq + kh * G + frow % G) * D + fd;
+        for (int d = 0; d < D / 4; d += D / 8) {
+          float x[D / 8];
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) x[i] = tot[frow * D + fd + d + i];
+          store_row<D>(dst + d, x, FL);
+        }
+      }
     }
+    __syncthreads();  // shared memory is free for the next tile
   }
 }
 

@@ -313,6 +313,12 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
 constexpr unsigned kFullMask = 0xFFFFFFFFu;
 
 // Self-test of the bounded wait: one thread waits on an mbarrier that nothing

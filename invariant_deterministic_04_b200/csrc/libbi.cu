@@ -242,10 +242,10 @@ struct Q8Call {
   cudaStream_t st;
 };
 
-template <int KIND, int D, int RH>
+template <int KIND, int D, int NT>
 cudaError_t q8_split(const Q8Call& a, const AttnWs& ws) {
   namespace a8 = bi::attnq8;
-  auto kernel = a8::split_kernel<KIND, D, RH>;
+  auto kernel = a8::split_kernel<KIND, D, NT>;
   struct Tag {};  // one set of once-flags per instantiation
   int per_sm = 0;
   const cudaError_t e = resident_ctas<Tag>(kernel, a8::kWarps * 32, a8::Ring<D>::SMEM, a.dev, &per_sm);
@@ -274,12 +274,18 @@ cudaError_t q8_decode(const Q8Call& a, const AttnWs& ws) {
 template <int KIND, int D>
 cudaError_t q8_prefill(const Q8Call& a, bi::attnq8::Tile* tiles, int32_t* count) {
   namespace a8 = bi::attnq8;
-  cudaError_t e = bi::launch_pdl(a8::plan_kernel, dim3(1), dim3(1024), 0, a.st, a.R, a.rows, 16 / (a.Hq / a.Hkv), tiles,
-                                 count);
+  auto kernel = a8::tile_kernel<KIND, D>;
+  struct Tag {};  // one set of once-flags per instantiation
+  int per_sm = 0;
+  cudaError_t e = resident_ctas<Tag>(kernel, a8::kTileWarps * 32, a8::TileSmem<D>::BYTES, a.dev, &per_sm);
   if (e != cudaSuccess) return e;
-  return bi::launch_pdl(a8::tile_kernel<KIND, D>, dim3((unsigned)(a.sms * 3)), dim3(a8::kTileWarps * 32),
-                        (size_t)a8::tile_smem_bytes<D>(), a.st, a.q, a.ldq, a.Hq, a.Hkv, a.C, a.R,
-                        (const a8::Tile*)tiles, (const int32_t*)count, a.out, a.c);
+  e = bi::launch_pdl(a8::plan_kernel, dim3(1), dim3(1024), 0, a.st, a.R, a.rows, a8::kTileRows / (a.Hq / a.Hkv), tiles,
+                     count);
+  if (e != cudaSuccess) return e;
+  const int64_t most = (int64_t)a.rows * a.Hkv, full = (int64_t)a.sms * per_sm;
+  return bi::launch_pdl(kernel, dim3((unsigned)(most < full ? most : full)), dim3(a8::kTileWarps * 32),
+                        (size_t)a8::TileSmem<D>::BYTES, a.st, a.q, a.ldq, a.Hq, a.Hkv, a.C, a.R, (const a8::Tile*)tiles,
+                        (const int32_t*)count, a.out, a.c);
 }
 
 // ---- LM head workspace: bf16 logits [M, V], fp32 logits [M, V], flagged list [M + 1],

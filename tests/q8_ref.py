@@ -87,10 +87,11 @@ def page_table(lens, max_pages, seed=0, spare=3):
 def attend(q, k, v, scale, sv=None):
     """Row softmax(scale q.k) v in float64: q [Hq, D], k, v [Hkv, n, D] -> (out, sum p |v|), [Hq, D] each.
 
-    With sv [Hkv, n], the value rows' scales, the second result has 2^-29 max_t(p_t sv_t) sum_t |v_t / sv_t|
+    With sv [Hkv, n], the value rows' scales, the second result has 2^-22 max_t(p_t sv_t) sum_t |v_t / sv_t|
     added: 2^-10 of that (the factor of assert_attention_close) is what f16's least step can take. A
-    weight 2^14 p_t sv_t / max(p sv) below f16's normal numbers is rounded to a multiple of 2^-24, so it is
-    off by 2^-25 at most, which is 2^-39 max(p sv) of p_t sv_t, once for each stored value v_t / sv_t."""
+    weight is held as 2^7 p_t sv_t / r with r <= max(p sv) (r follows the maximum from below). Below f16's
+    normal numbers that is rounded to a multiple of 2^-24, so it is off by 2^-25 at most, which is
+    2^-32 r <= 2^-32 max(p sv) of p_t sv_t, once for each stored value v_t / sv_t."""
     Hkv, n, D = k.shape
     if n == 0:
         z = np.zeros((q.shape[0], D))
@@ -102,7 +103,7 @@ def attend(q, k, v, scale, sv=None):
     mag = np.einsum("hgn,hnd->hgd", p, np.abs(v))
     if sv is not None:
         top = (p * sv[:, None, :]).max(-1, keepdims=True)                       # [Hkv, G, 1]
-        mag = mag + 2.0 ** -29 * top * np.abs(v / sv[..., None]).sum(1)[:, None, :]
+        mag = mag + 2.0 ** -22 * top * np.abs(v / sv[..., None]).sum(1)[:, None, :]
     return np.einsum("hgn,hnd->hgd", p, v).reshape(q.shape), mag.reshape(q.shape)
 
 
