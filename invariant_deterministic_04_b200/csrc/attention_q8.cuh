@@ -7,8 +7,8 @@
 // so the value scale rides in the exponent, the weights share one range however far apart the
 // rows' scales are, and both sums use the same w_t (an error of log2 sv_t is a common factor of
 // a token's two terms). m follows the running maximum of z lazily: it moves, to the maximum,
-// when that has risen by more than kSlack = 8, so w_t <= 2^8 and most pages need neither a
-// reduction over lanes nor a rescaling of the sums.
+// when that has risen by more than 8, so w_t <= 2^8 and most pages need neither a reduction
+// over lanes nor a rescaling of the sums.
 //
 // The products run on mma.sync m16n8k16 (f16 operands, fp32 sums), keys and values as the
 // 16-row operand, 8 query rows as the other: scores^T = K Q^T, out^T = V^T W^T. Decode has 1 to
@@ -33,6 +33,7 @@
 #pragma once
 
 #include "attention.cuh"
+#include "gemm.cuh"
 #include "kv_q8.cuh"
 
 namespace bi {
@@ -84,6 +85,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t
       "%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// d = A B.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
+      "%10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -147,11 +156,13 @@ __device__ __forceinline__ void value_operands(const uint32_t (&x)[4], uint4& a,
   widen<KIND>(__byte_perm(x[2], x[3], 0x7362), b.z, b.w);
 }
 
+constexpr float kLowest = -0x1p127f;  // the reference of a row that has seen nothing: below its scores
+
 // NT tiles of 8 query rows.
 template <int D, int NT>
 struct Query {
   uint32_t b[NT][D / 16][2];
-  float c[NT][2];  // of rows 8 n + 2c, + 1: scale log2(e) / the row's power of two; NaN if the row is not finite
+  float2 c[NT];  // of rows 8 n + 2c, + 1: scale log2(e) / the row's power of two; NaN if the row is not finite
 };
 
 // Loads query row g of tile n (nullptr: zeros). All lanes of the warp call it.
@@ -176,8 +187,7 @@ __device__ __forceinline__ void load_query(Query<D, NT>& Q, int n, const uint16_
   const float up = __uint_as_float((uint32_t)(127 + 14 - (finite ? e : 14)) << 23);
   const float down = __uint_as_float((uint32_t)(127 - 14 + (finite ? e : 14)) << 23);
   const float mine = finite ? __fmul_rn(scale_log2, down) : __uint_as_float(0x7FC00000u);
-  Q.c[n][0] = __shfl_sync(kFullMask, mine, 8 * c);
-  Q.c[n][1] = __shfl_sync(kFullMask, mine, 8 * c + 4);
+  Q.c[n] = make_float2(__shfl_sync(kFullMask, mine, 8 * c), __shfl_sync(kFullMask, mine, 8 * c + 4));
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) {
     // 4 dims: elements 4 (j%4) .. + 3 of the 16 in x[j/4]
@@ -192,13 +202,13 @@ __device__ __forceinline__ void load_query(Query<D, NT>& Q, int n, const uint16_
 // tokens, and 2^7 sum w v over the lane's output dims (o[n][i]: dims 2i | 2i + 1 of rows 2c, 2c+1).
 template <int D, int NT>
 struct State {
-  float m[NT][2], l[NT][2];
+  float2 m[NT], l[NT];
   float o[NT][D / 16][4];
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      m[n][0] = m[n][1] = -INFINITY;
-      l[n][0] = l[n][1] = 0.f;
+      m[n] = make_float2(kLowest, kLowest);
+      l[n] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -212,76 +222,89 @@ struct Tokens {
   float ks[2], lg[2], ri[2];  // key scale; log2 and reciprocal of the value scale
 };
 
-constexpr float kSlack = 8.f;
 
 // Weights of one page from its scores: moves m (and l and o with it) where it must, adds to l,
 // and gives 2^7 w as the operand of the value product. MASKED: query row (n, e) sees the
 // first nv[n][e] tokens only; otherwise all 16. live: tiles that hold query rows.
+// A row whose largest f16 weight exceeds 2^15 moves its reference to its largest score of the
+// page; weights are taken with the reference in hand first, which most pages keep.
 template <int D, int NT, bool MASKED>
 __device__ __forceinline__ void page_weights(const Query<D, NT>& Q, const float (&s)[NT][4], const Tokens& T,
                                              const int (&nv)[NT][2], int g, int live, State<D, NT>& S,
                                              uint32_t (&w)[NT][2]) {
-  float z[NT][4];
+  float2 z[NT][2], p[NT][2];  // [token g | g + 8], pairs of query rows 2c, 2c + 1
   bool over = false;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     if (NT > 1 && n >= live) break;
+    const float2 ref = make_float2(__fsub_rn(7.f, S.m[n].x), __fsub_rn(7.f, S.m[n].y));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int tok = e >> 1, r = e & 1;
-      z[n][e] = __fmaf_rn(s[n][e], __fmul_rn(T.ks[tok], Q.c[n][r]), T.lg[tok]);
-      if (MASKED && g + 8 * tok >= nv[n][r]) z[n][e] = -INFINITY;
-      over |= z[n][e] > __fadd_rn(S.m[n][r], kSlack);
+    for (int t = 0; t < 2; ++t) {
+      z[n][t] = __ffma2_rn(make_float2(s[n][2 * t], s[n][2 * t + 1]), __fmul2_rn(make_float2(T.ks[t], T.ks[t]), Q.c[n]),
+                           make_float2(T.lg[t], T.lg[t]));
+      if (MASKED) {
+        if (g + 8 * t >= nv[n][0]) z[n][t].x = -INFINITY;
+        if (g + 8 * t >= nv[n][1]) z[n][t].y = -INFINITY;
+      }
+      const float2 x = __fadd2_rn(z[n][t], ref);
+      p[n][t] = make_float2(ex2(x.x), ex2(x.y));
+      w[n][t] = pack_f16x2(p[n][t].x, p[n][t].y);
     }
+    const __half2 top = __hmax2(*reinterpret_cast<__half2*>(&w[n][0]), *reinterpret_cast<__half2*>(&w[n][1]));
+    over |= !__hble2(top, __halves2half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800)));  // 2^15
   }
   if (__any_sync(kFullMask, over)) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       if (NT > 1 && n >= live) break;
+      float mx[2] = {fmaxf(z[n][0].x, z[n][1].x), fmaxf(z[n][0].y, z[n][1].y)};
+      float pm[2] = {fmaxf(p[n][0].x, p[n][1].x), fmaxf(p[n][0].y, p[n][1].y)};
+      float al[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float mx = fmaxf(z[n][r], z[n][2 + r]);
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, d));
-        const bool up = mx > __fadd_rn(S.m[n][r], kSlack);
-        const float alpha = up ? ex2(__fsub_rn(S.m[n][r], mx)) : 1.f;  // x * 1 == x: the other rows keep their bits
-        if (up) S.m[n][r] = mx;
-        S.l[n][r] = __fmul_rn(S.l[n][r], alpha);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          S.o[n][i][r] = __fmul_rn(S.o[n][i][r], alpha);
-          S.o[n][i][2 + r] = __fmul_rn(S.o[n][i][2 + r], alpha);
+        for (int d = 4; d < 32; d <<= 1) {
+          mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFullMask, mx[r], d));
+          pm[r] = fmaxf(pm[r], __shfl_xor_sync(kFullMask, pm[r], d));
         }
+        float& m = r ? S.m[n].y : S.m[n].x;
+        const bool up = __half2float(__float2half_rn(pm[r])) > 32768.f;
+        al[r] = up ? ex2(__fsub_rn(m, mx[r])) : 1.f;  // x * 1 == x: the other rows keep their bits
+        if (up) m = mx[r];
+      }
+      const float2 alpha = make_float2(al[0], al[1]);
+      S.l[n] = __fmul2_rn(S.l[n], alpha);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        S.o[n][i][0] = __fmul_rn(S.o[n][i][0], al[0]);
+        S.o[n][i][1] = __fmul_rn(S.o[n][i][1], al[1]);
+        S.o[n][i][2] = __fmul_rn(S.o[n][i][2], al[0]);
+        S.o[n][i][3] = __fmul_rn(S.o[n][i][3], al[1]);
+      }
+      const float2 ref = make_float2(__fsub_rn(7.f, S.m[n].x), __fsub_rn(7.f, S.m[n].y));
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float2 x = __fadd2_rn(z[n][t], ref);
+        p[n][t] = make_float2(ex2(x.x), ex2(x.y));
+        w[n][t] = pack_f16x2(p[n][t].x, p[n][t].y);
       }
     }
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     if (NT > 1 && n >= live) break;
-    float p[4];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float ref = S.m[n][r] == -INFINITY ? 0.f : __fsub_rn(S.m[n][r], 7.f);
-#pragma unroll
-      for (int tok = 0; tok < 2; ++tok) {
-        p[2 * tok + r] = ex2(__fsub_rn(z[n][2 * tok + r], ref));
-        if (!MASKED || g + 8 * tok < nv[n][r]) S.l[n][r] = __fmaf_rn(p[2 * tok + r], T.ri[tok], S.l[n][r]);
+    for (int t = 0; t < 2; ++t) {
+      const float2 l = __ffma2_rn(p[n][t], make_float2(T.ri[t], T.ri[t]), S.l[n]);
+      if (MASKED) {
+        if (g + 8 * t < nv[n][0]) S.l[n].x = l.x;
+        if (g + 8 * t < nv[n][1]) S.l[n].y = l.y;
+      } else {
+        S.l[n] = l;
       }
+      w[n][t] = transpose8x8(w[n][t]);
     }
-    w[n][0] = transpose8x8(pack_f16x2(p[0], p[1]));
-    w[n][1] = transpose8x8(pack_f16x2(p[2], p[3]));
   }
-}
-
-template <int D, int NT>
-__device__ __forceinline__ void weights(const Query<D, NT>& Q, const float (&s)[NT][4], const Tokens& T,
-                                        const int (&nv)[NT][2], int g, int live, State<D, NT>& S,
-                                        uint32_t (&w)[NT][2]) {
-  bool all = true;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) all &= nv[n][0] >= PAGE && nv[n][1] >= PAGE;
-  if (__all_sync(kFullMask, all)) page_weights<D, NT, false>(Q, s, T, nv, g, live, S, w);
-  else page_weights<D, NT, true>(Q, s, T, nv, g, live, S, w);
 }
 
 // The xor tree over a query row's 8 lanes that ends a split.
@@ -291,121 +314,79 @@ __device__ __forceinline__ float row_sum(float l) {
   return l;
 }
 
-// One step of the fold over splits: M and a split's m -> the factors of both sides.
+// One step of the fold over splits: M and a split's m (kLowest at the least) -> the factors of both sides.
 __device__ __forceinline__ void join(float& M, float m, float& a, float& b) {
   const float mn = fmaxf(M, m);
-  const float ref = mn == -INFINITY ? 0.f : mn;
-  a = ex2(__fsub_rn(M, ref));
-  b = ex2(__fsub_rn(m, ref));
+  a = ex2(__fsub_rn(M, mn));
+  b = ex2(__fsub_rn(m, mn));
   M = mn;
 }
 
 // ---------------------------------------------------------------------------
-// Decode: one warp per (row, kv-head, split); the split's partial result goes to the workspace.
-//
-// Bound: HBM (4 (2 D + 8) L Hkv flops-free bytes per row against 4 L Hq D flops). Each lane
-// copies the bytes that it will itself widen into its own places of a ring in shared memory
-// (cp.async, 16 bytes each), kStages pages ahead across item boundaries, so that nothing but
-// the 32 scales of a page crosses lanes and no barrier beyond the warp's is needed; a warp's
-// reads back are contiguous, without bank conflicts.
-
-constexpr int kWarps = 4;
-constexpr int kStages = 4;
-constexpr int kCoarse = 1024;  // entries of the split-count prefix that a CTA keeps
+// A page in shared memory: 16 key rows of D bytes, then 16 value rows, each swizzled as a TMA
+// tile is (16-byte chunk i of row t at chunk i ^ (t % 8) for 128-byte rows, i ^ (t / 2 % 4) for
+// 64-byte rows), and its 16 key and 16 value scales elsewhere. With 128-byte rows a lane's key
+// reads meet one bank conflict in two and its value reads none.
 
 template <int D>
-struct Ring {
-  static constexpr int K_BYTES = PAGE * D;         // [token g | g + 8][64-dim part][lane] 16 bytes
-  static constexpr int V_BYTES = PAGE * D;         // [token of the lane's four][lane] D/8 bytes
-  static constexpr int STAGE = K_BYTES + V_BYTES + 2 * PAGE * 4;  // and the page's scales
-  static constexpr int WARP = kStages * STAGE;
-  static constexpr int SMEM = kWarps * WARP + (kCoarse + 1) * 4;
-};
+constexpr int kPageBytes = 2 * PAGE * D;
+constexpr int kScaleBytes = 2 * PAGE * 4;
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Starts the copies of one page (store rows row0 .. row0 + 15) into a ring stage.
+// Byte offset of 16-byte chunk i of token t's row.
 template <int D>
-__device__ __forceinline__ void copy_page(uint32_t stage, const Cache& C, int64_t row0, int lane) {
-  using T = Ring<D>;
-  const int g = lane >> 2, c = lane & 3;
-  const uint8_t* kp = C.k + (row0 + g) * D + 16 * c;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int v = 0; v < D / 64; ++v)
-      cp_async<16>(stage + ((i * (D / 64) + v) * 32 + lane) * 16, kp + i * 8 * D + 64 * v);
-  const uint8_t* vp = C.v + (row0 + 2 * c) * D + (D / 8) * g;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    cp_async<D / 8>(stage + T::K_BYTES + (i * 32 + lane) * (D / 8), vp + ((i & 1) + (i >> 1) * 8) * D);
-  if (lane < 8)
-    cp_async<16>(stage + T::K_BYTES + T::V_BYTES + 16 * lane, (lane < 4 ? C.ks + row0 : C.vs + row0 - 16) + 4 * lane);
+__device__ __forceinline__ uint32_t chunk_at(int t, int i) {
+  return (uint32_t)(t * D + ((i ^ (D == 128 ? (t & 7) : ((t >> 1) & 3))) << 4));
 }
 
-// Folds the page in a ring stage; `seen` of its tokens exist, query row (n, e) sees nv[n][e].
-template <int KIND, int D, int NT>
-__device__ __forceinline__ void fold_page(const Query<D, NT>& Q, uint32_t stage, const int (&nv)[NT][2], int seen,
-                                          int live, int lane, State<D, NT>& S) {
-  using R = Ring<D>;
+// Folds a page. MASKED: `seen` of its tokens exist, query row (n, e) sees nv[n][e].
+template <int KIND, int D, int NT, bool MASKED>
+__device__ __forceinline__ void fold_page(const Query<D, NT>& Q, uint32_t page, uint32_t scales, const int (&nv)[NT][2],
+                                          int seen, int live, int lane, State<D, NT>& S) {
   const int g = lane >> 2, c = lane & 3;
   float s[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+  const uint32_t k0 = page + chunk_at<D>(g, c);  // chunk c + 4 of a 128-byte row: bit 6 flipped
 #pragma unroll
   for (int v = 0; v < D / 64; ++v) {
-    const uint4 x = ld_shared_v4(stage + (v * 32 + lane) * 16);
-    const uint4 y = ld_shared_v4(stage + ((D / 64 + v) * 32 + lane) * 16);
+    const uint4 x = ld_shared_v4(v ? k0 ^ 64u : k0);
+    const uint4 y = ld_shared_v4((v ? k0 ^ 64u : k0) + 8 * D);
     const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       const uint4 a = key_operand<KIND>(xw[b], yw[b]);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        if (NT == 1 || n < live) mma16816(s[n], a, Q.b[n][4 * v + b][0], Q.b[n][4 * v + b][1]);
+        if (NT == 1 || n < live) {
+          if (v + b == 0) mma16816_first(s[n], a, Q.b[n][0][0], Q.b[n][0][1]);
+          else mma16816(s[n], a, Q.b[n][4 * v + b][0], Q.b[n][4 * v + b][1]);
+        }
     }
   }
   Tokens T;
-  const uint32_t sc = stage + R::K_BYTES + R::V_BYTES + 4 * g;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const float vs = ld_shared_f32(sc + 64 + 32 * t);
-    T.ks[t] = ld_shared_f32(sc + 32 * t);
+    const float vs = ld_shared_f32(scales + 64 + 4 * g + 32 * t);
+    T.ks[t] = ld_shared_f32(scales + 4 * g + 32 * t);
     T.lg[t] = lg2(vs);
     T.ri[t] = rcp(vs);
   }
   uint32_t w[NT][2];
-  weights<D, NT>(Q, s, T, nv, g, live, S, w);
+  page_weights<D, NT, MASKED>(Q, s, T, nv, g, live, S, w);
   uint32_t x[4][D / 32];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t at = stage + R::K_BYTES + (i * 32 + lane) * (D / 8);
+    const int t = 2 * c + (i & 1);
+    const uint32_t at = page + PAGE * D + (i >> 1) * 8 * D;
     if constexpr (D == 128) {
-      const uint4 t = ld_shared_v4(at);
-      x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
+      const uint4 y = ld_shared_v4(at + chunk_at<D>(t, g));
+      x[i][0] = y.x; x[i][1] = y.y; x[i][2] = y.z; x[i][3] = y.w;
     } else {
-      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[i][0]), "=r"(x[i][1]) : "r"(at));
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                   : "=r"(x[i][0]), "=r"(x[i][1])
+                   : "r"(at + chunk_at<D>(t, g >> 1) + 8 * (g & 1)));
     }
-  }
-  if (seen < PAGE) {
+    if (MASKED && t + 8 * (i >> 1) >= seen)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (2 * c + (i & 1) + 8 * (i >> 1) >= seen)
-#pragma unroll
-        for (int u = 0; u < D / 32; ++u) x[i][u] = 0;
+      for (int u = 0; u < D / 32; ++u) x[i][u] = 0;
   }
 #pragma unroll
   for (int u = 0; u < D / 32; ++u) {
@@ -421,22 +402,67 @@ __device__ __forceinline__ void fold_page(const Query<D, NT>& Q, uint32_t stage,
   }
 }
 
+// ---------------------------------------------------------------------------
+// Decode: one warp per (row, kv-head, split); the split's partial result goes to the workspace.
+//
+// Bound: HBM (Hkv (2 D + 8) bytes per token against 4 Hq D flops). Each warp has a ring of
+// kStages pages that one lane fills by TMA (two tiles and two 64-byte scale rows a page), ahead
+// across item boundaries, and widens pages from it. The same ring filled by cp.async, lane by
+// lane, took 0.50 ms for 2.2 GB without any arithmetic; TMA takes that off the warps.
+
+constexpr int kWarps = 4;
+constexpr int kStages = 3;
+constexpr int kCoarse = 512;  // entries of the split-count prefix that a CTA keeps
+
+template <int D>
+struct Ring {
+  static constexpr int SCALES = kWarps * kStages * kPageBytes<D>;
+  static constexpr int BARS = SCALES + kWarps * kStages * kScaleBytes;
+  static constexpr int PREFIX = BARS + kWarps * kStages * 8;
+  static constexpr int SMEM = 1024 + PREFIX + kCoarse * 4;  // pages start on a 1024-byte boundary
+};
+
+// Tensor map of a cache's rows [rows, D] of bytes, loaded a page (16 rows) at a time.
+template <int D>
+inline bool make_page_map(CUtensorMap* map, const void* ptr, int64_t rows) {
+  gemm::EncodeTiledFn enc = gemm::encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)D};
+  cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)PAGE};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // A work item: split s of row r for one kv-head; `page` is page `lane` of it (-1: unusable).
 struct Item {
   int r, s, kh, seen, page;
 };
 
 template <int KIND, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4)
-    split_kernel(const uint16_t* __restrict__ q, int Hq, int Hkv, Cache C, Rows R, int nrows, int max_splits,
+__global__ void __launch_bounds__(kWarps * 32, D * NT == 256 ? 3 : 4)
+    split_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
+                 const uint16_t* __restrict__ q, int Hq, int Hkv, Cache C, Rows R, int nrows, int max_splits,
                  float* __restrict__ po, float2* __restrict__ pml, float scale_log2) {
   using T = Ring<D>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   __shared__ int32_t warp_sum[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int G = Hq / Hkv;
-  int32_t* pre = reinterpret_cast<int32_t*>(smem + kWarps * T::WARP);  // pre[i]: splits of rows below i * per
+  int32_t* pre = reinterpret_cast<int32_t*>(smem + T::PREFIX);  // pre[i]: splits of rows below i * per
+  const uint32_t base_u = smem_u32(smem);
+  const uint32_t ring = base_u + (uint32_t)(warp * kStages * kPageBytes<D>);
+  const uint32_t scales = base_u + (uint32_t)(T::SCALES + warp * kStages * kScaleBytes);
+  const uint32_t bars = base_u + (uint32_t)(T::BARS + warp * kStages * 8);
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
   pdl_wait();  // the caller's inputs are complete from here on
   pdl_trigger();
 
@@ -498,12 +524,12 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4)
     return I;
   };
 
-  const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * T::WARP);
   int item = warp * (int)gridDim.x + (int)blockIdx.x;
   if (item >= total) return;
   Item cur = fetch(item), nxt = cur;
   bool ahead = false;            // the copies have gone on to nxt
-  int pj = 0, issued = 0, used = 0;
+  int pj = 0;
+  uint32_t issued = 0, used = 0, filled = 0, ph_bits = 0;
   // starts the copy of the next page of the item stream, if it is known by now
   auto issue = [&] {
     if (!ahead && pj * PAGE >= cur.seen && item + step < total) {
@@ -514,11 +540,24 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4)
     const Item& I = ahead ? nxt : cur;
     if (pj * PAGE < I.seen) {
       const int pg = __shfl_sync(kFullMask, I.page, pj);
-      if (pg >= 0) copy_page<D>(ring + (uint32_t)(issued % kStages) * T::STAGE, C, ((int64_t)pg * Hkv + I.kh) * PAGE, lane);
+      const uint32_t st = issued % kStages, bar = bars + 8 * st;
+      if (lane == 0) {
+        if (pg >= 0) {
+          const int64_t row0 = ((int64_t)pg * Hkv + I.kh) * PAGE;
+          note_fill(filled, ph_bits, (int)st, (issued / kStages) & 1u);
+          fence_proxy_async_smem();
+          mbar_arrive_expect_tx(bar, kPageBytes<D> + kScaleBytes);
+          tma_load_2d(ring + st * kPageBytes<D>, &km, 0, (int)row0, bar);
+          tma_load_2d(ring + st * kPageBytes<D> + PAGE * D, &vm, 0, (int)row0, bar);
+          bulk_g2s(scales + st * kScaleBytes, C.ks + row0, PAGE * 4, bar);
+          bulk_g2s(scales + st * kScaleBytes + PAGE * 4, C.vs + row0, PAGE * 4, bar);
+        } else {
+          mbar_arrive(bar);
+        }
+      }
       ++pj;
       ++issued;
     }
-    cp_commit();
   };
   for (int i = 0; i < kStages; ++i) issue();
 
@@ -532,27 +571,31 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4)
     State<D, NT> S;
     S.clear();
     for (int j = 0; j * PAGE < cur.seen; ++j) {
-      // with the ring full the oldest copy group is the page wanted; otherwise (the stream's end,
-      // or an item of few pages) wait for all of them
-      if (issued - used == kStages) cp_wait<kStages - 1>();
-      else cp_wait<0>();
-      __syncwarp();
+      const uint32_t st = used % kStages;
+      if (!__all_sync(kFullMask, mbar_wait(bars + 8 * st, (used / kStages) & 1u))) {
+        // a copy never landed (recorded): let the others land, then leave
+        if (lane == 0) drain_copies(bars, 8, filled, ph_bits);
+        __syncwarp();
+        return;
+      }
       if (__shfl_sync(kFullMask, cur.page, j) >= 0) {  // the tokens of an unusable page are not seen
         const int seen = cur.seen - j * PAGE;
         int nv[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) nv[n][0] = nv[n][1] = seen;
-        fold_page<KIND, D, NT>(Q, ring + (uint32_t)(used % kStages) * T::STAGE, nv, seen, NT, lane, S);
+        const uint32_t page = ring + st * kPageBytes<D>, sc = scales + st * kScaleBytes;
+        if (seen >= PAGE) fold_page<KIND, D, NT, false>(Q, page, sc, nv, seen, NT, lane, S);
+        else fold_page<KIND, D, NT, true>(Q, page, sc, nv, seen, NT, lane, S);
       }
       ++used;
-      __syncwarp();  // every lane has read this page's scales: its stage may be refilled
+      __syncwarp();  // every lane has read this page: its stage may be refilled
       issue();
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float l = row_sum(S.l[n][r]);
+        const float l = row_sum(r ? S.l[n].y : S.l[n].x);
         const int head = 8 * n + 2 * c + r;
         if (head >= G) continue;
         const int64_t slot = ((int64_t)cur.r * max_splits + cur.s) * Hq + cur.kh * G + head;
@@ -561,7 +604,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4)
         for (int i = 0; i < D / 16; i += 2)
           *reinterpret_cast<float4*>(dst + 2 * i) =
               make_float4(S.o[n][i][r], S.o[n][i][2 + r], S.o[n][i + 1][r], S.o[n][i + 1][2 + r]);
-        if (g == 0) pml[slot] = make_float2(S.m[n][r], l);
+        if (g == 0) pml[slot] = make_float2(r ? S.m[n].y : S.m[n].x, l);
       }
     if (item + step >= total) break;
     item += step;
@@ -572,7 +615,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4)
       cur = nxt;
       ahead = false;
     }
-    for (int i = issued - used; i < kStages; ++i) issue();  // short items left the ring less than full
+    for (uint32_t i = issued - used; i < kStages; ++i) issue();  // short items left the ring less than full
   }
 }
 
@@ -598,11 +641,11 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
   const int n = attn::num_splits(R, r);
   const int64_t slot0 = (int64_t)r * max_splits * Hq + h;
   const float* src = po + slot0 * D + d0;
-  float M = -INFINITY, L = 0.f, O[DPL];
+  float M = kLowest, L = 0.f, O[DPL];
 #pragma unroll
   for (int d = 0; d < DPL; ++d) O[d] = 0.f;
   for (int s0 = 0; s0 < n; s0 += 32) {
-    const float2 ml = s0 + lane < n ? pml[slot0 + (int64_t)(s0 + lane) * Hq] : make_float2(-INFINITY, 0.f);
+    const float2 ml = s0 + lane < n ? pml[slot0 + (int64_t)(s0 + lane) * Hq] : make_float2(kLowest, 0.f);
     float top = ml.x;  // the running maximum up to and with this lane's split
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -731,6 +774,28 @@ constexpr int kNT = 2;  // tiles of 8 query rows per warp
 constexpr int kWarpRows = 8 * kNT;
 constexpr int kTileRows = kTileWarps * kWarpRows;
 
+// cp.async of one page (store rows row0 .. + 15) by a warp, 16 contiguous bytes a lane.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <int D>
+__device__ __forceinline__ void copy_page(uint32_t page, uint32_t scales, const Cache& C, int64_t row0, int lane) {
+#pragma unroll
+  for (int i = 0; i < PAGE * D / 512; ++i) {
+    const int at = i * 32 + lane, t = at / (D / 16), chunk = at % (D / 16);
+    cp_async16(page + chunk_at<D>(t, chunk), C.k + row0 * D + at * 16);
+    cp_async16(page + PAGE * D + chunk_at<D>(t, chunk), C.v + row0 * D + at * 16);
+  }
+  if (lane < 8) cp_async16(scales + 16 * lane, (lane < 4 ? C.ks + row0 : C.vs + row0 - PAGE) + 4 * lane);
+}
+
+constexpr int kTileStages = 4;
+
 template <int D>
 struct TileSmem {
   static constexpr int PAGES = 256 / D;                   // pages a chunk: one item of each kind per warp
@@ -738,7 +803,8 @@ struct TileSmem {
   static constexpr int BUFFER = OPERANDS + PAGES * PAGE * 16;  // and {ks, log2 vs, 1 / vs, -} per token
   static constexpr int TOTALS = kTileRows * D * 4;
   // few rows: the rings, over which the four splits' partial results go, and the totals
-  static constexpr int RINGS = kTileWarps * Ring<D>::WARP;
+  static constexpr int STAGE = kPageBytes<D> + kScaleBytes;
+  static constexpr int RINGS = kTileWarps * kTileStages * STAGE;
   static constexpr int PARTIALS = kTileWarps * kWarpRows * D * 4;
   static constexpr int SMALL = (RINGS > PARTIALS ? RINGS : PARTIALS) + kTileWarps * kWarpRows * 8 + kWarpRows * D * 4;
   static constexpr int LARGE = 2 * BUFFER + TOTALS;
@@ -827,23 +893,22 @@ __device__ __forceinline__ void store_chunk(const Raw& X, uint32_t buf, int warp
 }
 
 // Folds one page of a buffer.
-template <int D>
+template <int D, bool MASKED>
 __device__ __forceinline__ void fold_wide(const Query<D, kNT>& Q, uint32_t buf, int page, const int (&nv)[kNT][2],
                                           int live, int lane, State<D, kNT>& S) {
   using M = TileSmem<D>;
   const int g = lane >> 2;
   float s[kNT][4];
-#pragma unroll
-  for (int n = 0; n < kNT; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
   const uint32_t kb = buf + (page * (D / 16) * 32 + lane) * 16, vb = kb + M::OPERANDS / 2;
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) {
     const uint4 a = ld_shared_v4(kb + j * 512);
 #pragma unroll
     for (int n = 0; n < kNT; ++n)
-      if (n < live) mma16816(s[n], a, Q.b[n][j][0], Q.b[n][j][1]);
+      if (n < live) {
+        if (j == 0) mma16816_first(s[n], a, Q.b[n][0][0], Q.b[n][0][1]);
+        else mma16816(s[n], a, Q.b[n][j][0], Q.b[n][j][1]);
+      }
   }
   Tokens T;
 #pragma unroll
@@ -854,7 +919,7 @@ __device__ __forceinline__ void fold_wide(const Query<D, kNT>& Q, uint32_t buf, 
     T.ri[t] = __uint_as_float(x.z);
   }
   uint32_t w[kNT][2];
-  weights<D, kNT>(Q, s, T, nv, g, live, S, w);
+  page_weights<D, kNT, MASKED>(Q, s, T, nv, g, live, S, w);
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
     const uint4 a = ld_shared_v4(vb + i * 512);
@@ -883,7 +948,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 2)
                 const Tile* __restrict__ tiles, const int32_t* __restrict__ count, uint16_t* __restrict__ out,
                 float scale_log2) {
   using M = TileSmem<D>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int G = Hq / Hkv;
@@ -901,7 +966,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 2)
     const int live = min(kNT, (rows - i0 + 7) / 8);               // its tiles that hold rows (<= 0: none)
     Query<D, kNT> Q;
     int len[kNT][2];
-    int longest = 0;
+    int longest = 0, shortest = INT_MAX / 2;
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
       const int i = i0 + 8 * n + g;
@@ -913,14 +978,16 @@ __global__ void __launch_bounds__(kTileWarps * 32, 2)
         int pt_row;
         len[n][r] = k < rows ? attn::row_len(R, t.first + k / G, pt_row) : INT_MAX / 2;  // no row: nothing to mask
         if (k < rows) longest = max(longest, len[n][r]);
+        shortest = min(shortest, len[n][r]);
       }
     }
     longest = __reduce_max_sync(kFullMask, longest);
+    shortest = __reduce_min_sync(kFullMask, shortest);
     const int32_t* prow = C.pt + (int64_t)t.pt_row * R.max_pages;
     float Mx[kNT][2], L[kNT][2];
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
-      Mx[n][0] = Mx[n][1] = -INFINITY;
+      Mx[n][0] = Mx[n][1] = kLowest;
       L[n][0] = L[n][1] = 0.f;
     }
     if (!small) {
@@ -945,7 +1012,8 @@ __global__ void __launch_bounds__(kTileWarps * 32, 2)
             for (int n = 0; n < kNT; ++n)
 #pragma unroll
               for (int r = 0; r < 2; ++r) nv[n][r] = len[n][r] - tp - p * PAGE;
-            fold_wide<D>(Q, buf, p, nv, live, lane, S);
+            if (tp + p * PAGE + PAGE <= shortest) fold_wide<D, false>(Q, buf, p, nv, live, lane, S);
+            else fold_wide<D, true>(Q, buf, p, nv, live, lane, S);
           }
         }
 #pragma unroll
@@ -953,8 +1021,8 @@ __global__ void __launch_bounds__(kTileWarps * 32, 2)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             float fa, fb;
-            const float l = row_sum(S.l[n][r]);
-            join(Mx[n][r], S.m[n][r], fa, fb);
+            const float l = row_sum(r ? S.l[n].y : S.l[n].x);
+            join(Mx[n][r], r ? S.m[n].y : S.m[n].x, fa, fb);
             L[n][r] = __fmaf_rn(l, fb, __fmul_rn(L[n][r], fa));
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
@@ -978,7 +1046,8 @@ __global__ void __launch_bounds__(kTileWarps * 32, 2)
         }
     } else {
       // four splits at a time, one a warp; then row k's thread group folds them in order
-      const uint32_t ring = base + (uint32_t)(warp * Ring<D>::WARP);
+      const uint32_t ring = base + (uint32_t)(warp * kTileStages * kPageBytes<D>);
+      const uint32_t scales = base + (uint32_t)(kTileWarps * kTileStages * kPageBytes<D> + warp * kTileStages * kScaleBytes);
       float* part = reinterpret_cast<float*>(smem);                                  // [warp][row][D]
       constexpr int OVER = M::RINGS > M::PARTIALS ? M::RINGS : M::PARTIALS;
       float2* pml = reinterpret_cast<float2*>(smem + OVER);                          // [warp][row]
@@ -986,7 +1055,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 2)
       for (int i = threadIdx.x; i < rows * D; i += kTileWarps * 32) tot[i] = 0.f;
       // thread -> (row, quarter of D) for the folds
       const int frow = threadIdx.x >> 2, fd = (threadIdx.x & 3) * (D / 4);
-      float FM = -INFINITY, FL = 0.f;
+      float FM = kLowest, FL = 0.f;
       for (int r0 = 0; r0 < t.len; r0 += kTileWarps * SPLIT) {
         const int t0 = r0 + warp * SPLIT, seen = min(SPLIT, t.len - t0);
         State<D, kNT> S;
@@ -1000,13 +1069,15 @@ __global__ void __launch_bounds__(kTileWarps * 32, 2)
         auto issue = [&](int j) {
           if (j < np) {
             const int pg = __shfl_sync(kFullMask, page, j);
-            if (pg >= 0) copy_page<D>(ring + (uint32_t)(j % kStages) * Ring<D>::STAGE, C, ((int64_t)pg * Hkv + kh) * PAGE, lane);
+            const uint32_t st = (uint32_t)(j % kTileStages);
+            if (pg >= 0)
+              copy_page<D>(ring + st * kPageBytes<D>, scales + st * kScaleBytes, C, ((int64_t)pg * Hkv + kh) * PAGE, lane);
           }
           cp_commit();
         };
-        for (int j = 0; j < kStages; ++j) issue(j);
+        for (int j = 0; j < kTileStages; ++j) issue(j);
         for (int j = 0; j < np; ++j) {
-          cp_wait<kStages - 1>();
+          cp_wait<kTileStages - 1>();
           __syncwarp();
           if (__shfl_sync(kFullMask, page, j) >= 0) {
             const int tp = t0 + j * PAGE;
@@ -1015,10 +1086,12 @@ __global__ void __launch_bounds__(kTileWarps * 32, 2)
             for (int n = 0; n < kNT; ++n)
 #pragma unroll
               for (int r = 0; r < 2; ++r) nv[n][r] = len[n][r] - tp;
-            fold_page<KIND, D, kNT>(Q, ring + (uint32_t)(j % kStages) * Ring<D>::STAGE, nv, t.len - tp, live, lane, S);
+            const uint32_t st = (uint32_t)(j % kTileStages), pg = ring + st * kPageBytes<D>, sc = scales + st * kScaleBytes;
+            if (tp + PAGE <= shortest) fold_page<KIND, D, kNT, false>(Q, pg, sc, nv, PAGE, live, lane, S);
+            else fold_page<KIND, D, kNT, true>(Q, pg, sc, nv, t.len - tp, live, lane, S);
           }
           __syncwarp();
-          issue(j + kStages);
+          issue(j + kTileStages);
         }
         cp_wait<0>();
         __syncthreads();  // the rings are free (and the totals cleared, or the last fold done)
@@ -1027,7 +1100,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 2)
           for (int n = 0; n < kNT; ++n)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const float l = row_sum(S.l[n][r]);
+              const float l = row_sum(r ? S.l[n].y : S.l[n].x);
               const int k = 8 * n + 2 * c + r;
               if (k >= rows) continue;
               float* dst = part + (warp * kWarpRows + k) * D + (D / 8) * g;
@@ -1035,7 +1108,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 2)
               for (int i = 0; i < D / 16; i += 2)
                 *reinterpret_cast<float4*>(dst + 2 * i) =
                     make_float4(S.o[n][i][r], S.o[n][i][2 + r], S.o[n][i + 1][r], S.o[n][i + 1][2 + r]);
-              if (g == 0) pml[warp * kWarpRows + k] = make_float2(S.m[n][r], l);
+              if (g == 0) pml[warp * kWarpRows + k] = make_float2(r ? S.m[n].y : S.m[n].x, l);
             }
         }
         __syncthreads();

@@ -192,7 +192,9 @@ bi_status attention_common(const uint16_t* q, int64_t ldq, const uint16_t* kc, c
 bi_status store_check(const void* kc, const void* vc, const float* ks, const float* vs, int kind, int64_t num_pages,
                       int max_pages, int Hkv, int D) {
   if (num_pages <= 0 || max_pages <= 0 || Hkv <= 0 || D <= 0) return BI_ERR_SHAPE;
-  if (num_pages > (int64_t(1) << 31) || max_pages > INT_MAX / BI_PAGE_TOKENS) return BI_ERR_SHAPE;
+  if (max_pages > INT_MAX / BI_PAGE_TOKENS) return BI_ERR_SHAPE;
+  // store rows are counted in 31 bits (a TMA coordinate)
+  if (num_pages > INT_MAX / BI_PAGE_TOKENS / (int64_t)Hkv) return BI_ERR_SHAPE;
   if ((kind != BI_KV_INT8 && kind != BI_KV_E4M3) || (D != 64 && D != 128)) return BI_ERR_UNSUPPORTED;
   if (!aligned16(kc) || !aligned16(vc) || !aligned16(ks) || !aligned16(vs)) return BI_ERR_ALIGN;
   return BI_OK;
@@ -250,12 +252,16 @@ cudaError_t q8_split(const Q8Call& a, const AttnWs& ws) {
   int per_sm = 0;
   const cudaError_t e = resident_ctas<Tag>(kernel, a8::kWarps * 32, a8::Ring<D>::SMEM, a.dev, &per_sm);
   if (e != cudaSuccess) return e;
+  CUtensorMap km, vm;
+  const int64_t store_rows = a.C.num_pages * a.Hkv * BI_PAGE_TOKENS;
+  if (!a8::make_page_map<D>(&km, a.C.k, store_rows) || !a8::make_page_map<D>(&vm, a.C.v, store_rows))
+    return cudaErrorInvalidValue;
   // no more CTAs than there can be items
   const int ms = max_splits(a.R.max_pages);
   const int64_t ctas = ((int64_t)a.rows * ms * a.Hkv + a8::kWarps - 1) / a8::kWarps;
   const int64_t full = (int64_t)a.sms * per_sm;
   return bi::launch_pdl(kernel, dim3((unsigned)(ctas < full ? ctas : full)), dim3(a8::kWarps * 32),
-                        (size_t)a8::Ring<D>::SMEM, a.st, a.q, a.Hq, a.Hkv, a.C, a.R, a.rows, ms, ws.po, ws.pml, a.c);
+                        (size_t)a8::Ring<D>::SMEM, a.st, km, vm, a.q, a.Hq, a.Hkv, a.C, a.R, a.rows, ms, ws.po, ws.pml, a.c);
 }
 
 template <int KIND, int D>
