@@ -133,6 +133,32 @@ def _on(device, stream):
                 yield
 
 
+_NO_SWITCH = contextlib.nullcontext()
+_raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch_on(device, stream):
+    """_on, or nothing to enter where the tensors' device is current and no stream was given."""
+    if stream is None and device.index is not None and torch.cuda.current_device() == device.index:
+        return _NO_SWITCH
+    return _on(device, stream)
+
+
+def _stream_of(device):
+    """The handle of the current stream of the tensors' device."""
+    if _raw_stream_of is not None and device.index is not None:
+        return _raw_stream_of(device.index)
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _need(t, dtype, name: str, dims: int):
+    """_req and _contig in one look."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == dims and t.is_contiguous():
+        return
+    _req(t, dtype, name, dims)
+    _contig(t, name)
+
+
 def _same_device(first: torch.Tensor, *others):
     """The device of `first`; every other tensor given (None entries skipped) must be on it."""
     d = first.device
@@ -465,14 +491,11 @@ def _store_q8(k_cache, v_cache, k_scale, v_scale, page_table):
     """Check an 8-bit store; returns (num_pages, Hkv, D, kind)."""
     if not isinstance(k_cache, torch.Tensor) or k_cache.dtype not in _KV_KINDS:
         raise TypeError("k_cache must be a CUDA tensor of torch.int8 or torch.float8_e4m3fn")
-    _req(k_cache, k_cache.dtype, "k_cache", 4)
-    _req(v_cache, k_cache.dtype, "v_cache", 4)
-    _req(k_scale, torch.float32, "k_scale", 3)
-    _req(v_scale, torch.float32, "v_scale", 3)
-    _req(page_table, torch.int32, "page_table", 2)
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale"),
-                 (page_table, "page_table")):
-        _contig(t, n)
+    _need(k_cache, k_cache.dtype, "k_cache", 4)
+    _need(v_cache, k_cache.dtype, "v_cache", 4)
+    _need(k_scale, torch.float32, "k_scale", 3)
+    _need(v_scale, torch.float32, "v_scale", 3)
+    _need(page_table, torch.int32, "page_table", 2)
     num_pages, Hkv, P, D = k_cache.shape
     if v_cache.shape != k_cache.shape or P != PAGE_TOKENS:
         raise ValueError("k_cache/v_cache must be [num_pages, Hkv, 16, D]")
@@ -482,11 +505,10 @@ def _store_q8(k_cache, v_cache, k_scale, v_scale, page_table):
 
 
 def _row_ids(q_seq, q_pos, T: int):
-    for t, n in ((q_seq, "q_seq"), (q_pos, "q_pos")):
-        _req(t, torch.int32, n, 1)
-        _contig(t, n)
-        if t.shape[0] != T:
-            raise ValueError("q_seq and q_pos need one entry per row")
+    _need(q_seq, torch.int32, "q_seq", 1)
+    _need(q_pos, torch.int32, "q_pos", 1)
+    if q_seq.shape[0] != T or q_pos.shape[0] != T:
+        raise ValueError("q_seq and q_pos need one entry per row")
 
 
 def kv_append_q8(k_new, v_new, q_seq, q_pos, k_cache, v_cache, k_scale, v_scale, page_table, stream=None):
@@ -508,11 +530,11 @@ def kv_append_q8(k_new, v_new, q_seq, q_pos, k_cache, v_cache, k_scale, v_scale,
     device = _same_device(k_new, v_new, q_seq, q_pos, k_cache, v_cache, k_scale, v_scale, page_table)
     if T == 0:  # empty tensors have no address to pass on
         return
-    with _on(device, stream):
+    with _launch_on(device, stream):
         _check("bi_kv_append_q8", lib().bi_kv_append_q8(
-            _ptr(k_new), _ptr(v_new), ld, _ptr(q_seq), _ptr(q_pos), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-            _ptr(v_scale), kind, num_pages, _ptr(page_table), page_table.shape[0], page_table.shape[1], T, Hkv, D,
-            _stream()))
+            k_new.data_ptr(), v_new.data_ptr(), ld, q_seq.data_ptr(), q_pos.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), kind, num_pages, page_table.data_ptr(), page_table.shape[0], page_table.shape[1], T, Hkv, D,
+            _stream_of(device)))
 
 
 def kv_read_q8(q_seq, q_pos, k_cache, v_cache, k_scale, v_scale, page_table, k_out=None, v_out=None, stream=None):
@@ -533,16 +555,16 @@ def kv_read_q8(q_seq, q_pos, k_cache, v_cache, k_scale, v_scale, page_table, k_o
         if _rows3(v_out, "v_out") != ld:
             raise ValueError("k_out and v_out must have the same row stride")
     device = _same_device(k_cache, v_cache, k_scale, v_scale, page_table, q_seq, q_pos, k_out, v_out)
-    with _on(device, stream):
+    with _launch_on(device, stream):
         if k_out is None:
             k_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=device)
             v_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=device)
         if T == 0:
             return k_out, v_out
         _check("bi_kv_read_q8", lib().bi_kv_read_q8(
-            _ptr(k_out), _ptr(v_out), ld, _ptr(q_seq), _ptr(q_pos), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-            _ptr(v_scale), kind, num_pages, _ptr(page_table), page_table.shape[0], page_table.shape[1], T, Hkv, D,
-            _stream()))
+            k_out.data_ptr(), v_out.data_ptr(), ld, q_seq.data_ptr(), q_pos.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), kind, num_pages, page_table.data_ptr(), page_table.shape[0], page_table.shape[1], T, Hkv, D,
+            _stream_of(device)))
     return k_out, v_out
 
 
@@ -552,10 +574,8 @@ def attention_decode_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_l
 
     workspace: at least attention_workspace_size(B, Hq, D, page_table.shape[1]) bytes."""
     num_pages, Hkv, Dc, kind = _store_q8(k_cache, v_cache, k_scale, v_scale, page_table)
-    _req(q, torch.bfloat16, "q", 3)
-    _req(seq_lens, torch.int32, "seq_lens", 1)
-    _contig(q, "q")
-    _contig(seq_lens, "seq_lens")
+    _need(q, torch.bfloat16, "q", 3)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
     B, Hq, D = q.shape
     if D != Dc:
         raise ValueError(f"q has heads of {D} dims, the store of {Dc}")
@@ -567,14 +587,14 @@ def attention_decode_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_l
     if out is not None:
         _out(out, torch.bfloat16, (B, Hq, D), "out")
     _check_workspace(workspace)
-    with _on(device, stream):
+    with _launch_on(device, stream):
         out = torch.empty_like(q) if out is None else out
         if B == 0:
             return out
         ws, nbytes = _workspace(attention_workspace_size(B, Hq, D, maxp), device, workspace)
         _check("bi_attention_decode_q8", lib().bi_attention_decode_q8(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kind, num_pages, _ptr(page_table),
-            maxp, _ptr(seq_lens), _ptr(out), B, Hq, Hkv, D, scale, _ptr(ws), nbytes, _stream()))
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), kind, num_pages, page_table.data_ptr(),
+            maxp, seq_lens.data_ptr(), out.data_ptr(), B, Hq, Hkv, D, scale, ws.data_ptr(), nbytes, _stream_of(device)))
     return out
 
 
@@ -602,15 +622,15 @@ def attention_prefill_q8(q, q_seq, q_pos, k_cache, v_cache, k_scale, v_scale, pa
     if out is not None:
         _out(out, torch.bfloat16, (T, Hq, D), "out")
     _check_workspace(workspace)
-    with _on(device, stream):
+    with _launch_on(device, stream):
         out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=device) if out is None else out
         if T == 0:
             return out
         ws, nbytes = _workspace(attention_prefill_q8_workspace_size(T), device, workspace)
         _check("bi_attention_prefill_q8", lib().bi_attention_prefill_q8(
-            _ptr(q), ldq, _ptr(q_seq), _ptr(q_pos), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kind,
-            num_pages, _ptr(page_table), num_seqs, maxp, _ptr(out), T, Hq, Hkv, D, scale, _ptr(ws), nbytes,
-            _stream()))
+            q.data_ptr(), ldq, q_seq.data_ptr(), q_pos.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), kind,
+            num_pages, page_table.data_ptr(), num_seqs, maxp, out.data_ptr(), T, Hq, Hkv, D, scale, ws.data_ptr(), nbytes,
+            _stream_of(device)))
     return out
 
 
@@ -620,16 +640,16 @@ def qk_norm_rope(q, k, q_weight, k_weight, pos, cos_sin, eps: float = 1e-6, q_ou
     q_weight, k_weight bf16 [D]; cos_sin fp32 [max_pos, D/2, 2]. Returns (q, k) as written."""
     _req(q, torch.bfloat16, "q", 3)
     _req(k, torch.bfloat16, "k", 3)
-    _req(pos, torch.int32, "pos", 1)
-    _req(cos_sin, torch.float32, "cos_sin", 3)
+    _need(pos, torch.int32, "pos", 1)
+    _need(cos_sin, torch.float32, "cos_sin", 3)
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     if k.shape[0] != T or k.shape[2] != D:
         raise ValueError("q and k must be [T, Hq, D] and [T, Hkv, D]")
     for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        _out(t, torch.bfloat16, (D,), n)
-    _contig(pos, "pos")
-    _contig(cos_sin, "cos_sin")
+        _need(t, torch.bfloat16, n, 1)
+        if t.shape[0] != D:
+            raise ValueError(f"{n} must have shape {(D,)}, got {tuple(t.shape)}")
     if cos_sin.shape[1:] != (D // 2, 2):
         raise ValueError("cos_sin must be [max_pos, D/2, 2]")
     if pos.shape != (T,):
@@ -643,11 +663,11 @@ def qk_norm_rope(q, k, q_weight, k_weight, pos, cos_sin, eps: float = 1e-6, q_ou
     device = _same_device(q, k, q_weight, k_weight, pos, cos_sin, q_out, k_out)
     if T == 0:
         return q_out, k_out
-    with _on(device, stream):
+    with _launch_on(device, stream):
         _check("bi_qk_norm_rope", lib().bi_qk_norm_rope(
-            _ptr(q), _rows3(q, "q"), _ptr(k), _rows3(k, "k"), _ptr(q_weight), _ptr(k_weight), _ptr(pos),
-            _ptr(cos_sin), cos_sin.shape[0], eps, _ptr(q_out), _rows3(q_out, "q_out"), _ptr(k_out),
-            _rows3(k_out, "k_out"), T, Hq, Hkv, D, _stream()))
+            q.data_ptr(), _rows3(q, "q"), k.data_ptr(), _rows3(k, "k"), q_weight.data_ptr(), k_weight.data_ptr(), pos.data_ptr(),
+            cos_sin.data_ptr(), cos_sin.shape[0], eps, q_out.data_ptr(), _rows3(q_out, "q_out"), k_out.data_ptr(),
+            _rows3(k_out, "k_out"), T, Hq, Hkv, D, _stream_of(device)))
     return q_out, k_out
 
 
