@@ -223,87 +223,76 @@ struct Tokens {
 };
 
 
-// Weights of one page from its scores: moves m (and l and o with it) where it must, adds to l,
-// and gives 2^7 w as the operand of the value product. MASKED: query row (n, e) sees the
-// first nv[n][e] tokens only; otherwise all 16. live: tiles that hold query rows.
-// A row whose largest f16 weight exceeds 2^15 moves its reference to its largest score of the
-// page; weights are taken with the reference in hand first, which most pages keep.
+// Weights of one page for one tile of 8 query rows, from its scores: moves m (and l and o with
+// it) where it must, adds to l, and gives 2^7 w as the operand of the value product. MASKED:
+// query row e of the lane sees the first nv[e] tokens only; otherwise all 16. A row whose largest
+// f16 weight exceeds 2^15 moves its reference to its largest score of the page; weights are
+// taken with the reference in hand first, which most pages keep.
+template <int D, bool MASKED>
+__device__ __forceinline__ void tile_weights(const float2& qc, const float (&s)[4], const Tokens& T, const int (&nv)[2],
+                                             int g, float2& m, float2& l, float (&o)[D / 16][4], uint32_t (&w)[2]) {
+  float2 z[2], p[2];  // token g | g + 8, pairs of query rows 2c, 2c + 1
+  float2 ref = make_float2(__fsub_rn(7.f, m.x), __fsub_rn(7.f, m.y));
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    z[t] = __ffma2_rn(make_float2(s[2 * t], s[2 * t + 1]), __fmul2_rn(make_float2(T.ks[t], T.ks[t]), qc),
+                      make_float2(T.lg[t], T.lg[t]));
+    if (MASKED) {
+      if (g + 8 * t >= nv[0]) z[t].x = -INFINITY;
+      if (g + 8 * t >= nv[1]) z[t].y = -INFINITY;
+    }
+    const float2 x = __fadd2_rn(z[t], ref);
+    p[t] = make_float2(ex2(x.x), ex2(x.y));
+    w[t] = pack_f16x2(p[t].x, p[t].y);
+  }
+  const __half2 top = __hmax2(*reinterpret_cast<__half2*>(&w[0]), *reinterpret_cast<__half2*>(&w[1]));
+  const bool over = !__hble2(top, __halves2half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800)));  // 2^15
+  if (__any_sync(kFullMask, over)) {
+    float mx[2] = {fmaxf(z[0].x, z[1].x), fmaxf(z[0].y, z[1].y)};
+    float pm[2] = {fmaxf(p[0].x, p[1].x), fmaxf(p[0].y, p[1].y)};
+    float al[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFullMask, mx[r], d));
+        pm[r] = fmaxf(pm[r], __shfl_xor_sync(kFullMask, pm[r], d));
+      }
+      float& mr = r ? m.y : m.x;
+      const bool up = __half2float(__float2half_rn(pm[r])) > 32768.f;
+      al[r] = up ? ex2(__fsub_rn(mr, mx[r])) : 1.f;  // x * 1 == x: the other rows keep their bits
+      if (up) mr = mx[r];
+    }
+    l = __fmul2_rn(l, make_float2(al[0], al[1]));
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = __fmul_rn(o[i][e], al[e & 1]);
+    ref = make_float2(__fsub_rn(7.f, m.x), __fsub_rn(7.f, m.y));
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const float2 x = __fadd2_rn(z[t], ref);
+      p[t] = make_float2(ex2(x.x), ex2(x.y));
+      w[t] = pack_f16x2(p[t].x, p[t].y);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const float2 x = __ffma2_rn(p[t], make_float2(T.ri[t], T.ri[t]), l);
+    if (!MASKED || g + 8 * t < nv[0]) l.x = x.x;
+    if (!MASKED || g + 8 * t < nv[1]) l.y = x.y;
+    w[t] = transpose8x8(w[t]);
+  }
+}
+
 template <int D, int NT, bool MASKED>
 __device__ __forceinline__ void page_weights(const Query<D, NT>& Q, const float (&s)[NT][4], const Tokens& T,
                                              const int (&nv)[NT][2], int g, int live, State<D, NT>& S,
                                              uint32_t (&w)[NT][2]) {
-  float2 z[NT][2], p[NT][2];  // [token g | g + 8], pairs of query rows 2c, 2c + 1
-  bool over = false;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     if (NT > 1 && n >= live) break;
-    const float2 ref = make_float2(__fsub_rn(7.f, S.m[n].x), __fsub_rn(7.f, S.m[n].y));
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      z[n][t] = __ffma2_rn(make_float2(s[n][2 * t], s[n][2 * t + 1]), __fmul2_rn(make_float2(T.ks[t], T.ks[t]), Q.c[n]),
-                           make_float2(T.lg[t], T.lg[t]));
-      if (MASKED) {
-        if (g + 8 * t >= nv[n][0]) z[n][t].x = -INFINITY;
-        if (g + 8 * t >= nv[n][1]) z[n][t].y = -INFINITY;
-      }
-      const float2 x = __fadd2_rn(z[n][t], ref);
-      p[n][t] = make_float2(ex2(x.x), ex2(x.y));
-      w[n][t] = pack_f16x2(p[n][t].x, p[n][t].y);
-    }
-    const __half2 top = __hmax2(*reinterpret_cast<__half2*>(&w[n][0]), *reinterpret_cast<__half2*>(&w[n][1]));
-    over |= !__hble2(top, __halves2half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800)));  // 2^15
-  }
-  if (__any_sync(kFullMask, over)) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (NT > 1 && n >= live) break;
-      float mx[2] = {fmaxf(z[n][0].x, z[n][1].x), fmaxf(z[n][0].y, z[n][1].y)};
-      float pm[2] = {fmaxf(p[n][0].x, p[n][1].x), fmaxf(p[n][0].y, p[n][1].y)};
-      float al[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFullMask, mx[r], d));
-          pm[r] = fmaxf(pm[r], __shfl_xor_sync(kFullMask, pm[r], d));
-        }
-        float& m = r ? S.m[n].y : S.m[n].x;
-        const bool up = __half2float(__float2half_rn(pm[r])) > 32768.f;
-        al[r] = up ? ex2(__fsub_rn(m, mx[r])) : 1.f;  // x * 1 == x: the other rows keep their bits
-        if (up) m = mx[r];
-      }
-      const float2 alpha = make_float2(al[0], al[1]);
-      S.l[n] = __fmul2_rn(S.l[n], alpha);
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        S.o[n][i][0] = __fmul_rn(S.o[n][i][0], al[0]);
-        S.o[n][i][1] = __fmul_rn(S.o[n][i][1], al[1]);
-        S.o[n][i][2] = __fmul_rn(S.o[n][i][2], al[0]);
-        S.o[n][i][3] = __fmul_rn(S.o[n][i][3], al[1]);
-      }
-      const float2 ref = make_float2(__fsub_rn(7.f, S.m[n].x), __fsub_rn(7.f, S.m[n].y));
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float2 x = __fadd2_rn(z[n][t], ref);
-        p[n][t] = make_float2(ex2(x.x), ex2(x.y));
-        w[n][t] = pack_f16x2(p[n][t].x, p[n][t].y);
-      }
-    }
-  }
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    if (NT > 1 && n >= live) break;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const float2 l = __ffma2_rn(p[n][t], make_float2(T.ri[t], T.ri[t]), S.l[n]);
-      if (MASKED) {
-        if (g + 8 * t < nv[n][0]) S.l[n].x = l.x;
-        if (g + 8 * t < nv[n][1]) S.l[n].y = l.y;
-      } else {
-        S.l[n] = l;
-      }
-      w[n][t] = transpose8x8(w[n][t]);
-    }
+    tile_weights<D, MASKED>(Q.c[n], s[n], T, nv[n], g, S.m[n], S.l[n], S.o[n], w[n]);
   }
 }
 
@@ -699,37 +688,44 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
 }
 
 // ---------------------------------------------------------------------------
-// Prefill: rows of one sequence that follow one another in the batch are taken in tiles.
-//
-// A tile has up to kTileRows query rows (row i is query head i % G of token i / G) and one kv-head,
-// and runs on one CTA of four warps:
-//   * more than kWarpRows query rows: each warp takes kWarpRows of them, and the CTA widens a chunk of pages
-//     once into f16 operands in shared memory (in fragment order, so every access is a contiguous
-//     16 bytes a lane), double buffered, the next chunk's bytes on their way in registers;
-//   * fewer (decode rows in a mixed batch, ends of chunks): every warp takes all the rows and
-//     every fourth split with its own ring, as in decode, and the CTA folds four splits at a time.
+// Prefill: rows of one sequence that follow one another in the batch are taken in tiles, and a
+// tile and one kv-head run on one CTA. Query row i of a tile is query head i % G of token i / G.
+//   * tile_kernel, tiles of up to 192 query rows: the CTA's eight warps share out the tiles of 8
+//     query rows (1 to kNT each), and widen a chunk of keys and values once for all of them, in
+//     fragment order (every access is 16 contiguous bytes a lane), while they work on the chunk
+//     before; the bytes after that are on their way (cp.async).
+//   * few_kernel, tiles of up to kFewRows query rows (decode rows in a mixed batch, ends of
+//     chunks): every warp takes all the rows and every fourth split, reading pages as decode does,
+//     and the CTA folds four splits at a time.
 // Either way a split is folded by one warp in the order above, and splits in ascending order.
-// Bound: the tensor cores' mma.sync rate and the softmax's arithmetic between the MMAs.
+// Bound: the tensor cores' mma.sync rate (509 TFLOP/s measured on operands in registers), with
+// the reads of the widened operands from shared memory next.
 
-// A tile: rows first .. first + n - 1 (one sequence), the longest of their visible lengths.
-struct Tile {
-  int first, n, pt_row, len;
+constexpr int kFewRows = 16;
+
+// What the plan holds, at the front of the workspace.
+struct Counts {
+  int32_t tiles, few;   // first rows of tiles: list[0 .. tiles - 1], and of few-row tiles: list[T - few .. T - 1]
+  int32_t next;         // the next work item of tile_kernel
 };
 
-// tiles[0 .. *count - 1] over T rows: runs of rows of one sequence cut into tiles of `per`
-// rows. One CTA of 1024 threads, each owning a contiguous stretch of rows.
-__global__ void __launch_bounds__(1024) plan_kernel(Rows R, int T, int per, Tile* __restrict__ tiles,
-                                                    int32_t* __restrict__ count) {
-  __shared__ int32_t start[1024], sums[1024];
+// Cuts the runs of rows of one sequence into tiles of `per` tokens. One CTA of 1024 threads, each
+// owning a contiguous stretch of rows. A tile whose run ends within `few` tokens is a few-row tile.
+__global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ q_seq, int T, int per, int few,
+                                                    int32_t* __restrict__ list, Counts* __restrict__ counts) {
+  __shared__ int32_t start[1024];
+  __shared__ int32_t sums[2][1024];
   const int tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
   const int each = (T + 1023) / 1024;
-  const int r0 = min(tid * each, T), r1 = min(r0 + each, T);
+  const int r0 = (int)min((int64_t)tid * each, (int64_t)T), r1 = min(r0 + each, T);
+  auto starts = [&](int r) { return r == 0 || q_seq[r] != q_seq[r - 1]; };
+  auto is_few = [&](int r) { return r + few >= T || q_seq[r + few] != q_seq[r]; };
   // the start of the run that row r0 - 1 lies in, from the running maximum of run starts
   int last = -1;
   for (int r = r0; r < r1; ++r)
-    if (r == 0 || R.q_seq[r] != R.q_seq[r - 1]) last = r;
+    if (starts(r)) last = r;
   start[tid] = last;
   __syncthreads();
   for (int d = 1; d < 1024; d <<= 1) {
@@ -739,40 +735,57 @@ __global__ void __launch_bounds__(1024) plan_kernel(Rows R, int T, int per, Tile
     __syncthreads();
   }
   const int before = tid ? start[tid - 1] : -1;
-  int run = before, local = 0;
+  int run = before, n0 = 0, n1 = 0;
   for (int r = r0; r < r1; ++r) {
-    if (r == 0 || R.q_seq[r] != R.q_seq[r - 1]) run = r;
-    local += (r - run) % per == 0;
+    if (starts(r)) run = r;
+    if ((r - run) % per) continue;
+    if (is_few(r)) ++n1;
+    else ++n0;
   }
-  sums[tid] = local;
+  sums[0][tid] = n0;
+  sums[1][tid] = n1;
   __syncthreads();
   for (int d = 1; d < 1024; d <<= 1) {
-    const int v = tid >= d ? sums[tid - d] : 0;
+    const int a = tid >= d ? sums[0][tid - d] : 0, b = tid >= d ? sums[1][tid - d] : 0;
     __syncthreads();
-    sums[tid] += v;
+    sums[0][tid] += a;
+    sums[1][tid] += b;
     __syncthreads();
   }
-  int at = sums[tid] - local;
+  int at0 = sums[0][tid] - n0, at1 = T - (sums[1][tid] - n1) - 1;
   run = before;
   for (int r = r0; r < r1; ++r) {
-    if (r == 0 || R.q_seq[r] != R.q_seq[r - 1]) run = r;
+    if (starts(r)) run = r;
     if ((r - run) % per) continue;
-    Tile t{r, 0, 0, 0};
-    while (t.n < per && r + t.n < T && R.q_seq[r + t.n] == R.q_seq[r]) {
-      int pt_row;
-      const int len = attn::row_len(R, r + t.n, pt_row);
-      if (len > t.len) t.len = len, t.pt_row = pt_row;
-      ++t.n;
-    }
-    tiles[at++] = t;
+    if (is_few(r)) list[at1--] = r;
+    else list[at0++] = r;
   }
-  if (tid == 1023) *count = sums[1023];
+  if (tid == 1023) *counts = Counts{sums[0][1023], sums[1][1023], 0};
 }
 
-constexpr int kTileWarps = 4;
-constexpr int kNT = 2;  // tiles of 8 query rows per warp
-constexpr int kWarpRows = 8 * kNT;
-constexpr int kTileRows = kTileWarps * kWarpRows;
+// Tokens of the tile that starts at row `first`: rows of its sequence that follow it, `per` at most.
+__device__ __forceinline__ int tile_tokens(const int32_t* __restrict__ q_seq, int first, int T, int per, int lane) {
+  const int seq = q_seq[first];
+  int n = 0;
+  while (n < per) {
+    const int r = first + n + lane;
+    const uint32_t same = __ballot_sync(kFullMask, r < T && n + lane < per && q_seq[r] == seq);
+    if (same != kFullMask) return n + __ffs(~same) - 1;
+    n += 32;
+  }
+  return per;
+}
+
+// The page of tokens tp .. tp + 15 as a store row, or -1 past `len` or if the page is unusable.
+__device__ __forceinline__ int64_t tile_row0(const Cache& C, const int32_t* prow, int tp, int len, int Hkv, int kh) {
+  if (tp >= len) return -1;
+  const int pg = prow[tp / PAGE];
+  if (pg < 0 || pg >= C.num_pages) {
+    record_error(BI_ERR_DEVICE_INDEX);
+    return -1;
+  }
+  return ((int64_t)pg * Hkv + kh) * PAGE;
+}
 
 // cp.async of one page (store rows row0 .. + 15) by a warp, 16 contiguous bytes a lane.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -794,139 +807,18 @@ __device__ __forceinline__ void copy_page(uint32_t page, uint32_t scales, const 
   if (lane < 8) cp_async16(scales + 16 * lane, (lane < 4 ? C.ks + row0 : C.vs + row0 - PAGE) + 4 * lane);
 }
 
-constexpr int kTileStages = 4;
-
-template <int D>
-struct TileSmem {
-  static constexpr int PAGES = 256 / D;                   // pages a chunk: one item of each kind per warp
-  static constexpr int OPERANDS = PAGES * 2 * PAGE * D * 2;  // f16 keys and values
-  static constexpr int BUFFER = OPERANDS + PAGES * PAGE * 16;  // and {ks, log2 vs, 1 / vs, -} per token
-  static constexpr int TOTALS = kTileRows * D * 4;
-  // few rows: the rings, over which the four splits' partial results go, and the totals
-  static constexpr int STAGE = kPageBytes<D> + kScaleBytes;
-  static constexpr int RINGS = kTileWarps * kTileStages * STAGE;
-  static constexpr int PARTIALS = kTileWarps * kWarpRows * D * 4;
-  static constexpr int SMALL = (RINGS > PARTIALS ? RINGS : PARTIALS) + kTileWarps * kWarpRows * 8 + kWarpRows * D * 4;
-  static constexpr int LARGE = 2 * BUFFER + TOTALS;
-  static constexpr int BYTES = SMALL > LARGE ? SMALL : LARGE;
-};
+template <int BYTES>
+__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void* src, bool take) {
+  const int n = take ? BYTES : 0;  // the rest of the BYTES is filled with zeros
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
-}
-
-// One lane's bytes of a chunk: key bytes of tokens g, g + 8 and value bytes of four tokens of
-// the page and part that its warp widens, and a token's scales.
-struct Raw {
-  uint4 k[2];
-  uint2 v[4];
-  float ks, vs;
-};
-
-template <int D>
-__device__ __forceinline__ int64_t tile_row0(const Cache& C, const int32_t* prow, int tp, int len, int Hkv, int kh) {
-  if (tp >= len) return -1;
-  const int pg = prow[tp / PAGE];
-  if (pg < 0 || pg >= C.num_pages) {
-    record_error(BI_ERR_DEVICE_INDEX);
-    return -1;
-  }
-  return ((int64_t)pg * Hkv + kh) * PAGE;
-}
-
-// Loads chunk tp .. of a tile; bytes of unusable pages and of tokens from len on are zeros.
-template <int D>
-__device__ __forceinline__ void load_chunk(Raw& X, const Cache& C, const int32_t* prow, int tp, int len, int Hkv, int kh,
-                                           int warp, int lane) {
-  const int g = lane >> 2, c = lane & 3;
-  static_assert(TileSmem<D>::PAGES * (D / 64) == kTileWarps, "one page part a warp");
-  const int page = warp / (D / 64), part = warp % (D / 64);
-  const int t0 = tp + page * PAGE;
-  const int64_t row0 = tile_row0<D>(C, prow, t0, len, Hkv, kh);
-  const uint8_t* kp = C.k + (row0 + g) * D + 64 * part + 16 * c;
-  X.k[0] = row0 >= 0 ? ldg16(kp) : make_uint4(0, 0, 0, 0);
-  X.k[1] = row0 >= 0 ? ldg16(kp + 8 * D) : make_uint4(0, 0, 0, 0);
-  const uint8_t* vp = C.v + (row0 + 2 * c) * D + (D / 8) * g + 8 * part;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = (i & 1) + 8 * (i >> 1);
-    X.v[i] = row0 >= 0 && t0 + 2 * c + t < len ? __ldg(reinterpret_cast<const uint2*>(vp + t * D)) : make_uint2(0, 0);
-  }
-  const int tok = warp * 32 + lane;
-  X.ks = 0.f;
-  X.vs = 0.f;  // log2 is -infinity: the token has no weight
-  if (tok < TileSmem<D>::PAGES * PAGE) {
-    const int64_t r = tile_row0<D>(C, prow, tp + tok / PAGE * PAGE, len, Hkv, kh);
-    if (r >= 0 && tp + tok < len) {
-      X.ks = __ldg(C.ks + r + tok % PAGE);
-      X.vs = __ldg(C.vs + r + tok % PAGE);
-    }
-  }
-}
-
-// Widens the loaded chunk into a buffer: keys [page][step][lane], values [page][tile][lane], tokens.
-template <int KIND, int D>
-__device__ __forceinline__ void store_chunk(const Raw& X, uint32_t buf, int warp, int lane) {
-  using M = TileSmem<D>;
-  const int page = warp / (D / 64), part = warp % (D / 64);
-  const uint32_t kb = buf + ((page * (D / 16) + 4 * part) * 32 + lane) * 16;
-  const uint32_t xw[4] = {X.k[0].x, X.k[0].y, X.k[0].z, X.k[0].w}, yw[4] = {X.k[1].x, X.k[1].y, X.k[1].z, X.k[1].w};
-#pragma unroll
-  for (int b = 0; b < 4; ++b) st_shared_v4(kb + b * 512, key_operand<KIND>(xw[b], yw[b]));
-  const uint32_t vb = buf + M::OPERANDS / 2 + ((page * (D / 16) + 4 * part) * 32 + lane) * 16;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    uint32_t x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = u ? X.v[i].y : X.v[i].x;
-    uint4 a, b;
-    value_operands<KIND>(x, a, b);
-    st_shared_v4(vb + (2 * u) * 512, a);
-    st_shared_v4(vb + (2 * u + 1) * 512, b);
-  }
-  const int tok = warp * 32 + lane;
-  if (tok < M::PAGES * PAGE) {
-    const float4 t = make_float4(X.ks, lg2(X.vs), X.vs == 0.f ? 0.f : rcp(X.vs), 0.f);
-    st_shared_v4(buf + M::OPERANDS + tok * 16, *reinterpret_cast<const uint4*>(&t));
-  }
-}
-
-// Folds one page of a buffer.
-template <int D, bool MASKED>
-__device__ __forceinline__ void fold_wide(const Query<D, kNT>& Q, uint32_t buf, int page, const int (&nv)[kNT][2],
-                                          int live, int lane, State<D, kNT>& S) {
-  using M = TileSmem<D>;
-  const int g = lane >> 2;
-  float s[kNT][4];
-  const uint32_t kb = buf + (page * (D / 16) * 32 + lane) * 16, vb = kb + M::OPERANDS / 2;
-#pragma unroll
-  for (int j = 0; j < D / 16; ++j) {
-    const uint4 a = ld_shared_v4(kb + j * 512);
-#pragma unroll
-    for (int n = 0; n < kNT; ++n)
-      if (n < live) {
-        if (j == 0) mma16816_first(s[n], a, Q.b[n][0][0], Q.b[n][0][1]);
-        else mma16816(s[n], a, Q.b[n][j][0], Q.b[n][j][1]);
-      }
-  }
-  Tokens T;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const uint4 x = ld_shared_v4(buf + M::OPERANDS + (page * PAGE + g + 8 * t) * 16);
-    T.ks[t] = __uint_as_float(x.x);
-    T.lg[t] = __uint_as_float(x.y);
-    T.ri[t] = __uint_as_float(x.z);
-  }
-  uint32_t w[kNT][2];
-  page_weights<D, kNT, MASKED>(Q, s, T, nv, g, live, S, w);
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
-    const uint4 a = ld_shared_v4(vb + i * 512);
-#pragma unroll
-    for (int n = 0; n < kNT; ++n)
-      if (n < live) mma16816(S.o[n][i], a, w[n][0], w[n][1]);
-  }
 }
 
 // Writes a query row's dims (D/8) g .. + D/8 - 1.
@@ -942,196 +834,435 @@ __device__ __forceinline__ void store_row(uint16_t* dst, const float (&x)[D / 8]
   }
 }
 
+constexpr int kNT = 3;         // tiles of 8 query rows per warp, at most
+constexpr int kTileWarps = 8;
+constexpr int kTileRows = kTileWarps * kNT * 8;
+
+template <int D>
+struct TileSmem {
+  static constexpr int PAGES = 512 / D;                      // pages a chunk: one item of each kind per warp
+  static constexpr int OPERANDS = PAGES * 2 * PAGE * D * 2;  // f16 keys, then values
+  static constexpr int BUFFER = OPERANDS + PAGES * PAGE * 16;  // and {ks, log2 vs, 1 / vs, -} per token
+  static constexpr int RAW = kTileWarps * 32 * 64 + PAGES * PAGE * 8;  // one thread's 64 bytes; scales
+  static constexpr int RAW_AT = 2 * BUFFER;
+  static constexpr int TOTALS = RAW_AT + 2 * RAW;            // fp32 totals [row][D], lane by lane
+  static constexpr int STATS = TOTALS + kTileRows * D * 4;   // M and L, lane by lane
+  static constexpr int MISC = STATS + kTileWarps * 32 * kNT * 16;
+  static constexpr int BYTES = MISC + 64;
+  static_assert(BYTES <= 227 * 1024, "shared memory");
+};
+
+// Starts the copies of this thread's part of the chunk at token tp: key bytes of tokens g and
+// g + 8 and value bytes of four tokens, of the page and part that its warp widens, and a token's
+// scales. Bytes of unusable pages, and of tokens from len on, become zeros.
+template <int D>
+__device__ __forceinline__ void copy_chunk(uint32_t raw, const Cache& C, const int32_t* prow, int tp, int len, int Hkv,
+                                           int kh, int warp, int lane) {
+  const int g = lane >> 2, c = lane & 3;
+  static_assert(TileSmem<D>::PAGES * (D / 64) == kTileWarps, "one page part a warp");
+  const int page = warp / (D / 64), part = warp % (D / 64);
+  const int t0 = tp + page * PAGE;
+  const int64_t at = tile_row0(C, prow, t0, len, Hkv, kh);
+  const bool ok = at >= 0;
+  const int64_t row0 = ok ? at : 0;
+  const uint32_t mine = raw + (uint32_t)(warp * 2048 + lane * 16);
+  const uint8_t* kp = C.k + (row0 + g) * D + 64 * part + 16 * c;
+  cp_async_or_zero<16>(mine, kp, ok);
+  cp_async_or_zero<16>(mine + 512, kp + 8 * D, ok);
+  const uint8_t* vp = C.v + (row0 + 2 * c) * D + (D / 8) * g + 8 * part;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = (i & 1) + 8 * (i >> 1);
+    cp_async_or_zero<8>(raw + (uint32_t)(warp * 2048 + 1024 + i * 256 + lane * 8), vp + t * D, ok && t0 + 2 * c + t < len);
+  }
+  const int tok = warp * 32 + lane;
+  if (tok < TileSmem<D>::PAGES * PAGE) {
+    const int64_t r = tile_row0(C, prow, tp + tok / PAGE * PAGE, len, Hkv, kh);
+    const bool seen = r >= 0 && tp + tok < len;
+    const uint32_t sc = raw + (uint32_t)(kTileWarps * 2048 + tok * 8);
+    cp_async_or_zero<4>(sc, C.ks + (seen ? r + tok % PAGE : 0), seen);
+    cp_async_or_zero<4>(sc + 4, C.vs + (seen ? r + tok % PAGE : 0), seen);
+  }
+  cp_commit();
+}
+
+// Widens this thread's part of a chunk (its own copies, complete) into a buffer: keys
+// [page][step][lane], values [page][tile][lane], tokens. A token without a value scale (0) has
+// log2 -infinity: no weight.
 template <int KIND, int D>
-__global__ void __launch_bounds__(kTileWarps * 32, 2)
-    tile_kernel(const uint16_t* __restrict__ q, int64_t ldq, int Hq, int Hkv, Cache C, Rows R,
-                const Tile* __restrict__ tiles, const int32_t* __restrict__ count, uint16_t* __restrict__ out,
+__device__ __forceinline__ void widen_chunk(uint32_t raw, uint32_t buf, int warp, int lane) {
+  using M = TileSmem<D>;
+  const int page = warp / (D / 64), part = warp % (D / 64);
+  const uint32_t kb = buf + ((page * (D / 16) + 4 * part) * 32 + lane) * 16;
+  const uint4 x = ld_shared_v4(raw + warp * 2048 + lane * 16), y = ld_shared_v4(raw + warp * 2048 + 512 + lane * 16);
+  const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int b = 0; b < 4; ++b) st_shared_v4(kb + b * 512, key_operand<KIND>(xw[b], yw[b]));
+  const uint32_t vb = buf + M::OPERANDS / 2 + ((page * (D / 16) + 4 * part) * 32 + lane) * 16;
+  uint2 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(v[i].x), "=r"(v[i].y)
+                 : "r"(raw + warp * 2048 + 1024 + i * 256 + lane * 8));
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = u ? v[i].y : v[i].x;
+    uint4 a, b;
+    value_operands<KIND>(w, a, b);
+    st_shared_v4(vb + (2 * u) * 512, a);
+    st_shared_v4(vb + (2 * u + 1) * 512, b);
+  }
+  const int tok = warp * 32 + lane;
+  if (tok < M::PAGES * PAGE) {
+    const uint32_t sc = raw + (uint32_t)(kTileWarps * 2048 + tok * 8);
+    const float ks = ld_shared_f32(sc), vs = ld_shared_f32(sc + 4);
+    const float4 t = make_float4(ks, lg2(vs), vs == 0.f ? 0.f : rcp(vs), 0.f);
+    st_shared_v4(buf + M::OPERANDS + tok * 16, *reinterpret_cast<const uint4*>(&t));
+  }
+}
+
+// Folds one page of a buffer into the warp's LIVE tiles.
+template <int D, int LIVE, bool MASKED>
+__device__ __forceinline__ void fold_wide(const Query<D, LIVE>& Q, uint32_t buf, int page, const int (&nv)[LIVE][2],
+                                          int lane, State<D, LIVE>& S) {
+  using M = TileSmem<D>;
+  const int g = lane >> 2;
+  float s[LIVE][4];
+  const uint32_t kb = buf + (page * (D / 16) * 32 + lane) * 16, vb = kb + M::OPERANDS / 2;
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) {
+    const uint4 a = ld_shared_v4(kb + j * 512);
+#pragma unroll
+    for (int n = 0; n < LIVE; ++n) {
+      if (j == 0) mma16816_first(s[n], a, Q.b[n][0][0], Q.b[n][0][1]);
+      else mma16816(s[n], a, Q.b[n][j][0], Q.b[n][j][1]);
+    }
+  }
+  Tokens T;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const uint4 x = ld_shared_v4(buf + M::OPERANDS + (page * PAGE + g + 8 * t) * 16);
+    T.ks[t] = __uint_as_float(x.x);
+    T.lg[t] = __uint_as_float(x.y);
+    T.ri[t] = __uint_as_float(x.z);
+  }
+  uint32_t w[LIVE][2];
+  page_weights<D, LIVE, MASKED>(Q, s, T, nv, g, LIVE, S, w);
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const uint4 a = ld_shared_v4(vb + i * 512);
+#pragma unroll
+    for (int n = 0; n < LIVE; ++n) mma16816(S.o[n][i], a, w[n][0], w[n][1]);
+  }
+}
+
+// What a warp needs of its tile.
+struct TileArgs {
+  const uint16_t* q;
+  int64_t ldq;
+  uint16_t* out;
+  Cache C;
+  Rows R;
+  const int32_t* prow;
+  int Hq, Hkv, G, first, rows, kh, len;
+  float scale_log2;
+};
+
+// One tile on a CTA whose warps have LIVE tiles of 8 query rows at most (the warp's n-th is tile
+// 8 n + warp). Rows past the tile's end are zeros whose results go nowhere.
+template <int KIND, int D, int LIVE>
+__device__ __noinline__ void run_tile(const TileArgs A, uint32_t base, float* totals, int warp, int lane) {
+  using M = TileSmem<D>;
+  const int g = lane >> 2, c = lane & 3;
+  constexpr int CHUNK = M::PAGES * PAGE;
+  copy_chunk<D>(base + M::RAW_AT, A.C, A.prow, 0, A.len, A.Hkv, A.kh, warp, lane);
+  Query<D, LIVE> Q;
+  int shortest = INT_MAX, longest = 0;
+  auto len_of = [&](int n, int r) {  // visible tokens of the lane's query row (n, r)
+    const int k = (n * kTileWarps + warp) * 8 + 2 * c + r;
+    int pt_row;
+    return k < A.rows ? attn::row_len(A.R, A.first + k / A.G, pt_row) : -1;
+  };
+#pragma unroll
+  for (int n = 0; n < LIVE; ++n) {
+    const int i = (n * kTileWarps + warp) * 8 + g;
+    load_query<D, LIVE>(Q, n,
+                        i < A.rows ? A.q + (int64_t)(A.first + i / A.G) * A.ldq + (int64_t)(A.kh * A.G + i % A.G) * D : nullptr,
+                        lane, A.scale_log2);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int len = len_of(n, r);
+      if (len < 0) continue;
+      longest = max(longest, len);
+      shortest = min(shortest, len);
+    }
+  }
+  longest = __reduce_max_sync(kFullMask, longest);
+  shortest = __reduce_min_sync(kFullMask, shortest);
+  // running totals over splits, in places of this lane's own: totals, M and L
+  float* tot = totals + warp * (kNT * 8) * D + lane;  // entry i at tot[32 i]
+  float4* stats = reinterpret_cast<float4*>(totals + kTileRows * D) + warp * 32 * kNT + lane;  // entry n at [32 n]
+#pragma unroll
+  for (int n = 0; n < LIVE; ++n) stats[32 * n] = make_float4(kLowest, kLowest, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = 0; i < LIVE * D / 4; ++i) tot[32 * i] = 0.f;
+
+  cp_wait<0>();
+  widen_chunk<KIND, D>(base + M::RAW_AT, base, warp, lane);
+  if (CHUNK < A.len) copy_chunk<D>(base + M::RAW_AT + M::RAW, A.C, A.prow, CHUNK, A.len, A.Hkv, A.kh, warp, lane);
+  int b = 0;
+  for (int t0 = 0; t0 < A.len; t0 += SPLIT) {
+    State<D, LIVE> S;
+    S.clear();
+    for (int tp = t0; tp < min(t0 + SPLIT, A.len); tp += CHUNK, b ^= 1) {
+      __syncthreads();  // this chunk is widened, and every warp is done with the buffer of the one before
+      // the next chunk is widened before this one is folded by half of the warps, after it by the
+      // other half, so that a scheduler's two warps do not both widen while the tensor cores wait
+      auto next = [&] {
+        if (tp + CHUNK >= A.len) return;
+        cp_wait<0>();
+        widen_chunk<KIND, D>(base + M::RAW_AT + (b ^ 1) * M::RAW, base + (b ^ 1) * M::BUFFER, warp, lane);
+        if (tp + 2 * CHUNK < A.len)
+          copy_chunk<D>(base + M::RAW_AT + b * M::RAW, A.C, A.prow, tp + 2 * CHUNK, A.len, A.Hkv, A.kh, warp, lane);
+      };
+      if (warp < kTileWarps / 2) next();
+#pragma unroll 1
+      for (int p = 0; p < M::PAGES; ++p) {
+        const int at = tp + p * PAGE;
+        if (at >= longest) break;
+        int nv[LIVE][2];
+        if (at + PAGE <= shortest) {
+          fold_wide<D, LIVE, false>(Q, base + b * M::BUFFER, p, nv, lane, S);
+        } else {
+#pragma unroll
+          for (int n = 0; n < LIVE; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) nv[n][r] = len_of(n, r) - at;
+          fold_wide<D, LIVE, true>(Q, base + b * M::BUFFER, p, nv, lane, S);
+        }
+      }
+      if (warp >= kTileWarps / 2) next();
+    }
+#pragma unroll
+    for (int n = 0; n < LIVE; ++n) {
+      float4 st = stats[32 * n];
+      float a0, b0, a1, b1;
+      const float l0 = row_sum(S.l[n].x), l1 = row_sum(S.l[n].y);
+      join(st.x, S.m[n].x, a0, b0);
+      join(st.y, S.m[n].y, a1, b1);
+      st.z = __fmaf_rn(l0, b0, __fmul_rn(st.z, a0));
+      st.w = __fmaf_rn(l1, b1, __fmul_rn(st.w, a1));
+      stats[32 * n] = st;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float* x = tot + 32 * ((n * 2 + (e & 1)) * (D / 8) + 2 * i + (e >> 1));
+          *x = __fmaf_rn(S.o[n][i][e], e & 1 ? b1 : b0, __fmul_rn(*x, e & 1 ? a1 : a0));
+        }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < LIVE; ++n)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int k = (n * kTileWarps + warp) * 8 + 2 * c + r;
+      if (k >= A.rows) continue;
+      const float4 st = stats[32 * n];
+      float x[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) x[i] = tot[32 * ((n * 2 + r) * (D / 8) + i)];
+      store_row<D>(A.out + ((int64_t)(A.first + k / A.G) * A.Hq + A.kh * A.G + k % A.G) * D + (D / 8) * g, x, r ? st.w : st.z);
+    }
+}
+
+template <int KIND, int D>
+__global__ void __launch_bounds__(kTileWarps * 32, 1)
+    tile_kernel(const uint16_t* __restrict__ q, int64_t ldq, int Hq, int Hkv, Cache C, Rows R, int T, int per,
+                const int32_t* __restrict__ list, Counts* __restrict__ counts, uint16_t* __restrict__ out,
                 float scale_log2) {
   using M = TileSmem<D>;
   extern __shared__ __align__(16) uint8_t smem[];
+  int* misc = reinterpret_cast<int*>(smem + M::MISC);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = smem_u32(smem);
+  pdl_wait();  // the plan (and the caller's q and store) are complete from here on
+  pdl_trigger();
+  const int total = counts->tiles * Hkv;
+  while (true) {
+    if (threadIdx.x == 0) misc[0] = atomicAdd(&counts->next, 1);  // who takes which item is all this decides
+    __syncthreads();
+    const int item = total - 1 - misc[0];  // later rows of a prompt see more keys: longest first
+    if (item < 0) return;
+    TileArgs A;
+    A.q = q; A.ldq = ldq; A.out = out; A.C = C; A.R = R; A.Hq = Hq; A.Hkv = Hkv; A.G = Hq / Hkv;
+    A.scale_log2 = scale_log2;
+    A.first = list[item / Hkv];
+    A.kh = item % Hkv;
+    const int n = tile_tokens(R.q_seq, A.first, T, per, lane);
+    A.rows = n * A.G;
+    int len = 0, pt_row = 0;
+    for (int i = lane; i < n; i += 32) {
+      int row;
+      const int x = attn::row_len(R, A.first + i, row);
+      if (x > len) len = x, pt_row = row;
+    }
+    A.len = __reduce_max_sync(kFullMask, len);
+    pt_row = __reduce_max_sync(kFullMask, pt_row);  // rows that see anything share it; the others gave 0
+    A.prow = C.pt + (int64_t)pt_row * R.max_pages;
+    float* totals = reinterpret_cast<float*>(smem + M::TOTALS);
+    const int tiles = (A.rows + 7) / 8;  // of 8 query rows
+    if (tiles > 2 * kTileWarps) run_tile<KIND, D, 3>(A, base, totals, warp, lane);
+    else if (tiles > kTileWarps) run_tile<KIND, D, 2>(A, base, totals, warp, lane);
+    else run_tile<KIND, D, 1>(A, base, totals, warp, lane);
+    __syncthreads();  // shared memory is free for the next tile
+  }
+}
+
+constexpr int kFewWarps = 4;
+constexpr int kFewStages = 3;
+constexpr int kFewNT = kFewRows / 8;
+
+template <int D>
+struct FewSmem {
+  static constexpr int STAGE = kPageBytes<D> + kScaleBytes;
+  static constexpr int RINGS = kFewWarps * kFewStages * STAGE;       // over which the partial results go
+  static constexpr int PARTIALS = kFewWarps * kFewRows * D * 4;
+  static constexpr int OVER = RINGS > PARTIALS ? RINGS : PARTIALS;
+  static constexpr int BYTES = OVER + kFewWarps * kFewRows * 8 + kFewRows * D * 4;
+};
+
+template <int KIND, int D>
+__global__ void __launch_bounds__(kFewWarps * 32, 3)
+    few_kernel(const uint16_t* __restrict__ q, int64_t ldq, int Hq, int Hkv, Cache C, Rows R, int T, int few,
+               const int32_t* __restrict__ list, const Counts* __restrict__ counts, uint16_t* __restrict__ out,
+               float scale_log2) {
+  using M = FewSmem<D>;
+  extern __shared__ __align__(1024) uint8_t smem_few[];  // pages' swizzle counts from 128-byte boundaries
+  uint8_t* smem = smem_few;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int G = Hq / Hkv;
   const uint32_t base = smem_u32(smem);
   pdl_wait();  // the plan (and the caller's q and store) are complete from here on
   pdl_trigger();
-  const int64_t total = (int64_t)*count * Hkv;
-  // later rows of a prompt see more keys: longest first
-  for (int64_t item = total - 1 - blockIdx.x; item >= 0; item -= gridDim.x) {
-    const Tile t = tiles[item / Hkv];
-    const int kh = (int)(item % Hkv);
-    const int rows = t.n * G;
-    const bool small = rows <= kWarpRows;
-    const int i0 = small ? 0 : warp * kWarpRows;                    // the warp's first query row
-    const int live = min(kNT, (rows - i0 + 7) / 8);               // its tiles that hold rows (<= 0: none)
-    Query<D, kNT> Q;
-    int len[kNT][2];
-    int longest = 0, shortest = INT_MAX / 2;
+  const int total = counts->few * Hkv;
+  for (int item = blockIdx.x; item < total; item += gridDim.x) {
+    const int first = list[T - 1 - item / Hkv], kh = item % Hkv;
+    const int n_tok = tile_tokens(R.q_seq, first, T, few, lane);
+    const int rows = n_tok * G, live = (rows + 7) / 8;
+    Query<D, kFewNT> Q;
+    int len[kFewNT][2], longest = 0, shortest = INT_MAX / 2, pt_row = 0;
 #pragma unroll
-    for (int n = 0; n < kNT; ++n) {
-      const int i = i0 + 8 * n + g;
-      load_query<D, kNT>(Q, n, i < rows ? q + (int64_t)(t.first + i / G) * ldq + (int64_t)(kh * G + i % G) * D : nullptr,
-                         lane, scale_log2);
+    for (int n = 0; n < kFewNT; ++n) {
+      const int i = 8 * n + g;
+      load_query<D, kFewNT>(Q, n, i < rows ? q + (int64_t)(first + i / G) * ldq + (int64_t)(kh * G + i % G) * D : nullptr,
+                            lane, scale_log2);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int k = i0 + 8 * n + 2 * c + r;
-        int pt_row;
-        len[n][r] = k < rows ? attn::row_len(R, t.first + k / G, pt_row) : INT_MAX / 2;  // no row: nothing to mask
-        if (k < rows) longest = max(longest, len[n][r]);
+        const int k = 8 * n + 2 * c + r;
+        len[n][r] = INT_MAX / 2;  // no row: nothing to mask
+        if (k < rows) {
+          int row;
+          len[n][r] = attn::row_len(R, first + k / G, row);
+          longest = max(longest, len[n][r]);
+          pt_row = max(pt_row, row);
+        }
         shortest = min(shortest, len[n][r]);
       }
     }
     longest = __reduce_max_sync(kFullMask, longest);
     shortest = __reduce_min_sync(kFullMask, shortest);
-    const int32_t* prow = C.pt + (int64_t)t.pt_row * R.max_pages;
-    float Mx[kNT][2], L[kNT][2];
-#pragma unroll
-    for (int n = 0; n < kNT; ++n) {
-      Mx[n][0] = Mx[n][1] = kLowest;
-      L[n][0] = L[n][1] = 0.f;
-    }
-    if (!small) {
-      float* tot = reinterpret_cast<float*>(smem + 2 * M::BUFFER) + warp * kWarpRows * D + lane;  // entry i at tot[32 i]
-      for (int i = 0; i < kWarpRows * D / 32; ++i) tot[32 * i] = 0.f;
-      constexpr int CHUNK = M::PAGES * PAGE;
-      Raw X;
-      if (t.len > 0) load_chunk<D>(X, C, prow, 0, t.len, Hkv, kh, warp, lane);
-      int b = 0;
-      for (int t0 = 0; t0 < t.len; t0 += SPLIT) {
-        State<D, kNT> S;
-        S.clear();
-        for (int tp = t0; tp < min(t0 + SPLIT, t.len); tp += CHUNK, b ^= 1) {
-          const uint32_t buf = base + b * M::BUFFER;
-          store_chunk<KIND, D>(X, buf, warp, lane);
-          if (tp + CHUNK < t.len) load_chunk<D>(X, C, prow, tp + CHUNK, t.len, Hkv, kh, warp, lane);
-          __syncthreads();  // the buffer is complete, and every warp is done with the other one
-          for (int p = 0; p < M::PAGES; ++p) {
-            if (tp + p * PAGE >= longest) break;
-            int nv[kNT][2];
-#pragma unroll
-            for (int n = 0; n < kNT; ++n)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) nv[n][r] = len[n][r] - tp - p * PAGE;
-            if (tp + p * PAGE + PAGE <= shortest) fold_wide<D, false>(Q, buf, p, nv, live, lane, S);
-            else fold_wide<D, true>(Q, buf, p, nv, live, lane, S);
-          }
+    pt_row = __reduce_max_sync(kFullMask, pt_row);  // rows that see anything share it; the others gave 0
+    const int32_t* prow = C.pt + (int64_t)pt_row * R.max_pages;
+    // four splits at a time, one a warp; then row k's thread group folds them in order
+    const uint32_t ring = base + (uint32_t)(warp * kFewStages * kPageBytes<D>);
+    const uint32_t scales = base + (uint32_t)(kFewWarps * kFewStages * kPageBytes<D> + warp * kFewStages * kScaleBytes);
+    float* part = reinterpret_cast<float*>(smem);                                  // [warp][row][D]
+    float2* pml = reinterpret_cast<float2*>(smem + M::OVER);                          // [warp][row]
+    float* tot = reinterpret_cast<float*>(smem + M::OVER + kFewWarps * kFewRows * 8);      // [row][D]
+    for (int i = threadIdx.x; i < rows * D; i += kFewWarps * 32) tot[i] = 0.f;
+    // thread -> (row, quarter of D) for the folds
+    const int frow = threadIdx.x >> 2, fd = (threadIdx.x & 3) * (D / 4);
+    float FM = kLowest, FL = 0.f;
+    for (int r0 = 0; r0 < longest; r0 += kFewWarps * SPLIT) {
+      const int t0 = r0 + warp * SPLIT, seen = min(SPLIT, longest - t0);
+      State<D, kFewNT> S;
+      S.clear();
+      const int np = seen > 0 ? (seen + PAGE - 1) / PAGE : 0;
+      int page = -1;
+      if (lane < np) {
+        const int64_t row0 = tile_row0(C, prow, t0 + lane * PAGE, longest, Hkv, kh);
+        page = row0 < 0 ? -1 : (int)(row0 / (Hkv * PAGE));
+      }
+      auto issue = [&](int j) {
+        if (j < np) {
+          const int pg = __shfl_sync(kFullMask, page, j);
+          const uint32_t st = (uint32_t)(j % kFewStages);
+          if (pg >= 0)
+            copy_page<D>(ring + st * kPageBytes<D>, scales + st * kScaleBytes, C, ((int64_t)pg * Hkv + kh) * PAGE, lane);
         }
+        cp_commit();
+      };
+      for (int j = 0; j < kFewStages; ++j) issue(j);
+      for (int j = 0; j < np; ++j) {
+        cp_wait<kFewStages - 1>();
+        __syncwarp();
+        if (__shfl_sync(kFullMask, page, j) >= 0) {
+          const int tp = t0 + j * PAGE;
+          int nv[kFewNT][2];
 #pragma unroll
-        for (int n = 0; n < kNT; ++n)
+          for (int n = 0; n < kFewNT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) nv[n][r] = len[n][r] - tp;
+          const uint32_t st = (uint32_t)(j % kFewStages), pg = ring + st * kPageBytes<D>, sc = scales + st * kScaleBytes;
+          if (tp + PAGE <= shortest) fold_page<KIND, D, kFewNT, false>(Q, pg, sc, nv, PAGE, live, lane, S);
+          else fold_page<KIND, D, kFewNT, true>(Q, pg, sc, nv, longest - tp, live, lane, S);
+        }
+        __syncwarp();
+        issue(j + kFewStages);
+      }
+      cp_wait<0>();
+      __syncthreads();  // the rings are free (and the totals cleared, or the last fold done)
+      if (np > 0) {
+#pragma unroll
+        for (int n = 0; n < kFewNT; ++n)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float fa, fb;
             const float l = row_sum(r ? S.l[n].y : S.l[n].x);
-            join(Mx[n][r], r ? S.m[n].y : S.m[n].x, fa, fb);
-            L[n][r] = __fmaf_rn(l, fb, __fmul_rn(L[n][r], fa));
+            const int k = 8 * n + 2 * c + r;
+            if (k >= rows) continue;
+            float* dst = part + (warp * kFewRows + k) * D + (D / 8) * g;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float* x = tot + 32 * ((n * 2 + r) * (D / 8) + 2 * i + e);
-                *x = __fmaf_rn(S.o[n][i][2 * e + r], fb, __fmul_rn(*x, fa));
-              }
+            for (int i = 0; i < D / 16; i += 2)
+              *reinterpret_cast<float4*>(dst + 2 * i) =
+                  make_float4(S.o[n][i][r], S.o[n][i][2 + r], S.o[n][i + 1][r], S.o[n][i + 1][2 + r]);
+            if (g == 0) pml[warp * kFewRows + k] = make_float2(r ? S.m[n].y : S.m[n].x, l);
           }
-      }
-#pragma unroll
-      for (int n = 0; n < kNT; ++n)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int k = i0 + 8 * n + 2 * c + r;
-          if (k >= rows) continue;
-          float x[D / 8];
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) x[i] = tot[32 * ((n * 2 + r) * (D / 8) + i)];
-          store_row<D>(out + ((int64_t)(t.first + k / G) * Hq + kh * G + k % G) * D + (D / 8) * g, x, L[n][r]);
-        }
-    } else {
-      // four splits at a time, one a warp; then row k's thread group folds them in order
-      const uint32_t ring = base + (uint32_t)(warp * kTileStages * kPageBytes<D>);
-      const uint32_t scales = base + (uint32_t)(kTileWarps * kTileStages * kPageBytes<D> + warp * kTileStages * kScaleBytes);
-      float* part = reinterpret_cast<float*>(smem);                                  // [warp][row][D]
-      constexpr int OVER = M::RINGS > M::PARTIALS ? M::RINGS : M::PARTIALS;
-      float2* pml = reinterpret_cast<float2*>(smem + OVER);                          // [warp][row]
-      float* tot = reinterpret_cast<float*>(smem + OVER + kTileWarps * kWarpRows * 8);      // [row][D]
-      for (int i = threadIdx.x; i < rows * D; i += kTileWarps * 32) tot[i] = 0.f;
-      // thread -> (row, quarter of D) for the folds
-      const int frow = threadIdx.x >> 2, fd = (threadIdx.x & 3) * (D / 4);
-      float FM = kLowest, FL = 0.f;
-      for (int r0 = 0; r0 < t.len; r0 += kTileWarps * SPLIT) {
-        const int t0 = r0 + warp * SPLIT, seen = min(SPLIT, t.len - t0);
-        State<D, kNT> S;
-        S.clear();
-        const int np = seen > 0 ? (seen + PAGE - 1) / PAGE : 0;
-        int page = -1;
-        if (lane < np) {
-          const int64_t row0 = tile_row0<D>(C, prow, t0 + lane * PAGE, t.len, Hkv, kh);
-          page = row0 < 0 ? -1 : (int)(row0 / (Hkv * PAGE));
-        }
-        auto issue = [&](int j) {
-          if (j < np) {
-            const int pg = __shfl_sync(kFullMask, page, j);
-            const uint32_t st = (uint32_t)(j % kTileStages);
-            if (pg >= 0)
-              copy_page<D>(ring + st * kPageBytes<D>, scales + st * kScaleBytes, C, ((int64_t)pg * Hkv + kh) * PAGE, lane);
-          }
-          cp_commit();
-        };
-        for (int j = 0; j < kTileStages; ++j) issue(j);
-        for (int j = 0; j < np; ++j) {
-          cp_wait<kTileStages - 1>();
-          __syncwarp();
-          if (__shfl_sync(kFullMask, page, j) >= 0) {
-            const int tp = t0 + j * PAGE;
-            int nv[kNT][2];
-#pragma unroll
-            for (int n = 0; n < kNT; ++n)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) nv[n][r] = len[n][r] - tp;
-            const uint32_t st = (uint32_t)(j % kTileStages), pg = ring + st * kPageBytes<D>, sc = scales + st * kScaleBytes;
-            if (tp + PAGE <= shortest) fold_page<KIND, D, kNT, false>(Q, pg, sc, nv, PAGE, live, lane, S);
-            else fold_page<KIND, D, kNT, true>(Q, pg, sc, nv, t.len - tp, live, lane, S);
-          }
-          __syncwarp();
-          issue(j + kTileStages);
-        }
-        cp_wait<0>();
-        __syncthreads();  // the rings are free (and the totals cleared, or the last fold done)
-        if (np > 0) {
-#pragma unroll
-          for (int n = 0; n < kNT; ++n)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float l = row_sum(r ? S.l[n].y : S.l[n].x);
-              const int k = 8 * n + 2 * c + r;
-              if (k >= rows) continue;
-              float* dst = part + (warp * kWarpRows + k) * D + (D / 8) * g;
-#pragma unroll
-              for (int i = 0; i < D / 16; i += 2)
-                *reinterpret_cast<float4*>(dst + 2 * i) =
-                    make_float4(S.o[n][i][r], S.o[n][i][2 + r], S.o[n][i + 1][r], S.o[n][i + 1][2 + r]);
-              if (g == 0) pml[warp * kWarpRows + k] = make_float2(r ? S.m[n].y : S.m[n].x, l);
-            }
-        }
-        __syncthreads();
-        if (frow < rows)
-          for (int w = 0; w < kTileWarps && r0 + w * SPLIT < t.len; ++w) {
-            const float2 ml = pml[w * kWarpRows + frow];
-            float fa, fb;
-            join(FM, ml.x, fa, fb);
-            FL = __fmaf_rn(ml.y, fb, __fmul_rn(FL, fa));
-            for (int d = fd; d < fd + D / 4; ++d)
-              tot[frow * D + d] = __fmaf_rn(part[(w * kWarpRows + frow) * D + d], fb, __fmul_rn(tot[frow * D + d], fa));
-          }
-        __syncthreads();  // the partial results are read: the rings may be refilled
       }
       __syncthreads();
-      if (frow < rows) {
-        uint16_t* dst = out + ((int64_t)(t.first + frow / G) * Hq + kh * G + frow % G) * D + fd;
-        for (int d = 0; d < D / 4; d += D / 8) {
-          float x[D / 8];
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) x[i] = tot[frow * D + fd + d + i];
-          store_row<D>(dst + d, x, FL);
+      if (frow < rows)
+        for (int w = 0; w < kFewWarps && r0 + w * SPLIT < longest; ++w) {
+          const float2 ml = pml[w * kFewRows + frow];
+          float fa, fb;
+          join(FM, ml.x, fa, fb);
+          FL = __fmaf_rn(ml.y, fb, __fmul_rn(FL, fa));
+          for (int d = fd; d < fd + D / 4; ++d)
+            tot[frow * D + d] = __fmaf_rn(part[(w * kFewRows + frow) * D + d], fb, __fmul_rn(tot[frow * D + d], fa));
         }
+      __syncthreads();  // the partial results are read: the rings may be refilled
+    }
+    __syncthreads();
+    if (frow < rows) {
+      uint16_t* dst = out + ((int64_t)(first + frow / G) * Hq + kh * G + frow % G) * D + fd;
+      for (int d = 0; d < D / 4; d += D / 8) {
+        float x[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) x[i] = tot[frow * D + fd + d + i];
+        store_row<D>(dst + d, x, FL);
       }
     }
     __syncthreads();  // shared memory is free for the next tile

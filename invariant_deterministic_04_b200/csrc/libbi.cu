@@ -277,21 +277,47 @@ cudaError_t q8_decode(const Q8Call& a, const AttnWs& ws) {
                         (const float*)ws.po, (const float2*)ws.pml, a.R, a.rows, max_splits(a.R.max_pages), a.Hq, a.out);
 }
 
+// Tokens a prefill tile takes: of 1, 2 or 3 tiles of 8 query rows a warp, what makes the
+// CTAs' rounds over T rows (if they were one chunk) cheapest, a round costing the tiles and about
+// as much again as 0.6 of one for the work that a chunk of keys takes whatever the rows.
+int q8_tile_tokens(int64_t T, int G, int Hkv, int sms) {
+  int best = 1;
+  double least = 0;
+  for (int live = 1; live <= bi::attnq8::kNT; ++live) {
+    const int per = 8 * bi::attnq8::kTileWarps * live / G;
+    const int64_t rounds = ((T + per - 1) / per * Hkv + sms - 1) / sms;
+    const double cost = (double)rounds * (live + 0.6);
+    if (live == 1 || cost <= least) best = per, least = cost;
+  }
+  return best;
+}
+
 template <int KIND, int D>
-cudaError_t q8_prefill(const Q8Call& a, bi::attnq8::Tile* tiles, int32_t* count) {
+cudaError_t q8_prefill(const Q8Call& a, int32_t* list, bi::attnq8::Counts* counts) {
   namespace a8 = bi::attnq8;
-  auto kernel = a8::tile_kernel<KIND, D>;
-  struct Tag {};  // one set of once-flags per instantiation
-  int per_sm = 0;
-  cudaError_t e = resident_ctas<Tag>(kernel, a8::kTileWarps * 32, a8::TileSmem<D>::BYTES, a.dev, &per_sm);
+  auto tile = a8::tile_kernel<KIND, D>;
+  auto rest = a8::few_kernel<KIND, D>;
+  struct TileTag {};  // one set of once-flags per instantiation
+  struct FewTag {};
+  int tile_sm = 0, few_sm = 0;
+  cudaError_t e = resident_ctas<TileTag>(tile, a8::kTileWarps * 32, a8::TileSmem<D>::BYTES, a.dev, &tile_sm);
+  if (e == cudaSuccess) e = resident_ctas<FewTag>(rest, a8::kFewWarps * 32, a8::FewSmem<D>::BYTES, a.dev, &few_sm);
   if (e != cudaSuccess) return e;
-  e = bi::launch_pdl(a8::plan_kernel, dim3(1), dim3(1024), 0, a.st, a.R, a.rows, a8::kTileRows / (a.Hq / a.Hkv), tiles,
-                     count);
+  const int G = a.Hq / a.Hkv, few = a8::kFewRows / G, per = q8_tile_tokens(a.rows, G, a.Hkv, a.sms);
+  e = bi::launch_pdl(a8::plan_kernel, dim3(1), dim3(1024), 0, a.st, a.R.q_seq, a.rows, per, few, list, counts);
   if (e != cudaSuccess) return e;
-  const int64_t most = (int64_t)a.rows * a.Hkv, full = (int64_t)a.sms * per_sm;
-  return bi::launch_pdl(kernel, dim3((unsigned)(most < full ? most : full)), dim3(a8::kTileWarps * 32),
-                        (size_t)a8::TileSmem<D>::BYTES, a.st, a.q, a.ldq, a.Hq, a.Hkv, a.C, a.R, (const a8::Tile*)tiles,
-                        (const int32_t*)count, a.out, a.c);
+  const int64_t most = (int64_t)a.rows * a.Hkv;
+  if (a.rows > few) {  // else there are few-row tiles only
+    const int64_t full = (int64_t)a.sms * tile_sm;
+    e = bi::launch_pdl(tile, dim3((unsigned)(most < full ? most : full)), dim3(a8::kTileWarps * 32),
+                       (size_t)a8::TileSmem<D>::BYTES, a.st, a.q, a.ldq, a.Hq, a.Hkv, a.C, a.R, a.rows, per,
+                       (const int32_t*)list, counts, a.out, a.c);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t full = (int64_t)a.sms * few_sm;
+  return bi::launch_pdl(rest, dim3((unsigned)(most < full ? most : full)), dim3(a8::kFewWarps * 32),
+                        (size_t)a8::FewSmem<D>::BYTES, a.st, a.q, a.ldq, a.Hq, a.Hkv, a.C, a.R, a.rows, few,
+                        (const int32_t*)list, (const a8::Counts*)counts, a.out, a.c);
 }
 
 // ---- LM head workspace: bf16 logits [M, V], fp32 logits [M, V], flagged list [M + 1],
@@ -654,7 +680,7 @@ bi_status bi_attention_decode_q8(const bi_bf16* q, const void* k_cache, const vo
 }
 
 size_t bi_attention_prefill_q8_workspace_size(int64_t T) {
-  return T < 0 ? 0 : 256 + align256((size_t)T * sizeof(bi::attnq8::Tile));
+  return T < 0 ? 0 : 256 + align256((size_t)T * 4);
 }
 
 bi_status bi_attention_prefill_q8(const bi_bf16* q, int64_t ldq, const int32_t* q_seq, const int32_t* q_pos,
@@ -676,12 +702,12 @@ bi_status bi_attention_prefill_q8(const bi_bf16* q, int64_t ldq, const int32_t* 
   const bi::attnq8::Cache C{(const uint8_t*)k_cache, (const uint8_t*)v_cache, k_scale, v_scale, num_pages, page_table};
   const bi::attn::Rows R{nullptr, q_seq, q_pos, num_seqs, max_pages_per_seq};
   const float c = (float)((double)scale * 1.4426950408889634);  // scale * log2(e)
-  int32_t* count = static_cast<int32_t*>(workspace);
-  auto* tiles = reinterpret_cast<bi::attnq8::Tile*>(static_cast<uint8_t*>(workspace) + 256);
+  auto* counts = static_cast<bi::attnq8::Counts*>(workspace);
+  int32_t* list = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + 256);
   auto call = kind == BI_KV_INT8 ? (D == 128 ? q8_prefill<BI_KV_INT8, 128> : q8_prefill<BI_KV_INT8, 64>)
                                  : (D == 128 ? q8_prefill<BI_KV_E4M3, 128> : q8_prefill<BI_KV_E4M3, 64>);
   const Q8Call a{q, ldq, Hq, Hkv, C, R, T, out, c, sms, dev, as_stream(stream)};
-  return call(a, tiles, count) == cudaSuccess ? BI_OK : BI_ERR_CUDA;
+  return call(a, list, counts) == cudaSuccess ? BI_OK : BI_ERR_CUDA;
 }
 
 bi_status bi_qk_norm_rope(const bi_bf16* q, int64_t ldq, const bi_bf16* k, int64_t ldk, const bi_bf16* q_weight,
