@@ -690,8 +690,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
 // ---------------------------------------------------------------------------
 // Prefill: rows of one sequence that follow one another in the batch are taken in tiles, and a
 // tile and one kv-head run on one CTA. Query row i of a tile is query head i % G of token i / G.
-//   * tile_kernel, tiles of up to 192 query rows: the CTA's eight warps share out the tiles of 8
-//     query rows (1 to kNT each), and widen a chunk of keys and values once for all of them, in
+//   * tile_kernel, tiles of up to 192 query rows: the CTA's twelve warps share out the tiles of 8
+//     query rows (two each at most), and widen a chunk of keys and values once for all of them, in
 //     fragment order (every access is 16 contiguous bytes a lane), while they work on the chunk
 //     before; the bytes after that are on their way (cp.async).
 //   * few_kernel, tiles of up to kFewRows query rows (decode rows in a mixed batch, ends of
@@ -776,16 +776,33 @@ __device__ __forceinline__ int tile_tokens(const int32_t* __restrict__ q_seq, in
   return per;
 }
 
-// The page of tokens tp .. tp + 15 as a store row, or -1 past `len` or if the page is unusable.
-__device__ __forceinline__ int64_t tile_row0(const Cache& C, const int32_t* prow, int tp, int len, int Hkv, int kh) {
-  if (tp >= len) return -1;
-  const int pg = prow[tp / PAGE];
-  if (pg < 0 || pg >= C.num_pages) {
-    record_error(BI_ERR_DEVICE_INDEX);
-    return -1;
-  }
-  return ((int64_t)pg * Hkv + kh) * PAGE;
+// Page i of a sequence that is seen up to `len`: its id, or -1 past the end or if it is unusable.
+__device__ __forceinline__ int page_id(const Cache& C, const int32_t* prow, int i, int len) {
+  if (i * PAGE >= len) return -1;
+  const int pg = prow[i];
+  if (pg >= 0 && pg < C.num_pages) return pg;
+  record_error(BI_ERR_DEVICE_INDEX);
+  return -1;
 }
+
+// The ids of a sequence's pages as a walk over its chunks needs them: 32 pages from a multiple of
+// 32 on, one a lane, and the next 32 already asked for.
+struct PageIds {
+  int first, now, then;
+  __device__ __forceinline__ void start(const Cache& C, const int32_t* prow, int len, int lane) {
+    first = 0;
+    now = page_id(C, prow, lane, len);
+    then = page_id(C, prow, 32 + lane, len);
+  }
+  // Moves on to the 32 pages that page i is among (i never falls, nor rises by more than 32).
+  __device__ __forceinline__ void at(const Cache& C, const int32_t* prow, int i, int len, int lane) {
+    if (i < first + 32) return;
+    first += 32;
+    now = then;
+    then = page_id(C, prow, first + 32 + lane, len);
+  }
+  __device__ __forceinline__ int operator[](int i) const { return __shfl_sync(kFullMask, now, i & 31); }
+};
 
 // cp.async of one page (store rows row0 .. + 15) by a warp, 16 contiguous bytes a lane.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -834,16 +851,17 @@ __device__ __forceinline__ void store_row(uint16_t* dst, const float (&x)[D / 8]
   }
 }
 
-constexpr int kNT = 3;         // tiles of 8 query rows per warp, at most
-constexpr int kTileWarps = 8;
+constexpr int kNT = 2;  // tiles of 8 query rows per warp, at most
+constexpr int kTileWarps = 12;
 constexpr int kTileRows = kTileWarps * kNT * 8;
 
 template <int D>
 struct TileSmem {
-  static constexpr int PAGES = 512 / D;                      // pages a chunk: one item of each kind per warp
+  static constexpr int PAGES = 512 / D;                      // pages a chunk
+  static constexpr int ITEMS = PAGES * D / 64;               // 8 parts of its keys, and 8 of its values, to widen
   static constexpr int OPERANDS = PAGES * 2 * PAGE * D * 2;  // f16 keys, then values
   static constexpr int BUFFER = OPERANDS + PAGES * PAGE * 16;  // and {ks, log2 vs, 1 / vs, -} per token
-  static constexpr int RAW = kTileWarps * 32 * 64 + PAGES * PAGE * 8;  // one thread's 64 bytes; scales
+  static constexpr int RAW = 2 * ITEMS * 1024 + PAGES * PAGE * 8;  // the parts' bytes; scales
   static constexpr int RAW_AT = 2 * BUFFER;
   static constexpr int TOTALS = RAW_AT + 2 * RAW;            // fp32 totals [row][D], lane by lane
   static constexpr int STATS = TOTALS + kTileRows * D * 4;   // M and L, lane by lane
@@ -852,86 +870,103 @@ struct TileSmem {
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
-// Starts the copies of this thread's part of the chunk at token tp: key bytes of tokens g and
-// g + 8 and value bytes of four tokens, of the page and part that its warp widens, and a token's
+// The twelve warps' shares of chunk number `chunk`: key part `role` (0 .. 7), value part role - 4
+// (0 .. 7) and 32 tokens' scales (role - 8), where these exist; the shares move on by four warps a chunk.
+__device__ __forceinline__ int chunk_role(int warp, int chunk) { return (warp + 4 * (chunk % 3)) % kTileWarps; }
+
+// Starts the copies of this lane's part of the chunk at token tp: key bytes of tokens g and g + 8
+// and value bytes of four tokens, of one page and 64 (8 of the lane's) dims each, and a token's
 // scales. Bytes of unusable pages, and of tokens from len on, become zeros.
 template <int D>
-__device__ __forceinline__ void copy_chunk(uint32_t raw, const Cache& C, const int32_t* prow, int tp, int len, int Hkv,
-                                           int kh, int warp, int lane) {
+__device__ __forceinline__ void copy_chunk(uint32_t raw, const Cache& C, const int32_t* prow, PageIds& ids, int tp, int len,
+                                           int Hkv, int kh, int role, int lane) {
+  using M = TileSmem<D>;
   const int g = lane >> 2, c = lane & 3;
-  static_assert(TileSmem<D>::PAGES * (D / 64) == kTileWarps, "one page part a warp");
-  const int page = warp / (D / 64), part = warp % (D / 64);
-  const int t0 = tp + page * PAGE;
-  const int64_t at = tile_row0(C, prow, t0, len, Hkv, kh);
-  const bool ok = at >= 0;
-  const int64_t row0 = ok ? at : 0;
-  const uint32_t mine = raw + (uint32_t)(warp * 2048 + lane * 16);
-  const uint8_t* kp = C.k + (row0 + g) * D + 64 * part + 16 * c;
-  cp_async_or_zero<16>(mine, kp, ok);
-  cp_async_or_zero<16>(mine + 512, kp + 8 * D, ok);
-  const uint8_t* vp = C.v + (row0 + 2 * c) * D + (D / 8) * g + 8 * part;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = (i & 1) + 8 * (i >> 1);
-    cp_async_or_zero<8>(raw + (uint32_t)(warp * 2048 + 1024 + i * 256 + lane * 8), vp + t * D, ok && t0 + 2 * c + t < len);
+  static_assert(M::ITEMS == 8 && kTileWarps == 12 && M::PAGES * PAGE <= 128, "shares of a chunk");
+  ids.at(C, prow, tp / PAGE, len, lane);  // a chunk lies within 32 pages
+  if (role < 8) {
+    const int page = role / (D / 64), part = role % (D / 64);
+    const int pg = ids[tp / PAGE + page];
+    const bool ok = pg >= 0;
+    const uint8_t* kp = C.k + ((ok ? ((int64_t)pg * Hkv + kh) * PAGE : 0) + g) * D + 64 * part + 16 * c;
+    const uint32_t at = raw + (uint32_t)(role * 1024 + lane * 16);
+    cp_async_or_zero<16>(at, kp, ok);
+    cp_async_or_zero<16>(at + 512, kp + 8 * D, ok);
   }
-  const int tok = warp * 32 + lane;
-  if (tok < TileSmem<D>::PAGES * PAGE) {
-    const int64_t r = tile_row0(C, prow, tp + tok / PAGE * PAGE, len, Hkv, kh);
-    const bool seen = r >= 0 && tp + tok < len;
-    const uint32_t sc = raw + (uint32_t)(kTileWarps * 2048 + tok * 8);
-    cp_async_or_zero<4>(sc, C.ks + (seen ? r + tok % PAGE : 0), seen);
-    cp_async_or_zero<4>(sc + 4, C.vs + (seen ? r + tok % PAGE : 0), seen);
+  if (role >= 4) {
+    const int item = role - 4, page = item / (D / 64), part = item % (D / 64);
+    const int t0 = tp + page * PAGE;
+    const int pg = ids[tp / PAGE + page];
+    const bool ok = pg >= 0;
+    const uint8_t* vp = C.v + ((ok ? ((int64_t)pg * Hkv + kh) * PAGE : 0) + 2 * c) * D + (D / 8) * g + 8 * part;
+    const uint32_t at = raw + (uint32_t)((M::ITEMS + item) * 1024 + lane * 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = (i & 1) + 8 * (i >> 1);
+      cp_async_or_zero<8>(at + 256 * i, vp + t * D, ok && t0 + 2 * c + t < len);
+    }
+  }
+  const int tok = (role - 8) * 32 + lane;
+  if (role >= 8 && (role - 8) * 32 < M::PAGES * PAGE) {
+    const int pg = ids[(tp + tok) / PAGE];
+    const bool seen = pg >= 0 && tp + tok < len;
+    const int64_t r = seen ? ((int64_t)pg * Hkv + kh) * PAGE + tok % PAGE : 0;
+    const uint32_t at = raw + (uint32_t)(2 * M::ITEMS * 1024 + tok * 8);
+    cp_async_or_zero<4>(at, C.ks + r, seen);
+    cp_async_or_zero<4>(at + 4, C.vs + r, seen);
   }
   cp_commit();
 }
 
-// Widens this thread's part of a chunk (its own copies, complete) into a buffer: keys
+// Widens this lane's part of a chunk (its own copies, complete) into a buffer: keys
 // [page][step][lane], values [page][tile][lane], tokens. A token without a value scale (0) has
 // log2 -infinity: no weight.
 template <int KIND, int D>
-__device__ __forceinline__ void widen_chunk(uint32_t raw, uint32_t buf, int warp, int lane) {
+__device__ __forceinline__ void widen_chunk(uint32_t raw, uint32_t buf, int role, int lane) {
   using M = TileSmem<D>;
-  const int page = warp / (D / 64), part = warp % (D / 64);
-  const uint32_t kb = buf + ((page * (D / 16) + 4 * part) * 32 + lane) * 16;
-  const uint4 x = ld_shared_v4(raw + warp * 2048 + lane * 16), y = ld_shared_v4(raw + warp * 2048 + 512 + lane * 16);
-  const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+  if (role < 8) {
+    const int page = role / (D / 64), part = role % (D / 64);
+    const uint32_t kb = buf + ((page * (D / 16) + 4 * part) * 32 + lane) * 16, at = raw + (uint32_t)(role * 1024 + lane * 16);
+    const uint4 x = ld_shared_v4(at), y = ld_shared_v4(at + 512);
+    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-  for (int b = 0; b < 4; ++b) st_shared_v4(kb + b * 512, key_operand<KIND>(xw[b], yw[b]));
-  const uint32_t vb = buf + M::OPERANDS / 2 + ((page * (D / 16) + 4 * part) * 32 + lane) * 16;
-  uint2 v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                 : "=r"(v[i].x), "=r"(v[i].y)
-                 : "r"(raw + warp * 2048 + 1024 + i * 256 + lane * 8));
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = u ? v[i].y : v[i].x;
-    uint4 a, b;
-    value_operands<KIND>(w, a, b);
-    st_shared_v4(vb + (2 * u) * 512, a);
-    st_shared_v4(vb + (2 * u + 1) * 512, b);
+    for (int b = 0; b < 4; ++b) st_shared_v4(kb + b * 512, key_operand<KIND>(xw[b], yw[b]));
   }
-  const int tok = warp * 32 + lane;
-  if (tok < M::PAGES * PAGE) {
-    const uint32_t sc = raw + (uint32_t)(kTileWarps * 2048 + tok * 8);
+  if (role >= 4) {
+    const int item = role - 4, page = item / (D / 64), part = item % (D / 64);
+    const uint32_t vb = buf + M::OPERANDS / 2 + ((page * (D / 16) + 4 * part) * 32 + lane) * 16;
+    const uint32_t at = raw + (uint32_t)((M::ITEMS + item) * 1024 + lane * 8);
+    uint2 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[i].x), "=r"(v[i].y) : "r"(at + 256 * i));
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = u ? v[i].y : v[i].x;
+      uint4 a, b;
+      value_operands<KIND>(w, a, b);
+      st_shared_v4(vb + (2 * u) * 512, a);
+      st_shared_v4(vb + (2 * u + 1) * 512, b);
+    }
+  }
+  const int tok = (role - 8) * 32 + lane;
+  if (role >= 8 && (role - 8) * 32 < M::PAGES * PAGE) {
+    const uint32_t sc = raw + (uint32_t)(2 * M::ITEMS * 1024 + tok * 8);
     const float ks = ld_shared_f32(sc), vs = ld_shared_f32(sc + 4);
     const float4 t = make_float4(ks, lg2(vs), vs == 0.f ? 0.f : rcp(vs), 0.f);
     st_shared_v4(buf + M::OPERANDS + tok * 16, *reinterpret_cast<const uint4*>(&t));
   }
 }
 
-// Folds one page of a buffer into the warp's LIVE tiles.
-template <int D, int LIVE, bool MASKED>
-__device__ __forceinline__ void fold_wide(const Query<D, LIVE>& Q, uint32_t buf, int page, const int (&nv)[LIVE][2],
-                                          int lane, State<D, LIVE>& S) {
-  using M = TileSmem<D>;
-  const int g = lane >> 2;
-  float s[LIVE][4];
-  const uint32_t kb = buf + (page * (D / 16) * 32 + lane) * 16, vb = kb + M::OPERANDS / 2;
+// The CTA's barrier; its warps may meet it in different instantiations of run_tile.
+__device__ __forceinline__ void tile_sync() { asm volatile("barrier.cta.sync 0, %0;" ::"n"(kTileWarps * 32) : "memory"); }
+
+// Scores of one page of a buffer for the warp's LIVE tiles, and a page's tokens.
+template <int D, int LIVE>
+__device__ __forceinline__ void wide_scores(const Query<D, LIVE>& Q, uint32_t buf, int page, int lane, float (&s)[LIVE][4]) {
+  const uint32_t kb = buf + (page * (D / 16) * 32 + lane) * 16;
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) {
     const uint4 a = ld_shared_v4(kb + j * 512);
@@ -941,21 +976,90 @@ __device__ __forceinline__ void fold_wide(const Query<D, LIVE>& Q, uint32_t buf,
       else mma16816(s[n], a, Q.b[n][j][0], Q.b[n][j][1]);
     }
   }
+}
+template <int D>
+__device__ __forceinline__ Tokens wide_tokens(uint32_t buf, int page, int lane) {
   Tokens T;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const uint4 x = ld_shared_v4(buf + M::OPERANDS + (page * PAGE + g + 8 * t) * 16);
+    const uint4 x = ld_shared_v4(buf + TileSmem<D>::OPERANDS + (page * PAGE + (lane >> 2) + 8 * t) * 16);
     T.ks[t] = __uint_as_float(x.x);
     T.lg[t] = __uint_as_float(x.y);
     T.ri[t] = __uint_as_float(x.z);
   }
-  uint32_t w[LIVE][2];
-  page_weights<D, LIVE, MASKED>(Q, s, T, nv, g, LIVE, S, w);
+  return T;
+}
+template <int D, int LIVE>
+__device__ __forceinline__ void wide_values(uint32_t buf, int page, int lane, const uint32_t (&w)[LIVE][2],
+                                            State<D, LIVE>& S) {
+  const uint32_t vb = buf + TileSmem<D>::OPERANDS / 2 + (page * (D / 16) * 32 + lane) * 16;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
     const uint4 a = ld_shared_v4(vb + i * 512);
 #pragma unroll
     for (int n = 0; n < LIVE; ++n) mma16816(S.o[n][i], a, w[n][0], w[n][1]);
+  }
+}
+
+// Folds one page of a buffer into the warp's LIVE tiles; query row (n, e) sees nv[n][e] tokens of it.
+template <int D, int LIVE>
+__device__ __forceinline__ void fold_wide_masked(const Query<D, LIVE>& Q, uint32_t buf, int page,
+                                                 const int (&nv)[LIVE][2], int lane, State<D, LIVE>& S) {
+  float s[LIVE][4];
+  wide_scores<D, LIVE>(Q, buf, page, lane, s);
+  const Tokens T = wide_tokens<D>(buf, page, lane);
+  uint32_t w[LIVE][2];
+  page_weights<D, LIVE, true>(Q, s, T, nv, lane >> 2, LIVE, S, w);
+  wide_values<D, LIVE>(buf, page, lane, w, S);
+}
+
+// Folds four whole pages of a buffer from `page` on, all of them seen by every query row. The
+// scores of a page are issued before the weights of the page before it, in one straight line
+// of code, so that the tensor cores work through the softmax; the one vote of a page asks whether
+// any row has to move its reference, and only then are the weights taken tile by tile as
+// tile_weights does (the values are the same either way).
+template <int D, int LIVE>
+__device__ __forceinline__ void fold_wide_pages(const Query<D, LIVE>& Q, uint32_t buf, int page, int lane, State<D, LIVE>& S) {
+  float s[2][LIVE][4];
+  wide_scores<D, LIVE>(Q, buf, page, lane, s[0]);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (u < 3) wide_scores<D, LIVE>(Q, buf, page + u + 1, lane, s[(u + 1) & 1]);
+    const Tokens T = wide_tokens<D>(buf, page + u, lane);
+    uint32_t w[LIVE][2];
+    float2 l[LIVE];
+    bool over = false;
+#pragma unroll
+    for (int n = 0; n < LIVE; ++n) {
+      const float (&sn)[4] = s[u & 1][n];
+      const float2 ref = make_float2(__fsub_rn(7.f, S.m[n].x), __fsub_rn(7.f, S.m[n].y));
+      l[n] = S.l[n];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float2 z = __ffma2_rn(make_float2(sn[2 * t], sn[2 * t + 1]), __fmul2_rn(make_float2(T.ks[t], T.ks[t]), Q.c[n]),
+                                    make_float2(T.lg[t], T.lg[t]));
+        const float2 x = __fadd2_rn(z, ref);
+        const float2 p = make_float2(ex2(x.x), ex2(x.y));
+        w[n][t] = pack_f16x2(p.x, p.y);
+        l[n] = __ffma2_rn(p, make_float2(T.ri[t], T.ri[t]), l[n]);
+      }
+      const __half2 top = __hmax2(*reinterpret_cast<__half2*>(&w[n][0]), *reinterpret_cast<__half2*>(&w[n][1]));
+      over |= !__hble2(top, __halves2half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800)));  // 2^15
+    }
+    if (__any_sync(kFullMask, over)) {
+      const int all[2] = {PAGE, PAGE};
+#pragma unroll
+      for (int n = 0; n < LIVE; ++n)
+        tile_weights<D, false>(Q.c[n], s[u & 1][n], T, all, lane >> 2, S.m[n], S.l[n], S.o[n], w[n]);
+    } else {
+#pragma unroll
+      for (int n = 0; n < LIVE; ++n) {
+        S.l[n] = l[n];
+        w[n][0] = transpose8x8(w[n][0]);
+        w[n][1] = transpose8x8(w[n][1]);
+      }
+    }
+    wide_values<D, LIVE>(buf, page + u, lane, w, S);
   }
 }
 
@@ -971,14 +1075,16 @@ struct TileArgs {
   float scale_log2;
 };
 
-// One tile on a CTA whose warps have LIVE tiles of 8 query rows at most (the warp's n-th is tile
-// 8 n + warp). Rows past the tile's end are zeros whose results go nowhere.
+// One tile on the CTA for a warp with LIVE (or LIVE - 1) of its tiles of 8 query rows: the warp's
+// n-th is tile 12 n + warp. Rows past the tile's end are zeros whose results go nowhere.
 template <int KIND, int D, int LIVE>
 __device__ __noinline__ void run_tile(const TileArgs A, uint32_t base, float* totals, int warp, int lane) {
   using M = TileSmem<D>;
   const int g = lane >> 2, c = lane & 3;
   constexpr int CHUNK = M::PAGES * PAGE;
-  copy_chunk<D>(base + M::RAW_AT, A.C, A.prow, 0, A.len, A.Hkv, A.kh, warp, lane);
+  PageIds ids;
+  ids.start(A.C, A.prow, A.len, lane);
+  copy_chunk<D>(base + M::RAW_AT, A.C, A.prow, ids, 0, A.len, A.Hkv, A.kh, chunk_role(warp, 0), lane);
   Query<D, LIVE> Q;
   int shortest = INT_MAX, longest = 0;
   auto len_of = [&](int n, int r) {  // visible tokens of the lane's query row (n, r)
@@ -1011,37 +1117,43 @@ __device__ __noinline__ void run_tile(const TileArgs A, uint32_t base, float* to
   for (int i = 0; i < LIVE * D / 4; ++i) tot[32 * i] = 0.f;
 
   cp_wait<0>();
-  widen_chunk<KIND, D>(base + M::RAW_AT, base, warp, lane);
-  if (CHUNK < A.len) copy_chunk<D>(base + M::RAW_AT + M::RAW, A.C, A.prow, CHUNK, A.len, A.Hkv, A.kh, warp, lane);
+  widen_chunk<KIND, D>(base + M::RAW_AT, base, chunk_role(warp, 0), lane);
+  if (CHUNK < A.len)
+    copy_chunk<D>(base + M::RAW_AT + M::RAW, A.C, A.prow, ids, CHUNK, A.len, A.Hkv, A.kh, chunk_role(warp, 1), lane);
   int b = 0;
   for (int t0 = 0; t0 < A.len; t0 += SPLIT) {
     State<D, LIVE> S;
     S.clear();
     for (int tp = t0; tp < min(t0 + SPLIT, A.len); tp += CHUNK, b ^= 1) {
-      __syncthreads();  // this chunk is widened, and every warp is done with the buffer of the one before
+      tile_sync();  // this chunk is widened, and every warp is done with the buffer of the one before
       // the next chunk is widened before this one is folded by half of the warps, after it by the
-      // other half, so that a scheduler's two warps do not both widen while the tensor cores wait
+      // other half, so that a scheduler's warps do not all widen while the tensor cores wait
       auto next = [&] {
         if (tp + CHUNK >= A.len) return;
         cp_wait<0>();
-        widen_chunk<KIND, D>(base + M::RAW_AT + (b ^ 1) * M::RAW, base + (b ^ 1) * M::BUFFER, warp, lane);
+        const int chunk = tp / CHUNK;
+        widen_chunk<KIND, D>(base + M::RAW_AT + (b ^ 1) * M::RAW, base + (b ^ 1) * M::BUFFER, chunk_role(warp, chunk + 1), lane);
         if (tp + 2 * CHUNK < A.len)
-          copy_chunk<D>(base + M::RAW_AT + b * M::RAW, A.C, A.prow, tp + 2 * CHUNK, A.len, A.Hkv, A.kh, warp, lane);
+          copy_chunk<D>(base + M::RAW_AT + b * M::RAW, A.C, A.prow, ids, tp + 2 * CHUNK, A.len, A.Hkv, A.kh,
+                        chunk_role(warp, chunk + 2), lane);
       };
       if (warp < kTileWarps / 2) next();
 #pragma unroll 1
-      for (int p = 0; p < M::PAGES; ++p) {
+      for (int p = 0; p < M::PAGES; p += 4) {
         const int at = tp + p * PAGE;
         if (at >= longest) break;
-        int nv[LIVE][2];
-        if (at + PAGE <= shortest) {
-          fold_wide<D, LIVE, false>(Q, base + b * M::BUFFER, p, nv, lane, S);
-        } else {
+        if (at + 4 * PAGE <= shortest) {
+          fold_wide_pages<D, LIVE>(Q, base + b * M::BUFFER, p, lane, S);
+          continue;
+        }
+#pragma unroll 1
+        for (int u = 0; u < 4 && at + u * PAGE < longest; ++u) {
+          int nv[LIVE][2];
 #pragma unroll
           for (int n = 0; n < LIVE; ++n)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) nv[n][r] = len_of(n, r) - at;
-          fold_wide<D, LIVE, true>(Q, base + b * M::BUFFER, p, nv, lane, S);
+            for (int r = 0; r < 2; ++r) nv[n][r] = len_of(n, r) - at - u * PAGE;
+          fold_wide_masked<D, LIVE>(Q, base + b * M::BUFFER, p + u, nv, lane, S);
         }
       }
       if (warp >= kTileWarps / 2) next();
@@ -1094,7 +1206,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
   const int total = counts->tiles * Hkv;
   while (true) {
     if (threadIdx.x == 0) misc[0] = atomicAdd(&counts->next, 1);  // who takes which item is all this decides
-    __syncthreads();
+    tile_sync();
     const int item = total - 1 - misc[0];  // later rows of a prompt see more keys: longest first
     if (item < 0) return;
     TileArgs A;
@@ -1115,10 +1227,9 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1)
     A.prow = C.pt + (int64_t)pt_row * R.max_pages;
     float* totals = reinterpret_cast<float*>(smem + M::TOTALS);
     const int tiles = (A.rows + 7) / 8;  // of 8 query rows
-    if (tiles > 2 * kTileWarps) run_tile<KIND, D, 3>(A, base, totals, warp, lane);
-    else if (tiles > kTileWarps) run_tile<KIND, D, 2>(A, base, totals, warp, lane);
+    if (tiles > kTileWarps + warp) run_tile<KIND, D, 2>(A, base, totals, warp, lane);
     else run_tile<KIND, D, 1>(A, base, totals, warp, lane);
-    __syncthreads();  // shared memory is free for the next tile
+    tile_sync();  // shared memory is free for the next tile
   }
 }
 
@@ -1194,10 +1305,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3)
       S.clear();
       const int np = seen > 0 ? (seen + PAGE - 1) / PAGE : 0;
       int page = -1;
-      if (lane < np) {
-        const int64_t row0 = tile_row0(C, prow, t0 + lane * PAGE, longest, Hkv, kh);
-        page = row0 < 0 ? -1 : (int)(row0 / (Hkv * PAGE));
-      }
+      if (lane < np) page = page_id(C, prow, t0 / PAGE + lane, longest);
       auto issue = [&](int j) {
         if (j < np) {
           const int pg = __shfl_sync(kFullMask, page, j);

@@ -277,17 +277,17 @@ cudaError_t q8_decode(const Q8Call& a, const AttnWs& ws) {
                         (const float*)ws.po, (const float2*)ws.pml, a.R, a.rows, max_splits(a.R.max_pages), a.Hq, a.out);
 }
 
-// Tokens a prefill tile takes: of 1, 2 or 3 tiles of 8 query rows a warp, what makes the
-// CTAs' rounds over T rows (if they were one chunk) cheapest, a round costing the tiles and about
-// as much again as 0.6 of one for the work that a chunk of keys takes whatever the rows.
+// Tokens a prefill tile takes. A CTA's twelve warps sit on four schedulers, so its time goes by
+// the tiles of 8 query rows a scheduler has (1 to 6), and about one more for the work that a chunk of
+// keys takes whatever the rows; take what makes the CTAs' rounds over T rows (as if they were one
+// chunk) cheapest, the larger tile among equals.
 int q8_tile_tokens(int64_t T, int G, int Hkv, int sms) {
   int best = 1;
-  double least = 0;
-  for (int live = 1; live <= bi::attnq8::kNT; ++live) {
-    const int per = 8 * bi::attnq8::kTileWarps * live / G;
+  int64_t least = 0;
+  for (int k = 1; k <= bi::attnq8::kTileRows / 32; ++k) {
+    const int per = 32 * k / G;
     const int64_t rounds = ((T + per - 1) / per * Hkv + sms - 1) / sms;
-    const double cost = (double)rounds * (live + 0.6);
-    if (live == 1 || cost <= least) best = per, least = cost;
+    if (k == 1 || rounds * (k + 1) <= least) best = per, least = rounds * (k + 1);
   }
   return best;
 }
