@@ -690,10 +690,9 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
 // ---------------------------------------------------------------------------
 // Prefill: rows of one sequence that follow one another in the batch are taken in tiles, and a
 // tile and one kv-head run on one CTA. Query row i of a tile is query head i % G of token i / G.
-//   * tile_kernel, tiles of up to 192 query rows: the CTA's twelve warps share out the tiles of 8
-//     query rows (two each at most), and widen a chunk of keys and values once for all of them, in
-//     fragment order (every access is 16 contiguous bytes a lane), while they work on the chunk
-//     before; the bytes after that are on their way (cp.async).
+//   * tile_kernel, tiles of up to 192 query rows: eight warps share out the tiles of 8 query rows
+//     (three each at most), and four more widen keys and values once for all of them into a ring of
+//     stages in shared memory, in fragment order (every access is 16 contiguous bytes a lane).
 //   * few_kernel, tiles of up to kFewRows query rows (decode rows in a mixed batch, ends of
 //     chunks): every warp takes all the rows and every fourth split, reading pages as decode does,
 //     and the CTA folds four splits at a time.
@@ -824,15 +823,6 @@ __device__ __forceinline__ void copy_page(uint32_t page, uint32_t scales, const 
   if (lane < 8) cp_async16(scales + 16 * lane, (lane < 4 ? C.ks + row0 : C.vs + row0 - PAGE) + 4 * lane);
 }
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void* src, bool take) {
-  const int n = take ? BYTES : 0;  // the rest of the BYTES is filled with zeros
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
-}
-
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
@@ -851,117 +841,108 @@ __device__ __forceinline__ void store_row(uint16_t* dst, const float (&x)[D / 8]
   }
 }
 
-constexpr int kNT = 2;  // tiles of 8 query rows per warp, at most
-constexpr int kTileWarps = 12;
-constexpr int kTileRows = kTileWarps * kNT * 8;
+constexpr int kNT = 3;          // tiles of 8 query rows per folding warp, at most
+constexpr int kFoldWarps = 8;
+constexpr int kWidenWarps = 4;
+constexpr int kTileThreads = (kFoldWarps + kWidenWarps) * 32;
+constexpr int kTileRows = kFoldWarps * kNT * 8;
+constexpr int kRing = 4;
+// Registers: 384 threads start with 168 each; the widening warps keep 56 and the folding warps
+// take 224 (128 * 56 + 256 * 224 = 384 * 168).
+constexpr int kWidenRegs = 56, kFoldRegs = 224;
 
 template <int D>
 struct TileSmem {
-  static constexpr int PAGES = 512 / D;                      // pages a chunk
-  static constexpr int ITEMS = PAGES * D / 64;               // 8 parts of its keys, and 8 of its values, to widen
+  static constexpr int PAGES = 256 / D;                      // pages a stage: one part of each kind per widening warp
   static constexpr int OPERANDS = PAGES * 2 * PAGE * D * 2;  // f16 keys, then values
-  static constexpr int BUFFER = OPERANDS + PAGES * PAGE * 16;  // and {ks, log2 vs, 1 / vs, -} per token
-  static constexpr int RAW = 2 * ITEMS * 1024 + PAGES * PAGE * 8;  // the parts' bytes; scales
-  static constexpr int RAW_AT = 2 * BUFFER;
-  static constexpr int TOTALS = RAW_AT + 2 * RAW;            // fp32 totals [row][D], lane by lane
+  static constexpr int STAGE = OPERANDS + PAGES * PAGE * 16;  // and {ks, log2 vs, 1 / vs, -} per token
+  static constexpr int TOTALS = kRing * STAGE;               // fp32 totals [row][D], lane by lane
   static constexpr int STATS = TOTALS + kTileRows * D * 4;   // M and L, lane by lane
-  static constexpr int MISC = STATS + kTileWarps * 32 * kNT * 16;
-  static constexpr int BYTES = MISC + 64;
+  static constexpr int LENS = STATS + kFoldWarps * 32 * kNT * 16;  // visible lengths, lane by lane
+  static constexpr int BARS = LENS + kFoldWarps * 32 * kNT * 8;
+  static constexpr int ARGS = BARS + kRing * 16;                   // the item, and what its tile is
+  static constexpr int BYTES = ARGS + 16 + 256;
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
-// The twelve warps' shares of chunk number `chunk`: key part `role` (0 .. 7), value part role - 4
-// (0 .. 7) and 32 tokens' scales (role - 8), where these exist; the shares move on by four warps a chunk.
-__device__ __forceinline__ int chunk_role(int warp, int chunk) { return (warp + 4 * (chunk % 3)) % kTileWarps; }
+// A lane's part of a stage on its way: key bytes of tokens g and g + 8 and value bytes of four
+// tokens, of one page and 64 (8 of the lane's) dims each, and a token's scales.
+struct Raw {
+  uint4 k[2];
+  uint2 v[4];
+  float ks, vs;
+};
 
-// Starts the copies of this lane's part of the chunk at token tp: key bytes of tokens g and g + 8
-// and value bytes of four tokens, of one page and 64 (8 of the lane's) dims each, and a token's
-// scales. Bytes of unusable pages, and of tokens from len on, become zeros.
+// Loads the part of the stage at token tp that widening warp `warp` owns. Bytes of unusable pages,
+// and of tokens from len on, are zeros.
 template <int D>
-__device__ __forceinline__ void copy_chunk(uint32_t raw, const Cache& C, const int32_t* prow, PageIds& ids, int tp, int len,
-                                           int Hkv, int kh, int role, int lane) {
+__device__ __forceinline__ void load_raw(Raw& X, const Cache& C, const int32_t* prow, PageIds& ids, int tp, int len, int Hkv,
+                                         int kh, int warp, int lane) {
   using M = TileSmem<D>;
+  static_assert(M::PAGES * (D / 64) == kWidenWarps && M::PAGES * PAGE <= kWidenWarps * 32, "one part a warp");
   const int g = lane >> 2, c = lane & 3;
-  static_assert(M::ITEMS == 8 && kTileWarps == 12 && M::PAGES * PAGE <= 128, "shares of a chunk");
-  ids.at(C, prow, tp / PAGE, len, lane);  // a chunk lies within 32 pages
-  if (role < 8) {
-    const int page = role / (D / 64), part = role % (D / 64);
-    const int pg = ids[tp / PAGE + page];
-    const bool ok = pg >= 0;
-    const uint8_t* kp = C.k + ((ok ? ((int64_t)pg * Hkv + kh) * PAGE : 0) + g) * D + 64 * part + 16 * c;
-    const uint32_t at = raw + (uint32_t)(role * 1024 + lane * 16);
-    cp_async_or_zero<16>(at, kp, ok);
-    cp_async_or_zero<16>(at + 512, kp + 8 * D, ok);
-  }
-  if (role >= 4) {
-    const int item = role - 4, page = item / (D / 64), part = item % (D / 64);
-    const int t0 = tp + page * PAGE;
-    const int pg = ids[tp / PAGE + page];
-    const bool ok = pg >= 0;
-    const uint8_t* vp = C.v + ((ok ? ((int64_t)pg * Hkv + kh) * PAGE : 0) + 2 * c) * D + (D / 8) * g + 8 * part;
-    const uint32_t at = raw + (uint32_t)((M::ITEMS + item) * 1024 + lane * 8);
+  ids.at(C, prow, tp / PAGE, len, lane);  // a stage lies within 32 pages
+  const int page = warp / (D / 64), part = warp % (D / 64);
+  const int t0 = tp + page * PAGE;
+  const int pg = ids[t0 / PAGE];
+  const bool ok = pg >= 0;
+  const int64_t row0 = ok ? ((int64_t)pg * Hkv + kh) * PAGE : 0;
+  const uint8_t* kp = C.k + (row0 + g) * D + 64 * part + 16 * c;
+  X.k[0] = ok ? __ldg(reinterpret_cast<const uint4*>(kp)) : make_uint4(0, 0, 0, 0);
+  X.k[1] = ok ? __ldg(reinterpret_cast<const uint4*>(kp + 8 * D)) : make_uint4(0, 0, 0, 0);
+  const uint8_t* vp = C.v + (row0 + 2 * c) * D + (D / 8) * g + 8 * part;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = (i & 1) + 8 * (i >> 1);
-      cp_async_or_zero<8>(at + 256 * i, vp + t * D, ok && t0 + 2 * c + t < len);
+  for (int i = 0; i < 4; ++i) {
+    const int t = (i & 1) + 8 * (i >> 1);
+    X.v[i] = ok && t0 + 2 * c + t < len ? __ldg(reinterpret_cast<const uint2*>(vp + t * D)) : make_uint2(0, 0);
+  }
+  X.ks = 0.f;
+  X.vs = 0.f;
+  if (warp * 32 < M::PAGES * PAGE) {
+    const int tok = warp * 32 + lane, tpg = ids[(tp + tok) / PAGE];
+    if (tpg >= 0 && tp + tok < len) {
+      const int64_t r = ((int64_t)tpg * Hkv + kh) * PAGE + tok % PAGE;
+      X.ks = __ldg(C.ks + r);
+      X.vs = __ldg(C.vs + r);
     }
   }
-  const int tok = (role - 8) * 32 + lane;
-  if (role >= 8 && (role - 8) * 32 < M::PAGES * PAGE) {
-    const int pg = ids[(tp + tok) / PAGE];
-    const bool seen = pg >= 0 && tp + tok < len;
-    const int64_t r = seen ? ((int64_t)pg * Hkv + kh) * PAGE + tok % PAGE : 0;
-    const uint32_t at = raw + (uint32_t)(2 * M::ITEMS * 1024 + tok * 8);
-    cp_async_or_zero<4>(at, C.ks + r, seen);
-    cp_async_or_zero<4>(at + 4, C.vs + r, seen);
-  }
-  cp_commit();
 }
 
-// Widens this lane's part of a chunk (its own copies, complete) into a buffer: keys
-// [page][step][lane], values [page][tile][lane], tokens. A token without a value scale (0) has
-// log2 -infinity: no weight.
+// Widens a loaded part into a stage: keys [page][step][lane], values [page][tile][lane], tokens. A
+// token without a value scale (0) has log2 -infinity: no weight.
 template <int KIND, int D>
-__device__ __forceinline__ void widen_chunk(uint32_t raw, uint32_t buf, int role, int lane) {
+__device__ __forceinline__ void widen_raw(const Raw& X, uint32_t stage, int warp, int lane) {
   using M = TileSmem<D>;
-  if (role < 8) {
-    const int page = role / (D / 64), part = role % (D / 64);
-    const uint32_t kb = buf + ((page * (D / 16) + 4 * part) * 32 + lane) * 16, at = raw + (uint32_t)(role * 1024 + lane * 16);
-    const uint4 x = ld_shared_v4(at), y = ld_shared_v4(at + 512);
-    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+  const int page = warp / (D / 64), part = warp % (D / 64);
+  const uint32_t kb = stage + ((page * (D / 16) + 4 * part) * 32 + lane) * 16;
+  const uint32_t xw[4] = {X.k[0].x, X.k[0].y, X.k[0].z, X.k[0].w}, yw[4] = {X.k[1].x, X.k[1].y, X.k[1].z, X.k[1].w};
 #pragma unroll
-    for (int b = 0; b < 4; ++b) st_shared_v4(kb + b * 512, key_operand<KIND>(xw[b], yw[b]));
+  for (int b = 0; b < 4; ++b) st_shared_v4(kb + b * 512, key_operand<KIND>(xw[b], yw[b]));
+  const uint32_t vb = kb + M::OPERANDS / 2;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = u ? X.v[i].y : X.v[i].x;
+    uint4 a, b;
+    value_operands<KIND>(w, a, b);
+    st_shared_v4(vb + (2 * u) * 512, a);
+    st_shared_v4(vb + (2 * u + 1) * 512, b);
   }
-  if (role >= 4) {
-    const int item = role - 4, page = item / (D / 64), part = item % (D / 64);
-    const uint32_t vb = buf + M::OPERANDS / 2 + ((page * (D / 16) + 4 * part) * 32 + lane) * 16;
-    const uint32_t at = raw + (uint32_t)((M::ITEMS + item) * 1024 + lane * 8);
-    uint2 v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[i].x), "=r"(v[i].y) : "r"(at + 256 * i));
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = u ? v[i].y : v[i].x;
-      uint4 a, b;
-      value_operands<KIND>(w, a, b);
-      st_shared_v4(vb + (2 * u) * 512, a);
-      st_shared_v4(vb + (2 * u + 1) * 512, b);
-    }
-  }
-  const int tok = (role - 8) * 32 + lane;
-  if (role >= 8 && (role - 8) * 32 < M::PAGES * PAGE) {
-    const uint32_t sc = raw + (uint32_t)(2 * M::ITEMS * 1024 + tok * 8);
-    const float ks = ld_shared_f32(sc), vs = ld_shared_f32(sc + 4);
-    const float4 t = make_float4(ks, lg2(vs), vs == 0.f ? 0.f : rcp(vs), 0.f);
-    st_shared_v4(buf + M::OPERANDS + tok * 16, *reinterpret_cast<const uint4*>(&t));
+  if (warp * 32 < M::PAGES * PAGE) {
+    const float4 t = make_float4(X.ks, lg2(X.vs), X.vs == 0.f ? 0.f : rcp(X.vs), 0.f);
+    st_shared_v4(stage + M::OPERANDS + (warp * 32 + lane) * 16, *reinterpret_cast<const uint4*>(&t));
   }
 }
 
-// The CTA's barrier; its warps may meet it in different instantiations of run_tile.
-__device__ __forceinline__ void tile_sync() { asm volatile("barrier.cta.sync 0, %0;" ::"n"(kTileWarps * 32) : "memory"); }
+// The CTA's barrier; its warps meet it in different places.
+__device__ __forceinline__ void tile_sync() { asm volatile("barrier.cta.sync 0, %0;" ::"n"(kTileThreads) : "memory"); }
+
+// A wait that, once one of this thread's has given up (recorded), is skipped: the CTA then runs to
+// its end with wrong numbers instead of waiting again at every stage.
+__device__ __forceinline__ void ring_wait(uint32_t bar, uint32_t parity, bool& dead) {
+  if (!dead) dead = !mbar_wait(bar, parity);
+}
 
 // Scores of one page of a buffer for the warp's LIVE tiles, and a page's tokens.
 template <int D, int LIVE>
@@ -1013,18 +994,20 @@ __device__ __forceinline__ void fold_wide_masked(const Query<D, LIVE>& Q, uint32
   wide_values<D, LIVE>(buf, page, lane, w, S);
 }
 
-// Folds four whole pages of a buffer from `page` on, all of them seen by every query row. The
+// Folds two whole pages of a buffer from `page` on, both of them seen by every query row. The
 // scores of a page are issued before the weights of the page before it, in one straight line
 // of code, so that the tensor cores work through the softmax; the one vote of a page asks whether
 // any row has to move its reference, and only then are the weights taken tile by tile as
 // tile_weights does (the values are the same either way).
 template <int D, int LIVE>
 __device__ __forceinline__ void fold_wide_pages(const Query<D, LIVE>& Q, uint32_t buf, int page, int lane, State<D, LIVE>& S) {
+  constexpr bool AHEAD = LIVE < 3;  // (three tiles leave no registers for a second page's scores)
   float s[2][LIVE][4];
   wide_scores<D, LIVE>(Q, buf, page, lane, s[0]);
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    if (u < 3) wide_scores<D, LIVE>(Q, buf, page + u + 1, lane, s[(u + 1) & 1]);
+  for (int u = 0; u < 2; ++u) {
+    if (u == 0 && AHEAD) wide_scores<D, LIVE>(Q, buf, page + 1, lane, s[1]);
+    if (u == 1 && !AHEAD) wide_scores<D, LIVE>(Q, buf, page + 1, lane, s[1]);
     const Tokens T = wide_tokens<D>(buf, page + u, lane);
     uint32_t w[LIVE][2];
     float2 l[LIVE];
@@ -1074,89 +1057,77 @@ struct TileArgs {
   int Hq, Hkv, G, first, rows, kh, len;
   float scale_log2;
 };
+static_assert(sizeof(TileArgs) <= 256, "room in shared memory");
 
-// One tile on the CTA for a warp with LIVE (or LIVE - 1) of its tiles of 8 query rows: the warp's
-// n-th is tile 12 n + warp. Rows past the tile's end are zeros whose results go nowhere.
+// One tile for a folding warp with LIVE (or fewer) of its tiles of 8 query rows: the warp's n-th is
+// tile 8 n + warp. Rows past the tile's end are zeros whose results go nowhere. `it` counts the
+// ring's stages.
 template <int KIND, int D, int LIVE>
-__device__ __noinline__ void run_tile(const TileArgs A, uint32_t base, float* totals, int warp, int lane) {
+__device__ __forceinline__ void fold_tile(const TileArgs& A, uint8_t* smem, uint32_t base, uint32_t bars, uint32_t& it,
+                                          bool& dead, int warp, int lane) {
   using M = TileSmem<D>;
   const int g = lane >> 2, c = lane & 3;
   constexpr int CHUNK = M::PAGES * PAGE;
-  PageIds ids;
-  ids.start(A.C, A.prow, A.len, lane);
-  copy_chunk<D>(base + M::RAW_AT, A.C, A.prow, ids, 0, A.len, A.Hkv, A.kh, chunk_role(warp, 0), lane);
   Query<D, LIVE> Q;
   int shortest = INT_MAX, longest = 0;
-  auto len_of = [&](int n, int r) {  // visible tokens of the lane's query row (n, r)
-    const int k = (n * kTileWarps + warp) * 8 + 2 * c + r;
-    int pt_row;
-    return k < A.rows ? attn::row_len(A.R, A.first + k / A.G, pt_row) : -1;
-  };
+  // visible tokens of the lane's query rows, and running totals over splits, in places of this lane's own
+  int2* lens = reinterpret_cast<int2*>(smem + M::LENS) + warp * 32 * kNT + lane;               // entry n at [32 n]
+  float* tot = reinterpret_cast<float*>(smem + M::TOTALS) + warp * (kNT * 8) * D + lane;       // entry i at [32 i]
+  float4* stats = reinterpret_cast<float4*>(smem + M::STATS) + warp * 32 * kNT + lane;         // M and L, entry n at [32 n]
 #pragma unroll
   for (int n = 0; n < LIVE; ++n) {
-    const int i = (n * kTileWarps + warp) * 8 + g;
+    const int i = (n * kFoldWarps + warp) * 8 + g;
     load_query<D, LIVE>(Q, n,
                         i < A.rows ? A.q + (int64_t)(A.first + i / A.G) * A.ldq + (int64_t)(A.kh * A.G + i % A.G) * D : nullptr,
                         lane, A.scale_log2);
+    int len[2] = {0, 0};
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int len = len_of(n, r);
-      if (len < 0) continue;
-      longest = max(longest, len);
-      shortest = min(shortest, len);
+      const int k = (n * kFoldWarps + warp) * 8 + 2 * c + r;
+      if (k >= A.rows) continue;
+      int pt_row;
+      len[r] = attn::row_len(A.R, A.first + k / A.G, pt_row);
+      longest = max(longest, len[r]);
+      shortest = min(shortest, len[r]);
     }
+    lens[32 * n] = make_int2(len[0], len[1]);
   }
   longest = __reduce_max_sync(kFullMask, longest);
   shortest = __reduce_min_sync(kFullMask, shortest);
-  // running totals over splits, in places of this lane's own: totals, M and L
-  float* tot = totals + warp * (kNT * 8) * D + lane;  // entry i at tot[32 i]
-  float4* stats = reinterpret_cast<float4*>(totals + kTileRows * D) + warp * 32 * kNT + lane;  // entry n at [32 n]
 #pragma unroll
   for (int n = 0; n < LIVE; ++n) stats[32 * n] = make_float4(kLowest, kLowest, 0.f, 0.f);
 #pragma unroll 8
   for (int i = 0; i < LIVE * D / 4; ++i) tot[32 * i] = 0.f;
-
-  cp_wait<0>();
-  widen_chunk<KIND, D>(base + M::RAW_AT, base, chunk_role(warp, 0), lane);
-  if (CHUNK < A.len)
-    copy_chunk<D>(base + M::RAW_AT + M::RAW, A.C, A.prow, ids, CHUNK, A.len, A.Hkv, A.kh, chunk_role(warp, 1), lane);
-  int b = 0;
+#pragma unroll 1
   for (int t0 = 0; t0 < A.len; t0 += SPLIT) {
     State<D, LIVE> S;
     S.clear();
-    for (int tp = t0; tp < min(t0 + SPLIT, A.len); tp += CHUNK, b ^= 1) {
-      tile_sync();  // this chunk is widened, and every warp is done with the buffer of the one before
-      // the next chunk is widened before this one is folded by half of the warps, after it by the
-      // other half, so that a scheduler's warps do not all widen while the tensor cores wait
-      auto next = [&] {
-        if (tp + CHUNK >= A.len) return;
-        cp_wait<0>();
-        const int chunk = tp / CHUNK;
-        widen_chunk<KIND, D>(base + M::RAW_AT + (b ^ 1) * M::RAW, base + (b ^ 1) * M::BUFFER, chunk_role(warp, chunk + 1), lane);
-        if (tp + 2 * CHUNK < A.len)
-          copy_chunk<D>(base + M::RAW_AT + b * M::RAW, A.C, A.prow, ids, tp + 2 * CHUNK, A.len, A.Hkv, A.kh,
-                        chunk_role(warp, chunk + 2), lane);
-      };
-      if (warp < kTileWarps / 2) next();
 #pragma unroll 1
-      for (int p = 0; p < M::PAGES; p += 4) {
+    for (int tp = t0; tp < min(t0 + SPLIT, A.len); tp += CHUNK, ++it) {
+      const uint32_t stage = base + (it % kRing) * M::STAGE, full = bars + (it % kRing) * 16;
+      ring_wait(full, (it / kRing) & 1u, dead);
+#pragma unroll 1
+      for (int p = 0; p < M::PAGES; p += 2) {
         const int at = tp + p * PAGE;
         if (at >= longest) break;
-        if (at + 4 * PAGE <= shortest) {
-          fold_wide_pages<D, LIVE>(Q, base + b * M::BUFFER, p, lane, S);
+        if (at + 2 * PAGE <= shortest) {
+          fold_wide_pages<D, LIVE>(Q, stage, p, lane, S);
           continue;
         }
 #pragma unroll 1
-        for (int u = 0; u < 4 && at + u * PAGE < longest; ++u) {
+        for (int u = 0; u < 2 && at + u * PAGE < longest; ++u) {
           int nv[LIVE][2];
 #pragma unroll
-          for (int n = 0; n < LIVE; ++n)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) nv[n][r] = len_of(n, r) - at - u * PAGE;
-          fold_wide_masked<D, LIVE>(Q, base + b * M::BUFFER, p + u, nv, lane, S);
+          for (int n = 0; n < LIVE; ++n) {
+            const int2 len = lens[32 * n];
+            nv[n][0] = len.x - at - u * PAGE;
+            nv[n][1] = len.y - at - u * PAGE;
+          }
+          fold_wide_masked<D, LIVE>(Q, stage, p + u, nv, lane, S);
         }
       }
-      if (warp >= kTileWarps / 2) next();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + 8);  // this warp has read the stage
     }
 #pragma unroll
     for (int n = 0; n < LIVE; ++n) {
@@ -1181,7 +1152,7 @@ __device__ __noinline__ void run_tile(const TileArgs A, uint32_t base, float* to
   for (int n = 0; n < LIVE; ++n)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int k = (n * kTileWarps + warp) * 8 + 2 * c + r;
+      const int k = (n * kFoldWarps + warp) * 8 + 2 * c + r;
       if (k >= A.rows) continue;
       const float4 st = stats[32 * n];
       float x[D / 8];
@@ -1191,45 +1162,88 @@ __device__ __noinline__ void run_tile(const TileArgs A, uint32_t base, float* to
     }
 }
 
+// One tile for a widening warp: its part of every stage. (The ring is what hides the loads: the
+// widening warps are ahead of the folding ones by up to kRing stages.)
 template <int KIND, int D>
-__global__ void __launch_bounds__(kTileWarps * 32, 1)
+__device__ __forceinline__ void widen_tile(const TileArgs& A, uint32_t base, uint32_t bars, uint32_t& it, bool& dead, int warp,
+                                           int lane) {
+  using M = TileSmem<D>;
+  constexpr int CHUNK = M::PAGES * PAGE;
+  if (A.len <= 0) return;
+  PageIds ids;
+  ids.start(A.C, A.prow, A.len, lane);
+#pragma unroll 1
+  for (int tp = 0; tp < A.len; tp += CHUNK, ++it) {
+    const uint32_t stage = base + (it % kRing) * M::STAGE, full = bars + (it % kRing) * 16;
+    Raw X;
+    load_raw<D>(X, A.C, A.prow, ids, tp, A.len, A.Hkv, A.kh, warp, lane);
+    if (it >= kRing) ring_wait(full + 8, (it / kRing - 1) & 1u, dead);
+    widen_raw<KIND, D>(X, stage, warp, lane);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full);  // this warp's part is in place
+  }
+}
+
+template <int KIND, int D>
+__global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const uint16_t* __restrict__ q, int64_t ldq, int Hq, int Hkv, Cache C, Rows R, int T, int per,
                 const int32_t* __restrict__ list, Counts* __restrict__ counts, uint16_t* __restrict__ out,
                 float scale_log2) {
   using M = TileSmem<D>;
   extern __shared__ __align__(16) uint8_t smem[];
-  int* misc = reinterpret_cast<int*>(smem + M::MISC);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t base = smem_u32(smem);
+  const uint32_t base = smem_u32(smem), bars = base + M::BARS;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(bars + 16 * i, kWidenWarps);     // a stage is complete
+      mbar_init(bars + 16 * i + 8, kFoldWarps);  // a stage has been read
+    }
+    fence_mbar_init();
+  }
   pdl_wait();  // the plan (and the caller's q and store) are complete from here on
   pdl_trigger();
-  const int total = counts->tiles * Hkv;
-  while (true) {
-    if (threadIdx.x == 0) misc[0] = atomicAdd(&counts->next, 1);  // who takes which item is all this decides
-    tile_sync();
-    const int item = total - 1 - misc[0];  // later rows of a prompt see more keys: longest first
-    if (item < 0) return;
-    TileArgs A;
-    A.q = q; A.ldq = ldq; A.out = out; A.C = C; A.R = R; A.Hq = Hq; A.Hkv = Hkv; A.G = Hq / Hkv;
-    A.scale_log2 = scale_log2;
-    A.first = list[item / Hkv];
-    A.kh = item % Hkv;
-    const int n = tile_tokens(R.q_seq, A.first, T, per, lane);
-    A.rows = n * A.G;
-    int len = 0, pt_row = 0;
-    for (int i = lane; i < n; i += 32) {
-      int row;
-      const int x = attn::row_len(R, A.first + i, row);
-      if (x > len) len = x, pt_row = row;
+  uint32_t it = 0;
+  bool dead = false;
+  volatile int* item_at = reinterpret_cast<int*>(smem + M::ARGS);
+  TileArgs& A = *reinterpret_cast<TileArgs*>(smem + M::ARGS + 16);
+  // Takes the next tile (by the last warp, for all), or says that there is none. Later rows of a
+  // prompt see more keys: longest first.
+  auto next_tile = [&] {
+    tile_sync();  // every warp is done with the last tile's arguments (and the barriers are set up)
+    if (warp == kFoldWarps + kWidenWarps - 1) {
+      int item = 0;
+      if (lane == 0) item = counts->tiles * Hkv - 1 - atomicAdd(&counts->next, 1);  // all that this decides is who
+      item = __shfl_sync(kFullMask, item, 0);
+      if (item >= 0) {
+        const int first = list[item / Hkv], n = tile_tokens(R.q_seq, first, T, per, lane);
+        int len = 0, pt_row = 0;
+        for (int i = lane; i < n; i += 32) {
+          int row;
+          const int x = attn::row_len(R, first + i, row);
+          if (x > len) len = x, pt_row = row;
+        }
+        len = __reduce_max_sync(kFullMask, len);
+        pt_row = __reduce_max_sync(kFullMask, pt_row);  // rows that see anything share it; the others gave 0
+        if (lane == 0)
+          A = TileArgs{q, ldq, out, C, R, C.pt + (int64_t)pt_row * R.max_pages, Hq, Hkv, Hq / Hkv, first, n * (Hq / Hkv),
+                       item % Hkv, len, scale_log2};
+      }
+      if (lane == 0) *item_at = item;
     }
-    A.len = __reduce_max_sync(kFullMask, len);
-    pt_row = __reduce_max_sync(kFullMask, pt_row);  // rows that see anything share it; the others gave 0
-    A.prow = C.pt + (int64_t)pt_row * R.max_pages;
-    float* totals = reinterpret_cast<float*>(smem + M::TOTALS);
-    const int tiles = (A.rows + 7) / 8;  // of 8 query rows
-    if (tiles > kTileWarps + warp) run_tile<KIND, D, 2>(A, base, totals, warp, lane);
-    else run_tile<KIND, D, 1>(A, base, totals, warp, lane);
-    tile_sync();  // shared memory is free for the next tile
+    tile_sync();
+    return *item_at >= 0;
+  };
+  if (warp >= kFoldWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWidenRegs));
+    while (next_tile()) widen_tile<KIND, D>(A, base, bars, it, dead, warp - kFoldWarps, lane);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFoldRegs));
+    while (next_tile()) {
+      const int tiles = (A.rows + 7) / 8;  // of 8 query rows
+      if (tiles > 2 * kFoldWarps + warp) fold_tile<KIND, D, 3>(A, smem, base, bars, it, dead, warp, lane);
+      else if (tiles > kFoldWarps + warp) fold_tile<KIND, D, 2>(A, smem, base, bars, it, dead, warp, lane);
+      else fold_tile<KIND, D, 1>(A, smem, base, bars, it, dead, warp, lane);
+    }
   }
 }
 

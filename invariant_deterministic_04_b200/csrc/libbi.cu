@@ -277,7 +277,7 @@ cudaError_t q8_decode(const Q8Call& a, const AttnWs& ws) {
                         (const float*)ws.po, (const float2*)ws.pml, a.R, a.rows, max_splits(a.R.max_pages), a.Hq, a.out);
 }
 
-// Tokens a prefill tile takes. A CTA's twelve warps sit on four schedulers, so its time goes by
+// Tokens a prefill tile takes. A CTA's eight folding warps sit on four schedulers, so its time goes by
 // the tiles of 8 query rows a scheduler has (1 to 6), and about one more for the work that a chunk of
 // keys takes whatever the rows; take what makes the CTAs' rounds over T rows (as if they were one
 // chunk) cheapest, the larger tile among equals.
@@ -300,7 +300,7 @@ cudaError_t q8_prefill(const Q8Call& a, int32_t* list, bi::attnq8::Counts* count
   struct TileTag {};  // one set of once-flags per instantiation
   struct FewTag {};
   int tile_sm = 0, few_sm = 0;
-  cudaError_t e = resident_ctas<TileTag>(tile, a8::kTileWarps * 32, a8::TileSmem<D>::BYTES, a.dev, &tile_sm);
+  cudaError_t e = resident_ctas<TileTag>(tile, a8::kTileThreads, a8::TileSmem<D>::BYTES, a.dev, &tile_sm);
   if (e == cudaSuccess) e = resident_ctas<FewTag>(rest, a8::kFewWarps * 32, a8::FewSmem<D>::BYTES, a.dev, &few_sm);
   if (e != cudaSuccess) return e;
   const int G = a.Hq / a.Hkv, few = a8::kFewRows / G, per = q8_tile_tokens(a.rows, G, a.Hkv, a.sms);
@@ -309,7 +309,7 @@ cudaError_t q8_prefill(const Q8Call& a, int32_t* list, bi::attnq8::Counts* count
   const int64_t most = (int64_t)a.rows * a.Hkv;
   if (a.rows > few) {  // else there are few-row tiles only
     const int64_t full = (int64_t)a.sms * tile_sm;
-    e = bi::launch_pdl(tile, dim3((unsigned)(most < full ? most : full)), dim3(a8::kTileWarps * 32),
+    e = bi::launch_pdl(tile, dim3((unsigned)(most < full ? most : full)), dim3(a8::kTileThreads),
                        (size_t)a8::TileSmem<D>::BYTES, a.st, a.q, a.ldq, a.Hq, a.Hkv, a.C, a.R, a.rows, per,
                        (const int32_t*)list, counts, a.out, a.c);
     if (e != cudaSuccess) return e;
