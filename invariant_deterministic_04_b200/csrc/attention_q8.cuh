@@ -223,76 +223,104 @@ struct Tokens {
 };
 
 
-// Weights of one page for one tile of 8 query rows, from its scores: moves m (and l and o with
-// it) where it must, adds to l, and gives 2^7 w as the operand of the value product. MASKED:
-// query row e of the lane sees the first nv[e] tokens only; otherwise all 16. A row whose largest
-// f16 weight exceeds 2^15 moves its reference to its largest score of the page; weights are
-// taken with the reference in hand first, which most pages keep.
-template <int D, bool MASKED>
-__device__ __forceinline__ void tile_weights(const float2& qc, const float (&s)[4], const Tokens& T, const int (&nv)[2],
-                                             int g, float2& m, float2& l, float (&o)[D / 16][4], uint32_t (&w)[2]) {
-  float2 z[2], p[2];  // token g | g + 8, pairs of query rows 2c, 2c + 1
-  float2 ref = make_float2(__fsub_rn(7.f, m.x), __fsub_rn(7.f, m.y));
+// Weights of one page from its scores s (which become z): moves m (and l and o with it) where it
+// must, adds to l, and gives 2^7 w as the operand of the value product. masked (the same for the
+// whole warp): the lane's query row (n, r) sees the first nv(n, r) tokens only; otherwise all 16
+// are seen. live: tiles that hold query rows.
+// A row whose largest f16 weight exceeds 2^15 moves its reference to its largest score of the
+// page; weights are taken with the reference in hand first, which most pages keep.
+// There is one line of code through the accumulators, with small blocks beside it for what is
+// rare: with a second, masked form of the whole page the compiler joined two sets of
+// accumulators by register moves, which cost a third of the time of pages that never ran it.
+template <int D, int NT, typename Nv>
+__device__ __forceinline__ void page_weights(const Query<D, NT>& Q, float (&s)[NT][4], const Tokens& T, bool masked, Nv nv,
+                                             int g, int live, State<D, NT>& S, uint32_t (&w)[NT][2]) {
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    z[t] = __ffma2_rn(make_float2(s[2 * t], s[2 * t + 1]), __fmul2_rn(make_float2(T.ks[t], T.ks[t]), qc),
-                      make_float2(T.lg[t], T.lg[t]));
-    if (MASKED) {
-      if (g + 8 * t >= nv[0]) z[t].x = -INFINITY;
-      if (g + 8 * t >= nv[1]) z[t].y = -INFINITY;
-    }
-    const float2 x = __fadd2_rn(z[t], ref);
-    p[t] = make_float2(ex2(x.x), ex2(x.y));
-    w[t] = pack_f16x2(p[t].x, p[t].y);
-  }
-  const __half2 top = __hmax2(*reinterpret_cast<__half2*>(&w[0]), *reinterpret_cast<__half2*>(&w[1]));
-  const bool over = !__hble2(top, __halves2half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800)));  // 2^15
-  if (__any_sync(kFullMask, over)) {
-    float mx[2] = {fmaxf(z[0].x, z[1].x), fmaxf(z[0].y, z[1].y)};
-    float pm[2] = {fmaxf(p[0].x, p[1].x), fmaxf(p[0].y, p[1].y)};
-    float al[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) {
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFullMask, mx[r], d));
-        pm[r] = fmaxf(pm[r], __shfl_xor_sync(kFullMask, pm[r], d));
-      }
-      float& mr = r ? m.y : m.x;
-      const bool up = __half2float(__float2half_rn(pm[r])) > 32768.f;
-      al[r] = up ? ex2(__fsub_rn(mr, mx[r])) : 1.f;  // x * 1 == x: the other rows keep their bits
-      if (up) mr = mx[r];
-    }
-    l = __fmul2_rn(l, make_float2(al[0], al[1]));
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = __fmul_rn(o[i][e], al[e & 1]);
-    ref = make_float2(__fsub_rn(7.f, m.x), __fsub_rn(7.f, m.y));
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const float2 x = __fadd2_rn(z[t], ref);
-      p[t] = make_float2(ex2(x.x), ex2(x.y));
-      w[t] = pack_f16x2(p[t].x, p[t].y);
+      const float2 z = __ffma2_rn(make_float2(s[n][2 * t], s[n][2 * t + 1]), __fmul2_rn(make_float2(T.ks[t], T.ks[t]), Q.c[n]),
+                                  make_float2(T.lg[t], T.lg[t]));
+      s[n][2 * t] = z.x;
+      s[n][2 * t + 1] = z.y;
+    }
+  if (masked) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (g + 8 * (e >> 1) >= nv(n, e & 1)) s[n][e] = -INFINITY;
+  }
+  auto weight = [&](int n, int t) {  // pairs of query rows 2c, 2c + 1
+    const float2 x = __fadd2_rn(make_float2(s[n][2 * t], s[n][2 * t + 1]),
+                                make_float2(__fsub_rn(7.f, S.m[n].x), __fsub_rn(7.f, S.m[n].y)));
+    return make_float2(ex2(x.x), ex2(x.y));
+  };
+  float2 l[NT];
+  bool over = false;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    l[n] = S.l[n];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const float2 p = weight(n, t);
+      w[n][t] = pack_f16x2(p.x, p.y);
+      l[n] = __ffma2_rn(p, make_float2(T.ri[t], T.ri[t]), l[n]);
+    }
+    const __half2 top = __hmax2(*reinterpret_cast<__half2*>(&w[n][0]), *reinterpret_cast<__half2*>(&w[n][1]));
+    const bool up = !__hble2(top, __halves2half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800)));  // 2^15
+    over |= up && (NT == 1 || n < live);
+  }
+  if (__any_sync(kFullMask, over)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const __half2 top = __hmax2(*reinterpret_cast<__half2*>(&w[n][0]), *reinterpret_cast<__half2*>(&w[n][1]));
+      float pm[2] = {__low2float(top), __high2float(top)};
+      float mx[2] = {fmaxf(s[n][0], s[n][2]), fmaxf(s[n][1], s[n][3])};
+      float al[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFullMask, mx[r], d));
+          pm[r] = fmaxf(pm[r], __shfl_xor_sync(kFullMask, pm[r], d));
+        }
+        float& m = r ? S.m[n].y : S.m[n].x;
+        const bool up = pm[r] > 32768.f;
+        al[r] = up ? ex2(__fsub_rn(m, mx[r])) : 1.f;  // x * 1 == x: the other rows keep their bits
+        if (up) m = mx[r];
+      }
+      S.l[n] = __fmul2_rn(S.l[n], make_float2(al[0], al[1]));
+      l[n] = S.l[n];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S.o[n][i][e] = __fmul_rn(S.o[n][i][e], al[e & 1]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float2 p = weight(n, t);
+        w[n][t] = pack_f16x2(p.x, p.y);
+        l[n] = __ffma2_rn(p, make_float2(T.ri[t], T.ri[t]), l[n]);
+      }
+    }
+  }
+  if (masked) {  // tokens that a row does not see add nothing to its l, whatever their scales
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      l[n] = S.l[n];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float2 p = weight(n, t);
+        if (g + 8 * t < nv(n, 0)) l[n].x = __fmaf_rn(p.x, T.ri[t], l[n].x);
+        if (g + 8 * t < nv(n, 1)) l[n].y = __fmaf_rn(p.y, T.ri[t], l[n].y);
+      }
     }
   }
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const float2 x = __ffma2_rn(p[t], make_float2(T.ri[t], T.ri[t]), l);
-    if (!MASKED || g + 8 * t < nv[0]) l.x = x.x;
-    if (!MASKED || g + 8 * t < nv[1]) l.y = x.y;
-    w[t] = transpose8x8(w[t]);
-  }
-}
-
-template <int D, int NT, bool MASKED>
-__device__ __forceinline__ void page_weights(const Query<D, NT>& Q, const float (&s)[NT][4], const Tokens& T,
-                                             const int (&nv)[NT][2], int g, int live, State<D, NT>& S,
-                                             uint32_t (&w)[NT][2]) {
-#pragma unroll
   for (int n = 0; n < NT; ++n) {
-    if (NT > 1 && n >= live) break;
-    tile_weights<D, MASKED>(Q.c[n], s[n], T, nv[n], g, S.m[n], S.l[n], S.o[n], w[n]);
+    S.l[n] = l[n];
+    w[n][0] = transpose8x8(w[n][0]);
+    w[n][1] = transpose8x8(w[n][1]);
   }
 }
 
@@ -327,10 +355,10 @@ __device__ __forceinline__ uint32_t chunk_at(int t, int i) {
   return (uint32_t)(t * D + ((i ^ (D == 128 ? (t & 7) : ((t >> 1) & 3))) << 4));
 }
 
-// Folds a page. MASKED: `seen` of its tokens exist, query row (n, e) sees nv[n][e].
-template <int KIND, int D, int NT, bool MASKED>
-__device__ __forceinline__ void fold_page(const Query<D, NT>& Q, uint32_t page, uint32_t scales, const int (&nv)[NT][2],
-                                          int seen, int live, int lane, State<D, NT>& S) {
+// Folds a page. masked: `seen` of its tokens exist, query row (n, r) sees nv(n, r).
+template <int KIND, int D, int NT, typename Nv>
+__device__ __forceinline__ void fold_page(const Query<D, NT>& Q, uint32_t page, uint32_t scales, bool masked, Nv nv, int seen,
+                                          int live, int lane, State<D, NT>& S) {
   const int g = lane >> 2, c = lane & 3;
   float s[NT][4];
   const uint32_t k0 = page + chunk_at<D>(g, c);  // chunk c + 4 of a 128-byte row: bit 6 flipped
@@ -343,11 +371,10 @@ __device__ __forceinline__ void fold_page(const Query<D, NT>& Q, uint32_t page, 
     for (int b = 0; b < 4; ++b) {
       const uint4 a = key_operand<KIND>(xw[b], yw[b]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (NT == 1 || n < live) {
-          if (v + b == 0) mma16816_first(s[n], a, Q.b[n][0][0], Q.b[n][0][1]);
-          else mma16816(s[n], a, Q.b[n][4 * v + b][0], Q.b[n][4 * v + b][1]);
-        }
+      for (int n = 0; n < NT; ++n) {
+        if (v + b == 0) mma16816_first(s[n], a, Q.b[n][0][0], Q.b[n][0][1]);
+        else mma16816(s[n], a, Q.b[n][4 * v + b][0], Q.b[n][4 * v + b][1]);
+      }
     }
   }
   Tokens T;
@@ -359,7 +386,7 @@ __device__ __forceinline__ void fold_page(const Query<D, NT>& Q, uint32_t page, 
     T.ri[t] = rcp(vs);
   }
   uint32_t w[NT][2];
-  page_weights<D, NT, MASKED>(Q, s, T, nv, g, live, S, w);
+  page_weights<D, NT>(Q, s, T, masked, nv, g, live, S, w);
   uint32_t x[4][D / 32];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -373,9 +400,13 @@ __device__ __forceinline__ void fold_page(const Query<D, NT>& Q, uint32_t page, 
                    : "=r"(x[i][0]), "=r"(x[i][1])
                    : "r"(at + chunk_at<D>(t, g >> 1) + 8 * (g & 1)));
     }
-    if (MASKED && t + 8 * (i >> 1) >= seen)
+  }
+  if (masked) {
 #pragma unroll
-      for (int u = 0; u < D / 32; ++u) x[i][u] = 0;
+    for (int i = 0; i < 4; ++i)
+      if (2 * c + (i & 1) + 8 * (i >> 1) >= seen)
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) x[i][u] = 0;
   }
 #pragma unroll
   for (int u = 0; u < D / 32; ++u) {
@@ -384,7 +415,6 @@ __device__ __forceinline__ void fold_page(const Query<D, NT>& Q, uint32_t page, 
     value_operands<KIND>(xu, a, b);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if (NT > 1 && n >= live) break;
       mma16816(S.o[n][2 * u], a, w[n][0], w[n][1]);
       mma16816(S.o[n][2 * u + 1], b, w[n][0], w[n][1]);
     }
@@ -569,12 +599,8 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT == 256 ? 3 : 4)
       }
       if (__shfl_sync(kFullMask, cur.page, j) >= 0) {  // the tokens of an unusable page are not seen
         const int seen = cur.seen - j * PAGE;
-        int nv[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) nv[n][0] = nv[n][1] = seen;
-        const uint32_t page = ring + st * kPageBytes<D>, sc = scales + st * kScaleBytes;
-        if (seen >= PAGE) fold_page<KIND, D, NT, false>(Q, page, sc, nv, seen, NT, lane, S);
-        else fold_page<KIND, D, NT, true>(Q, page, sc, nv, seen, NT, lane, S);
+        fold_page<KIND, D, NT>(Q, ring + st * kPageBytes<D>, scales + st * kScaleBytes, seen < PAGE,
+                               [&](int, int) { return seen; }, seen, NT, lane, S);
       }
       ++used;
       __syncwarp();  // every lane has read this page: its stage may be refilled
@@ -982,67 +1008,22 @@ __device__ __forceinline__ void wide_values(uint32_t buf, int page, int lane, co
   }
 }
 
-// Folds one page of a buffer into the warp's LIVE tiles; query row (n, e) sees nv[n][e] tokens of it.
-template <int D, int LIVE>
-__device__ __forceinline__ void fold_wide_masked(const Query<D, LIVE>& Q, uint32_t buf, int page,
-                                                 const int (&nv)[LIVE][2], int lane, State<D, LIVE>& S) {
-  float s[LIVE][4];
-  wide_scores<D, LIVE>(Q, buf, page, lane, s);
-  const Tokens T = wide_tokens<D>(buf, page, lane);
-  uint32_t w[LIVE][2];
-  page_weights<D, LIVE, true>(Q, s, T, nv, lane >> 2, LIVE, S, w);
-  wide_values<D, LIVE>(buf, page, lane, w, S);
-}
-
-// Folds two whole pages of a buffer from `page` on, both of them seen by every query row. The
-// scores of a page are issued before the weights of the page before it, in one straight line
-// of code, so that the tensor cores work through the softmax; the one vote of a page asks whether
-// any row has to move its reference, and only then are the weights taken tile by tile as
-// tile_weights does (the values are the same either way).
-template <int D, int LIVE>
-__device__ __forceinline__ void fold_wide_pages(const Query<D, LIVE>& Q, uint32_t buf, int page, int lane, State<D, LIVE>& S) {
-  constexpr bool AHEAD = LIVE < 3;  // (three tiles leave no registers for a second page's scores)
+// Folds two pages of a stage from `page` on. The scores of the second are issued before the
+// weights of the first (of up to two tiles; three leave no registers for that), so that the
+// tensor cores work through the softmax. masked: query row (n, r) sees the first nv(n, r) tokens.
+template <int D, int LIVE, typename Nv>
+__device__ __forceinline__ void fold_wide(const Query<D, LIVE>& Q, uint32_t stage, int page, bool masked, Nv nv, int lane,
+                                          State<D, LIVE>& S) {
+  constexpr bool AHEAD = LIVE < 3;
   float s[2][LIVE][4];
-  wide_scores<D, LIVE>(Q, buf, page, lane, s[0]);
+  wide_scores<D, LIVE>(Q, stage, page, lane, s[0]);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    if (u == 0 && AHEAD) wide_scores<D, LIVE>(Q, buf, page + 1, lane, s[1]);
-    if (u == 1 && !AHEAD) wide_scores<D, LIVE>(Q, buf, page + 1, lane, s[1]);
-    const Tokens T = wide_tokens<D>(buf, page + u, lane);
+    if (u == (AHEAD ? 0 : 1)) wide_scores<D, LIVE>(Q, stage, page + 1, lane, s[1]);
+    const Tokens T = wide_tokens<D>(stage, page + u, lane);
     uint32_t w[LIVE][2];
-    float2 l[LIVE];
-    bool over = false;
-#pragma unroll
-    for (int n = 0; n < LIVE; ++n) {
-      const float (&sn)[4] = s[u & 1][n];
-      const float2 ref = make_float2(__fsub_rn(7.f, S.m[n].x), __fsub_rn(7.f, S.m[n].y));
-      l[n] = S.l[n];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float2 z = __ffma2_rn(make_float2(sn[2 * t], sn[2 * t + 1]), __fmul2_rn(make_float2(T.ks[t], T.ks[t]), Q.c[n]),
-                                    make_float2(T.lg[t], T.lg[t]));
-        const float2 x = __fadd2_rn(z, ref);
-        const float2 p = make_float2(ex2(x.x), ex2(x.y));
-        w[n][t] = pack_f16x2(p.x, p.y);
-        l[n] = __ffma2_rn(p, make_float2(T.ri[t], T.ri[t]), l[n]);
-      }
-      const __half2 top = __hmax2(*reinterpret_cast<__half2*>(&w[n][0]), *reinterpret_cast<__half2*>(&w[n][1]));
-      over |= !__hble2(top, __halves2half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800)));  // 2^15
-    }
-    if (__any_sync(kFullMask, over)) {
-      const int all[2] = {PAGE, PAGE};
-#pragma unroll
-      for (int n = 0; n < LIVE; ++n)
-        tile_weights<D, false>(Q.c[n], s[u & 1][n], T, all, lane >> 2, S.m[n], S.l[n], S.o[n], w[n]);
-    } else {
-#pragma unroll
-      for (int n = 0; n < LIVE; ++n) {
-        S.l[n] = l[n];
-        w[n][0] = transpose8x8(w[n][0]);
-        w[n][1] = transpose8x8(w[n][1]);
-      }
-    }
-    wide_values<D, LIVE>(buf, page + u, lane, w, S);
+    page_weights<D, LIVE>(Q, s[u], T, masked, [&](int n, int r) { return nv(n, r) - u * PAGE; }, lane >> 2, LIVE, S, w);
+    wide_values<D, LIVE>(stage, page + u, lane, w, S);
   }
 }
 
@@ -1110,21 +1091,12 @@ __device__ __forceinline__ void fold_tile(const TileArgs& A, uint8_t* smem, uint
       for (int p = 0; p < M::PAGES; p += 2) {
         const int at = tp + p * PAGE;
         if (at >= longest) break;
-        if (at + 2 * PAGE <= shortest) {
-          fold_wide_pages<D, LIVE>(Q, stage, p, lane, S);
-          continue;
-        }
-#pragma unroll 1
-        for (int u = 0; u < 2 && at + u * PAGE < longest; ++u) {
-          int nv[LIVE][2];
-#pragma unroll
-          for (int n = 0; n < LIVE; ++n) {
-            const int2 len = lens[32 * n];
-            nv[n][0] = len.x - at - u * PAGE;
-            nv[n][1] = len.y - at - u * PAGE;
-          }
-          fold_wide_masked<D, LIVE>(Q, stage, p + u, nv, lane, S);
-        }
+        fold_wide<D, LIVE>(Q, stage, p, at + 2 * PAGE > shortest,
+                           [&](int n, int r) {
+                             const int2 len = lens[32 * n];
+                             return (r ? len.y : len.x) - at;
+                           },
+                           lane, S);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(full + 8);  // this warp has read the stage
@@ -1335,14 +1307,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3)
         __syncwarp();
         if (__shfl_sync(kFullMask, page, j) >= 0) {
           const int tp = t0 + j * PAGE;
-          int nv[kFewNT][2];
-#pragma unroll
-          for (int n = 0; n < kFewNT; ++n)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) nv[n][r] = len[n][r] - tp;
-          const uint32_t st = (uint32_t)(j % kFewStages), pg = ring + st * kPageBytes<D>, sc = scales + st * kScaleBytes;
-          if (tp + PAGE <= shortest) fold_page<KIND, D, kFewNT, false>(Q, pg, sc, nv, PAGE, live, lane, S);
-          else fold_page<KIND, D, kFewNT, true>(Q, pg, sc, nv, longest - tp, live, lane, S);
+          const uint32_t st = (uint32_t)(j % kFewStages);
+          fold_page<KIND, D, kFewNT>(Q, ring + st * kPageBytes<D>, scales + st * kScaleBytes, tp + PAGE > shortest,
+                                     [&](int n, int r) { return len[n][r] - tp; }, longest - tp, live, lane, S);
         }
         __syncwarp();
         issue(j + kFewStages);
