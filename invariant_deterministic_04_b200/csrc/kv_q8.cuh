@@ -4,7 +4,7 @@
 // s; it stands for v * s. From a bf16 row x with a = max |x|:
 //   int8: s = a / 127 (one fp32 rounding), v = the integer nearest to 127 x / a, ties to even.
 //     127 x has at most 15 significant bits, so it is exact in fp32 and v takes one rounded
-//     division and one rounding to an integer. Together they are exact: with x = mx 2^(j-d)
+//     division (divide8) and one rounding to an integer. Together they are exact: with x = mx 2^(j-d)
 //     and a = ma 2^j (mx, ma < 2^8, ma >= 2^7) a quotient q >= 2^n that is no half-integer is
 //     at least 2^-d / 255 > 2^(n-16) from the nearest one, and the division is off by 2^(n-24)
 //     at most; a half-integer is representable, so the division gives it and the tie goes to even.
@@ -66,26 +66,45 @@ __device__ __forceinline__ uint32_t row_max_bits(const uint4& x) {
   return m;
 }
 
+// The int8 values of 8 elements, rows below 2^64 given as they are and others at 2^-64 (num = 127 or
+// 127 * 2^-64; a and its rounded reciprocal to match). The division is one step of a published
+// correction (Markstein, IBM J. R&D 34, 1990): q0 = y r, q = q0 + (y - q0 a) r. The remainder is exact
+// (y - q0 a is a multiple of ulp(q0) ulp(a) below 2^9 of it), so q is the quotient but for
+// 2^-47 of it, rounded once: what the exactness above asks for. Adding 1.5 * 2^23 rounds to an
+// integer, ties to even, whose low byte is the value.
+__device__ __forceinline__ uint2 divide8(const uint4& x, float num, float a, float r) {
+  float2 f[4];
+  unpack8x2(x, f);
+  const float2 n2 = make_float2(num, num), a2 = make_float2(-a, -a), r2 = make_float2(r, r);
+  const float2 magic = make_float2(12582912.f, 12582912.f);
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = __fmul2_rn(n2, f[i]);
+    const float2 q0 = __fmul2_rn(y, r2);
+    const float2 q = __fadd2_rn(__ffma2_rn(__ffma2_rn(q0, a2, y), r2, q0), magic);
+    v[i] = __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x0040);
+  }
+  return make_uint2(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410));
+}
+
 template <int KIND>
 __device__ __forceinline__ uint2 quantise8(const uint4& x, uint32_t amax_bits, float& scale) {
-  float f[8];
-  unpack8(x, f);
   const float a = __uint_as_float(amax_bits << 16);
   if (amax_bits < kEmptyBits || amax_bits >= kNonFiniteBits) {
     scale = amax_bits < kEmptyBits ? 1.f : __uint_as_float(0x7FC00000u);
     return make_uint2(0, 0);
   }
-  uint32_t b[8];
   if constexpr (KIND == BI_KV_INT8) {
     scale = __fdiv_rn(a, 127.f);
     // rows from 2^64 on are divided at 2^-64 of their size, where 127 x cannot overflow (elements
     // that this takes below the normal numbers are far below half a step)
     const bool loud = amax_bits >= kLoudBits;
-    const float num = loud ? 127.f * 0x1p-64f : 127.f, den = loud ? __fmul_rn(a, 0x1p-64f) : a;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = (uint32_t)__float2int_rn(__fdiv_rn(__fmul_rn(num, f[i]), den)) & 0xFFu;
-    return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
+    const float den = loud ? __fmul_rn(a, 0x1p-64f) : a;
+    return divide8(x, loud ? 127.f * 0x1p-64f : 127.f, den, __frcp_rn(den));
   } else {
+    float f[8];
+    unpack8(x, f);
     // a = (1 + m / 128) 2^n: 448 = 1.75 * 2^8, so e = n - 8, one more where 1 + m / 128 > 1.75
     const int e = (int)(amax_bits >> 7) - 127 - 8 + ((amax_bits & 0x7Fu) > 0x60u ? 1 : 0);
     scale = __uint_as_float((uint32_t)(e + 127) << 23);
@@ -99,33 +118,33 @@ __device__ __forceinline__ uint2 quantise8(const uint4& x, uint32_t amax_bits, f
   }
 }
 
-// D/8 lanes per (row, kv-head) and side; side 0 is K, side 1 is V.
+// D/8 lanes take the K and the V row of one (row, kv-head); items is T * Hkv.
 template <int KIND, int D>
 __global__ void __launch_bounds__(kThreads) kv_append_q8_kernel(const uint16_t* __restrict__ kn,
                                                                 const uint16_t* __restrict__ vn, int64_t ld_new,
                                                                 const int32_t* __restrict__ q_seq,
-                                                                const int32_t* __restrict__ q_pos, Store S, int T,
-                                                                int Hkv) {
-  constexpr int LANES = D / 8;
-  const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t item = e / LANES;
-  const int j = (int)(e % LANES);
+                                                                const int32_t* __restrict__ q_pos, Store S,
+                                                                uint32_t items, uint32_t Hkv) {
+  constexpr uint32_t LANES = D / 8;
+  const uint32_t item = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+  const int j = (int)(threadIdx.x % LANES);
   pdl_wait();  // inputs written by the previous kernel on the stream are complete from here on
   pdl_trigger();
-  const bool live = item < (int64_t)2 * T * Hkv;
-  const int64_t it = live ? item : 0;
-  const int side = (int)(it & 1);
-  const int64_t tg = it >> 1;
-  const int t = (int)(tg / Hkv), g = (int)(tg - (int64_t)t * Hkv);
-  const uint4 x = __ldg(reinterpret_cast<const uint4*>((side ? vn : kn) + (int64_t)t * ld_new + (int64_t)g * D) + j);
-  const uint32_t amax = row_max_bits<LANES>(x);
-  if (!live) return;
-  const int64_t row = slot_row(S, q_seq[t], q_pos[t], g, Hkv, j == 0);
-  if (row < 0) return;
-  float s;
-  const uint2 v = quantise8<KIND>(x, amax, s);
-  reinterpret_cast<uint2*>((side ? S.v : S.k) + row * D)[j] = v;
-  if (j == 0) (side ? S.vs : S.ks)[row] = s;
+  const bool live = item < items;  // (the others keep the shuffles whole)
+  const uint32_t it = live ? item : 0, t = it / Hkv, g = it - t * Hkv;
+  const int64_t at = (int64_t)t * ld_new + (int64_t)g * D;
+  const uint4 k = __ldg(reinterpret_cast<const uint4*>(kn + at) + j), v = __ldg(reinterpret_cast<const uint4*>(vn + at) + j);
+  const int64_t row = slot_row(S, q_seq[t], q_pos[t], (int)g, (int)Hkv, live && j == 0);
+  const uint32_t ka = row_max_bits<LANES>(k), va = row_max_bits<LANES>(v);
+  if (!live || row < 0) return;
+  float ks, vs;
+  const uint2 k8 = quantise8<KIND>(k, ka, ks), v8 = quantise8<KIND>(v, va, vs);
+  reinterpret_cast<uint2*>(S.k + row * D)[j] = k8;
+  reinterpret_cast<uint2*>(S.v + row * D)[j] = v8;
+  if (j == 0) {
+    S.ks[row] = ks;
+    S.vs[row] = vs;
+  }
 }
 
 template <int KIND>
@@ -144,36 +163,39 @@ __device__ __forceinline__ void widen4(uint32_t w, float (&f)[4]) {
   }
 }
 
+template <int KIND>
+__device__ __forceinline__ uint4 read8(const uint2& v, float s) {
+  float f[4], h[4];
+  widen4<KIND>(v.x, f);
+  widen4<KIND>(v.y, h);
+  return make_uint4(pack_bf16x2(__fmul_rn(f[0], s), __fmul_rn(f[1], s)), pack_bf16x2(__fmul_rn(f[2], s), __fmul_rn(f[3], s)),
+                    pack_bf16x2(__fmul_rn(h[0], s), __fmul_rn(h[1], s)), pack_bf16x2(__fmul_rn(h[2], s), __fmul_rn(h[3], s)));
+}
+
 // The inverse: bf16(v * s) of the store rows at (q_seq[t], q_pos[t]); zeros where an id is bad.
 template <int KIND, int D>
 __global__ void __launch_bounds__(kThreads) kv_read_q8_kernel(uint16_t* __restrict__ ko, uint16_t* __restrict__ vo,
                                                               int64_t ld_out, const int32_t* __restrict__ q_seq,
-                                                              const int32_t* __restrict__ q_pos, Store S, int T,
-                                                              int Hkv) {
-  constexpr int LANES = D / 8;
-  const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t it = e / LANES;
-  const int j = (int)(e % LANES);
+                                                              const int32_t* __restrict__ q_pos, Store S, uint32_t items,
+                                                              uint32_t Hkv) {
+  constexpr uint32_t LANES = D / 8;
+  const uint32_t item = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+  const int j = (int)(threadIdx.x % LANES);
   pdl_wait();  // the store is complete from here on
   pdl_trigger();
-  if (it >= (int64_t)2 * T * Hkv) return;
-  const int side = (int)(it & 1);
-  const int64_t tg = it >> 1;
-  const int t = (int)(tg / Hkv), g = (int)(tg - (int64_t)t * Hkv);
-  const int64_t row = slot_row(S, q_seq[t], q_pos[t], g, Hkv, j == 0);
-  uint4 o = make_uint4(0, 0, 0, 0);
+  if (item >= items) return;
+  const uint32_t t = item / Hkv, g = item - t * Hkv;
+  const int64_t row = slot_row(S, q_seq[t], q_pos[t], (int)g, (int)Hkv, j == 0);
+  uint4 k = make_uint4(0, 0, 0, 0), v = k;
   if (row >= 0) {
-    const uint2 v = reinterpret_cast<const uint2*>((side ? S.v : S.k) + row * D)[j];
-    const float s = (side ? S.vs : S.ks)[row];
-    float f[4], h[4];
-    widen4<KIND>(v.x, f);
-    widen4<KIND>(v.y, h);
-    o = make_uint4(pack_bf16x2(__fmul_rn(f[0], s), __fmul_rn(f[1], s)),
-                   pack_bf16x2(__fmul_rn(f[2], s), __fmul_rn(f[3], s)),
-                   pack_bf16x2(__fmul_rn(h[0], s), __fmul_rn(h[1], s)),
-                   pack_bf16x2(__fmul_rn(h[2], s), __fmul_rn(h[3], s)));
+    const uint2 k8 = reinterpret_cast<const uint2*>(S.k + row * D)[j], v8 = reinterpret_cast<const uint2*>(S.v + row * D)[j];
+    const float ks = S.ks[row], vs = S.vs[row];
+    k = read8<KIND>(k8, ks);
+    v = read8<KIND>(v8, vs);
   }
-  reinterpret_cast<uint4*>((side ? vo : ko) + (int64_t)t * ld_out + (int64_t)g * D)[j] = o;
+  const int64_t at = (int64_t)t * ld_out + (int64_t)g * D;
+  reinterpret_cast<uint4*>(ko + at)[j] = k;
+  reinterpret_cast<uint4*>(vo + at)[j] = v;
 }
 
 }  // namespace kvq8

@@ -606,8 +606,8 @@ bi_status bi_kv_append_q8(const bi_bf16* k_new, const bi_bf16* v_new, int64_t ld
   if (bi_status e = store_check(k_cache, v_cache, k_scale, v_scale, kind, num_pages, max_pages_per_seq, Hkv, D)) return e;
   if (ld_new < (int64_t)Hkv * D) return BI_ERR_SHAPE;
   if (!aligned16(k_new) || !aligned16(v_new) || ld_new % 8) return BI_ERR_ALIGN;
-  const int64_t grid = ((int64_t)2 * T * Hkv * (D / 8) + bi::kvq8::kThreads - 1) / bi::kvq8::kThreads;
-  if (grid > INT_MAX) return BI_ERR_SHAPE;
+  const int64_t items = (int64_t)T * Hkv, per = bi::kvq8::kThreads / (D / 8), grid = (items + per - 1) / per;
+  if (items > INT_MAX) return BI_ERR_SHAPE;  // (row, kv-head) pairs are counted in 31 bits
   if (T == 0) return BI_OK;
   const bi::kvq8::Store S{(uint8_t*)k_cache, (uint8_t*)v_cache, k_scale, v_scale, num_pages, page_table, num_seqs,
                           max_pages_per_seq};
@@ -616,7 +616,7 @@ bi_status bi_kv_append_q8(const bi_bf16* k_new, const bi_bf16* v_new, int64_t ld
                                    : (D == 128 ? bi::kvq8::kv_append_q8_kernel<BI_KV_E4M3, 128>
                                                : bi::kvq8::kv_append_q8_kernel<BI_KV_E4M3, 64>);
   return bi::launch_pdl(kernel, dim3((unsigned)grid), dim3(bi::kvq8::kThreads), 0, as_stream(stream), k_new, v_new,
-                        ld_new, q_seq, q_pos, S, T, Hkv) == cudaSuccess
+                        ld_new, q_seq, q_pos, S, (uint32_t)items, (uint32_t)Hkv) == cudaSuccess
              ? BI_OK
              : BI_ERR_CUDA;
 }
@@ -631,8 +631,8 @@ bi_status bi_kv_read_q8(bi_bf16* k_out, bi_bf16* v_out, int64_t ld_out, const in
   if (bi_status e = store_check(k_cache, v_cache, k_scale, v_scale, kind, num_pages, max_pages_per_seq, Hkv, D)) return e;
   if (ld_out < (int64_t)Hkv * D) return BI_ERR_SHAPE;
   if (!aligned16(k_out) || !aligned16(v_out) || ld_out % 8) return BI_ERR_ALIGN;
-  const int64_t grid = ((int64_t)2 * T * Hkv * (D / 8) + bi::kvq8::kThreads - 1) / bi::kvq8::kThreads;
-  if (grid > INT_MAX) return BI_ERR_SHAPE;
+  const int64_t items = (int64_t)T * Hkv, per = bi::kvq8::kThreads / (D / 8), grid = (items + per - 1) / per;
+  if (items > INT_MAX) return BI_ERR_SHAPE;  // (row, kv-head) pairs are counted in 31 bits
   if (T == 0) return BI_OK;
   const int64_t width = (int64_t)Hkv * D, rows = num_pages * Hkv * BI_PAGE_TOKENS;
   if (blocks_overlap(k_out, ld_out, width, v_out, ld_out, width, T)) return BI_ERR_SHAPE;
@@ -648,7 +648,7 @@ bi_status bi_kv_read_q8(bi_bf16* k_out, bi_bf16* v_out, int64_t ld_out, const in
                                    : (D == 128 ? bi::kvq8::kv_read_q8_kernel<BI_KV_E4M3, 128>
                                                : bi::kvq8::kv_read_q8_kernel<BI_KV_E4M3, 64>);
   return bi::launch_pdl(kernel, dim3((unsigned)grid), dim3(bi::kvq8::kThreads), 0, as_stream(stream), k_out, v_out,
-                        ld_out, q_seq, q_pos, S, T, Hkv) == cudaSuccess
+                        ld_out, q_seq, q_pos, S, (uint32_t)items, (uint32_t)Hkv) == cudaSuccess
              ? BI_OK
              : BI_ERR_CUDA;
 }
@@ -724,7 +724,7 @@ bi_status bi_qk_norm_rope(const bi_bf16* q, int64_t ldq, const bi_bf16* k, int64
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(cos_sin) ||
       !aligned16(q_out) || !aligned16(k_out) || ldq % 8 || ldk % 8 || ldq_out % 8 || ldk_out % 8)
     return BI_ERR_ALIGN;
-  if ((T * (Hq + Hkv) * (D / 16) + bi::qknorm::kThreads - 1) / bi::qknorm::kThreads > INT_MAX) return BI_ERR_SHAPE;
+  if (T * (Hq + Hkv) > INT_MAX) return BI_ERR_SHAPE;  // heads are counted in 31 bits
   if (T == 0) return BI_OK;
   // in place only row for row; otherwise no output may share an element with an input or the other output
   if (q_out == q ? ldq_out != ldq : blocks_overlap(q, ldq, nq, q_out, ldq_out, nq, T)) return BI_ERR_SHAPE;
@@ -732,8 +732,10 @@ bi_status bi_qk_norm_rope(const bi_bf16* q, int64_t ldq, const bi_bf16* k, int64
   if (blocks_overlap(q, ldq, nq, k_out, ldk_out, nk, T) || blocks_overlap(k, ldk, nk, q_out, ldq_out, nq, T) ||
       blocks_overlap(q_out, ldq_out, nq, k_out, ldk_out, nk, T))
     return BI_ERR_SHAPE;
+  const int sms = device_sms();
+  if (sms <= 0) return BI_ERR_CUDA;
   return bi::qknorm::launch({q, ldq, q_weight, q_out, ldq_out}, {k, ldk, k_weight, k_out, ldk_out}, T, Hq, Hkv, D, pos,
-                            reinterpret_cast<const float2*>(cos_sin), max_pos, eps, as_stream(stream)) == cudaSuccess
+                            reinterpret_cast<const float2*>(cos_sin), max_pos, eps, sms, as_stream(stream)) == cudaSuccess
              ? BI_OK
              : BI_ERR_CUDA;
 }

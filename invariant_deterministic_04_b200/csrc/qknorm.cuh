@@ -28,79 +28,96 @@ struct Part {  // queries or keys: rows t at x + t * ldx, written to y + t * ldy
 
 constexpr int kThreads = 256;
 
-// One head row per D/16 lanes; heads 0 .. Hq-1 are queries, Hq .. Hq+Hkv-1 keys.
-template <int D>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(Part q, Part k, int Hq, int H, int64_t nheads,
-                                                                const int32_t* __restrict__ pos,
+// D/16 lanes take HPG heads of one token: j, j + J, j + 2 J, ... with J = ceil(H / HPG) groups of
+// lanes a token (heads 0 .. Hq-1 are queries, Hq .. H-1 keys), so that the table row and
+// the weights are read once for several heads and several heads' loads are in flight.
+// groups is T * J.
+template <int D, int HPG>
+__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(Part q, Part k, uint32_t Hq, uint32_t H, uint32_t J,
+                                                                uint32_t groups, const int32_t* __restrict__ pos,
                                                                 const float2* __restrict__ table, int max_pos,
                                                                 float eps) {
-  constexpr int LPH = D / 16;
-  const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t th = e / LPH;
-  const int j = (int)(e % LPH);
+  constexpr uint32_t LPH = D / 16;
+  const uint32_t group = blockIdx.x * (kThreads / LPH) + threadIdx.x / LPH;
+  const int j = (int)(threadIdx.x % LPH);
   pdl_wait();  // inputs written by the previous kernel on the stream are complete from here on
   pdl_trigger();
-  // lanes past the end redo the last head's work without storing (the butterfly needs whole warps)
-  const bool live = th < nheads;
-  const int64_t hh = live ? th : nheads - 1;
-  const int64_t t = hh / H;
-  const int h = (int)(hh - t * H);
-  const bool is_q = h < Hq;
-  const Part p = is_q ? q : k;
-  const int64_t col = (int64_t)(is_q ? h : h - Hq) * D + 8 * j;
-  float a[8], b[8];
-  unpack8(*reinterpret_cast<const uint4*>(p.x + t * p.ldx + col), a);
-  unpack8(*reinterpret_cast<const uint4*>(p.x + t * p.ldx + col + D / 2), b);
-  float ss = 0.f;
+  // lanes past the end redo the last group's work without storing (the butterfly needs whole warps)
+  const uint32_t gr = min(group, groups - 1), t = gr / J, h0 = gr - t * J;
+  uint4 x[HPG][2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss = __fmaf_rn(a[i], a[i], ss);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ss = __fmaf_rn(b[i], b[i], ss);
-#pragma unroll
-  for (int off = LPH / 2; off >= 1; off >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(kFullMask, ss, off));
-  const float r = rsqrtf(__fadd_rn(__fdiv_rn(ss, (float)D), eps));
+  for (int i = 0; i < HPG; ++i) {
+    const uint32_t h = min(h0 + i * J, H - 1);
+    const uint16_t* row = h < Hq ? q.x + (int64_t)t * q.ldx + (int64_t)h * D : k.x + (int64_t)t * k.ldx + (int64_t)(h - Hq) * D;
+    x[i][0] = *reinterpret_cast<const uint4*>(row + 8 * j);
+    x[i][1] = *reinterpret_cast<const uint4*>(row + D / 2 + 8 * j);
+  }
   const int ps = pos[t];
-  if (!live) return;
-  if (ps < 0 || ps >= max_pos) {
-    if (j == 0) record_error(BI_ERR_DEVICE_INDEX);
-    return;
-  }
-  float wa[8], wb[8], ya[8], yb[8];
-  unpack8(__ldg(reinterpret_cast<const uint4*>(p.w + 8 * j)), wa);
-  unpack8(__ldg(reinterpret_cast<const uint4*>(p.w + D / 2 + 8 * j)), wb);
-  const float4* cs = reinterpret_cast<const float4*>(table + (int64_t)ps * (D / 2) + 8 * j);
+  const bool ok = ps >= 0 && ps < max_pos;
+  if (group < groups && !ok && j == 0) record_error(BI_ERR_DEVICE_INDEX);
+  float4 cs[4];
+  const float4* row_cs = reinterpret_cast<const float4*>(table + (int64_t)(ok ? ps : 0) * (D / 2) + 8 * j);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 c = __ldg(cs + i);
-    const float n0 = __fmul_rn(__fmul_rn(a[2 * i], r), wa[2 * i]), m0 = __fmul_rn(__fmul_rn(b[2 * i], r), wb[2 * i]);
-    const float n1 = __fmul_rn(__fmul_rn(a[2 * i + 1], r), wa[2 * i + 1]);
-    const float m1 = __fmul_rn(__fmul_rn(b[2 * i + 1], r), wb[2 * i + 1]);
-    ya[2 * i] = __fmaf_rn(n0, c.x, -__fmul_rn(m0, c.y));
-    yb[2 * i] = __fmaf_rn(m0, c.x, __fmul_rn(n0, c.y));
-    ya[2 * i + 1] = __fmaf_rn(n1, c.z, -__fmul_rn(m1, c.w));
-    yb[2 * i + 1] = __fmaf_rn(m1, c.z, __fmul_rn(n1, c.w));
+  for (int i = 0; i < 4; ++i) cs[i] = __ldg(row_cs + i);
+#pragma unroll
+  for (int i = 0; i < HPG; ++i) {
+    const uint32_t h = h0 + i * J;
+    float a[8], b[8];
+    unpack8(x[i][0], a);
+    unpack8(x[i][1], b);
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = __fmaf_rn(a[e], a[e], ss);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = __fmaf_rn(b[e], b[e], ss);
+#pragma unroll
+    for (int off = LPH / 2; off >= 1; off >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(kFullMask, ss, off));
+    const float r = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.f / D), eps));  // 1 / D is a power of two
+    const bool is_q = h < Hq;
+    const uint16_t* w = is_q ? q.w : k.w;
+    float wa[8], wb[8], ya[8], yb[8];
+    unpack8(__ldg(reinterpret_cast<const uint4*>(w + 8 * j)), wa);
+    unpack8(__ldg(reinterpret_cast<const uint4*>(w + D / 2 + 8 * j)), wb);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float c = e & 1 ? cs[e / 2].z : cs[e / 2].x, s = e & 1 ? cs[e / 2].w : cs[e / 2].y;
+      const float n = __fmul_rn(__fmul_rn(a[e], r), wa[e]), m = __fmul_rn(__fmul_rn(b[e], r), wb[e]);
+      ya[e] = __fmaf_rn(n, c, -__fmul_rn(m, s));
+      yb[e] = __fmaf_rn(m, c, __fmul_rn(n, s));
+    }
+    if (group >= groups || !ok || h >= H) continue;
+    uint16_t* y = (is_q ? q.y + (int64_t)t * q.ldy + (int64_t)h * D : k.y + (int64_t)t * k.ldy + (int64_t)(h - Hq) * D) + 8 * j;
+    *reinterpret_cast<uint4*>(y) = make_uint4(pack_bf16x2(ya[0], ya[1]), pack_bf16x2(ya[2], ya[3]),
+                                              pack_bf16x2(ya[4], ya[5]), pack_bf16x2(ya[6], ya[7]));
+    *reinterpret_cast<uint4*>(y + D / 2) = make_uint4(pack_bf16x2(yb[0], yb[1]), pack_bf16x2(yb[2], yb[3]),
+                                                      pack_bf16x2(yb[4], yb[5]), pack_bf16x2(yb[6], yb[7]));
   }
-  uint16_t* y = p.y + t * p.ldy + col;
-  *reinterpret_cast<uint4*>(y) = make_uint4(pack_bf16x2(ya[0], ya[1]), pack_bf16x2(ya[2], ya[3]),
-                                            pack_bf16x2(ya[4], ya[5]), pack_bf16x2(ya[6], ya[7]));
-  *reinterpret_cast<uint4*>(y + D / 2) = make_uint4(pack_bf16x2(yb[0], yb[1]), pack_bf16x2(yb[2], yb[3]),
-                                                    pack_bf16x2(yb[4], yb[5]), pack_bf16x2(yb[6], yb[7]));
+}
+
+template <int D, int HPG>
+inline cudaError_t launch_hpg(const Part& q, const Part& k, int64_t T, int Hq, int H, const int32_t* pos,
+                              const float2* table, int max_pos, float eps, cudaStream_t st) {
+  const uint32_t J = (uint32_t)((H + HPG - 1) / HPG), groups = (uint32_t)(T * J);
+  constexpr uint32_t per = kThreads / (D / 16);
+  return launch_pdl(qk_norm_rope_kernel<D, HPG>, dim3(groups / per + (groups % per != 0)), dim3(kThreads), 0, st, q, k,
+                    (uint32_t)Hq, (uint32_t)H, J, groups, pos, table, max_pos, eps);
+}
+
+// Four heads a group of lanes once one head each would give the SMs more than twice the threads
+// they hold; below that more, shorter threads finish sooner.
+template <int D>
+inline cudaError_t launch_d(const Part& q, const Part& k, int64_t T, int Hq, int H, const int32_t* pos, const float2* table,
+                            int max_pos, float eps, int sms, cudaStream_t st) {
+  return T * H * (D / 16) > (int64_t)sms * 4096 ? launch_hpg<D, 4>(q, k, T, Hq, H, pos, table, max_pos, eps, st)
+                                                : launch_hpg<D, 1>(q, k, T, Hq, H, pos, table, max_pos, eps, st);
 }
 
 inline cudaError_t launch(const Part& q, const Part& k, int64_t T, int Hq, int Hkv, int D, const int32_t* pos,
-                          const float2* table, int max_pos, float eps, cudaStream_t st) {
-  const int64_t nheads = T * (Hq + Hkv);
-  const unsigned grid = (unsigned)((nheads * (D / 16) + kThreads - 1) / kThreads);
+                          const float2* table, int max_pos, float eps, int sms, cudaStream_t st) {
   switch (D) {
-    case 64:
-      return launch_pdl(qk_norm_rope_kernel<64>, dim3(grid), dim3(kThreads), 0, st, q, k, Hq, Hq + Hkv, nheads, pos,
-                        table, max_pos, eps);
-    case 128:
-      return launch_pdl(qk_norm_rope_kernel<128>, dim3(grid), dim3(kThreads), 0, st, q, k, Hq, Hq + Hkv, nheads, pos,
-                        table, max_pos, eps);
-    default:
-      return launch_pdl(qk_norm_rope_kernel<256>, dim3(grid), dim3(kThreads), 0, st, q, k, Hq, Hq + Hkv, nheads, pos,
-                        table, max_pos, eps);
+    case 64: return launch_d<64>(q, k, T, Hq, Hq + Hkv, pos, table, max_pos, eps, sms, st);
+    case 128: return launch_d<128>(q, k, T, Hq, Hq + Hkv, pos, table, max_pos, eps, sms, st);
+    default: return launch_d<256>(q, k, T, Hq, Hq + Hkv, pos, table, max_pos, eps, sms, st);
   }
 }
 
