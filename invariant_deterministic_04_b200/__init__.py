@@ -484,12 +484,12 @@ def kv_append(k_new, v_new, q_seq, q_pos, k_cache, v_cache, page_table, stream=N
             _ptr(page_table), num_seqs, maxp, T, Hkv, D, _stream()))
 
 
-_KV_KINDS = {torch.int8: 0, torch.float8_e4m3fn: 1}
+KV_KINDS = {torch.int8: 0, torch.float8_e4m3fn: 1}  # BI_KV_INT8, BI_KV_E4M3
 
 
 def _store_q8(k_cache, v_cache, k_scale, v_scale, page_table):
     """Check an 8-bit store; returns (num_pages, Hkv, D, kind)."""
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dtype not in _KV_KINDS:
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dtype not in KV_KINDS:
         raise TypeError("k_cache must be a CUDA tensor of torch.int8 or torch.float8_e4m3fn")
     _need(k_cache, k_cache.dtype, "k_cache", 4)
     _need(v_cache, k_cache.dtype, "v_cache", 4)
@@ -501,7 +501,7 @@ def _store_q8(k_cache, v_cache, k_scale, v_scale, page_table):
         raise ValueError("k_cache/v_cache must be [num_pages, Hkv, 16, D]")
     if k_scale.shape != (num_pages, Hkv, P) or v_scale.shape != k_scale.shape:
         raise ValueError("k_scale/v_scale must be [num_pages, Hkv, 16]")
-    return num_pages, Hkv, D, _KV_KINDS[k_cache.dtype]
+    return num_pages, Hkv, D, KV_KINDS[k_cache.dtype]
 
 
 def _row_ids(q_seq, q_pos, T: int):

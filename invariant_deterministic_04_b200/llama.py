@@ -7,6 +7,9 @@ RMSNorm, the tcgen05 matmul, RoPE, KV append into the paged store, causal attent
 over the store (prefill chunks and decode tokens in one call), SwiGLU, residual add
 and the LM head with its selective FP32 recompute. Torch only provides memory.
 
+``kv_dtype`` (torch.int8 or torch.float8_e4m3fn) keeps the store in 8 bits, and layers
+with ``q_norm`` / ``k_norm`` weights norm each query and key head before the rotation.
+
 ``BaselineLlama`` runs the same weights through stock torch ops (cuBLAS matmuls,
 F.rms_norm, padded batched attention, matmul + argmax LM head): the non-invariant
 comparison path.
@@ -34,22 +37,36 @@ def rope_cos_sin(max_pos: int, D: int, theta: float, device) -> torch.Tensor:
 
 class PagedStore:
     """Per-layer K/V stores [num_pages, Hkv, 16, D] and one page-table row per sequence
-    (pages of a sequence are a fixed, shuffled set of physical pages)."""
+    (pages of a sequence are a fixed, shuffled set of physical pages). An 8-bit kv_dtype
+    adds the fp32 scales [num_pages, Hkv, 16] in ks and vs."""
 
-    def __init__(self, layers, n_seqs, max_pos, kv_heads, head_dim, device, seed=0):
+    def __init__(self, layers, n_seqs, max_pos, kv_heads, head_dim, device, seed=0, kv_dtype=torch.bfloat16):
+        if kv_dtype not in (torch.bfloat16, torch.int8, torch.float8_e4m3fn):
+            raise TypeError(f"kv_dtype must be torch.bfloat16, torch.int8 or torch.float8_e4m3fn, got {kv_dtype}")
         self.max_pages = math.ceil(max_pos / PAGE)
         n = n_seqs * self.max_pages
         perm = torch.randperm(n, generator=torch.Generator().manual_seed(seed)).to(torch.int32)
         self.page_table = perm.view(n_seqs, self.max_pages).contiguous().to(device)
         shape = (n, kv_heads, PAGE, head_dim)
-        self.k = [torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(layers)]
-        self.v = [torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(layers)]
+        self.quantised = kv_dtype != torch.bfloat16
+        self.k = [torch.zeros(shape, dtype=kv_dtype, device=device) for _ in range(layers)]
+        self.v = [torch.zeros(shape, dtype=kv_dtype, device=device) for _ in range(layers)]
+        if self.quantised:
+            self.ks = [torch.ones(shape[:3], dtype=torch.float32, device=device) for _ in range(layers)]
+            self.vs = [torch.ones(shape[:3], dtype=torch.float32, device=device) for _ in range(layers)]
+
+    def layer(self, l):
+        """The tensors that the binding's calls on layer l take (kv_append, attention_prefill, or their _q8 forms)."""
+        if self.quantised:
+            return self.k[l], self.v[l], self.ks[l], self.vs[l], self.page_table
+        return self.k[l], self.v[l], self.page_table
 
 
 class BiLlama:
-    def __init__(self, cfg, weights, n_seqs, max_pos, device, threshold=0.5):
+    def __init__(self, cfg, weights, n_seqs, max_pos, device, threshold=0.5, kv_dtype=torch.bfloat16):
         self.cfg, self.w, self.device, self.threshold = cfg, weights, device, threshold
-        self.store = PagedStore(cfg["layers"], n_seqs, max_pos, cfg["kv_heads"], cfg["head_dim"], device)
+        self.store = PagedStore(cfg["layers"], n_seqs, max_pos, cfg["kv_heads"], cfg["head_dim"], device,
+                                kv_dtype=kv_dtype)
         self.table = rope_cos_sin(max_pos, cfg["head_dim"], cfg["theta"], device)
         self.recomputed = 0
         self.lm_rows = 0
@@ -69,10 +86,17 @@ class BiLlama:
             q = qkv[:, : nh * D].view(T, nh, D)
             k = qkv[:, nh * D: (nh + nkv) * D].view(T, nkv, D)
             v = qkv[:, (nh + nkv) * D:].view(T, nkv, D)
-            bi.rope(q, q_pos, self.table)
-            bi.rope(k, q_pos, self.table)
-            bi.kv_append(k, v, q_seq, q_pos, st.k[l], st.v[l], st.page_table)
-            att = bi.attention_prefill(q, q_seq, q_pos, st.k[l], st.v[l], st.page_table)
+            if "q_norm" in lw:
+                bi.qk_norm_rope(q, k, lw["q_norm"], lw["k_norm"], q_pos, self.table, c["eps"])
+            else:
+                bi.rope(q, q_pos, self.table)
+                bi.rope(k, q_pos, self.table)
+            if st.quantised:
+                bi.kv_append_q8(k, v, q_seq, q_pos, *st.layer(l))
+                att = bi.attention_prefill_q8(q, q_seq, q_pos, *st.layer(l))
+            else:
+                bi.kv_append(k, v, q_seq, q_pos, *st.layer(l))
+                att = bi.attention_prefill(q, q_seq, q_pos, *st.layer(l))
             o = bi.matmul(att.view(T, nh * D), lw["wo"])
             bi.add(h, o, out=h)
             bi.rmsnorm(h, lw["mlp_norm"], c["eps"], out=x)
@@ -96,7 +120,12 @@ class BiLlama:
 
 
 class BaselineLlama(BiLlama):
-    """Same weights and store, stock torch ops (the non-invariant path)."""
+    """Same weights and (bf16) store, stock torch ops (the non-invariant path); no head norms."""
+
+    def __init__(self, cfg, weights, n_seqs, max_pos, device, threshold=0.5):
+        if any("q_norm" in lw for lw in weights["layers"]):
+            raise ValueError("BaselineLlama has no head norms")
+        super().__init__(cfg, weights, n_seqs, max_pos, device, threshold)
 
     def forward(self, seqs, poss, toks, want):
         c, w, st, dev = self.cfg, self.w, self.store, self.device
@@ -218,8 +247,9 @@ class FastBiLlama(BiLlama):
     """BiLlama with preallocated buffers and direct C-ABI calls (raw pointers, no
     per-call tensor checks): the same kernels and arguments, less host overhead."""
 
-    def __init__(self, cfg, weights, n_seqs, max_pos, device, threshold=0.5, max_rows=8192, max_want=64):
-        super().__init__(cfg, weights, n_seqs, max_pos, device, threshold)
+    def __init__(self, cfg, weights, n_seqs, max_pos, device, threshold=0.5, max_rows=8192, max_want=64,
+                 kv_dtype=torch.bfloat16):
+        super().__init__(cfg, weights, n_seqs, max_pos, device, threshold, kv_dtype)
         c = cfg
         H, nh, nkv, D, F, V = (c[k] for k in ("hidden", "heads", "kv_heads", "head_dim", "ffn", "vocab"))
         self.L = bi.lib()
@@ -236,7 +266,9 @@ class FastBiLlama(BiLlama):
         self.hs, self.hn = e(max_want, H), e(max_want, H)
         self.tok = torch.empty(max_want, dtype=torch.int32, device=device)
         self.rec = torch.empty(max_want, dtype=torch.int32, device=device)
-        self.ws_att = torch.empty(bi.attention_workspace_size(max_rows, nh, D, self.store.max_pages),
+        self.kind = bi.KV_KINDS.get(kv_dtype)
+        self.ws_att = torch.empty(bi.attention_prefill_q8_workspace_size(max_rows) if self.store.quantised else
+                                  bi.attention_workspace_size(max_rows, nh, D, self.store.max_pages),
                                   dtype=torch.uint8, device=device)
         self.ws_lm = torch.empty(bi.lmhead_workspace_size(max_want, V), dtype=torch.uint8, device=device)
         self.max_rows, self.max_want = max_rows, max_want
@@ -274,12 +306,25 @@ class FastBiLlama(BiLlama):
             kc, vc = st.k[l].data_ptr(), st.v[l].data_ptr()
             self._ok("rmsnorm", L.bi_rmsnorm(h, H, lw["attn_norm"].data_ptr(), x, H, T, H, c["eps"], s))
             self._ok("qkv", L.bi_matmul(x, H, lw["wqkv"].data_ptr(), H, qkv, QKV, T, QKV, H, s))
-            self._ok("rope q", L.bi_rope(qkv, QKV, T, nh, D, q_pos, tab, self.table.shape[0], s))
-            self._ok("rope k", L.bi_rope(qkv + 2 * nh * D, QKV, T, nkv, D, q_pos, tab, self.table.shape[0], s))
-            self._ok("append", L.bi_kv_append(qkv + 2 * nh * D, qkv + 2 * (nh + nkv) * D, QKV, q_seq, q_pos, kc, vc,
-                                              npages, pt, n_seqs, maxp, T, nkv, D, s))
-            self._ok("attn", L.bi_attention_prefill(qkv, QKV, q_seq, q_pos, kc, vc, npages, pt, n_seqs, maxp, att, T,
-                                                    nh, nkv, D, scale, ws, wsb, s))
+            kn, vn = qkv + 2 * nh * D, qkv + 2 * (nh + nkv) * D
+            if "q_norm" in lw:
+                self._ok("qk norm", L.bi_qk_norm_rope(qkv, QKV, kn, QKV, lw["q_norm"].data_ptr(), lw["k_norm"].data_ptr(),
+                                                      q_pos, tab, self.table.shape[0], c["eps"], qkv, QKV, kn, QKV, T,
+                                                      nh, nkv, D, s))
+            else:
+                self._ok("rope q", L.bi_rope(qkv, QKV, T, nh, D, q_pos, tab, self.table.shape[0], s))
+                self._ok("rope k", L.bi_rope(kn, QKV, T, nkv, D, q_pos, tab, self.table.shape[0], s))
+            if st.quantised:
+                ks, vs = st.ks[l].data_ptr(), st.vs[l].data_ptr()
+                self._ok("append", L.bi_kv_append_q8(kn, vn, QKV, q_seq, q_pos, kc, vc, ks, vs, self.kind, npages, pt,
+                                                     n_seqs, maxp, T, nkv, D, s))
+                self._ok("attn", L.bi_attention_prefill_q8(qkv, QKV, q_seq, q_pos, kc, vc, ks, vs, self.kind, npages,
+                                                           pt, n_seqs, maxp, att, T, nh, nkv, D, scale, ws, wsb, s))
+            else:
+                self._ok("append", L.bi_kv_append(kn, vn, QKV, q_seq, q_pos, kc, vc, npages, pt, n_seqs, maxp, T, nkv,
+                                                  D, s))
+                self._ok("attn", L.bi_attention_prefill(qkv, QKV, q_seq, q_pos, kc, vc, npages, pt, n_seqs, maxp, att,
+                                                        T, nh, nkv, D, scale, ws, wsb, s))
             self._ok("o", L.bi_matmul(att, nh * D, lw["wo"].data_ptr(), nh * D, o, H, T, H, nh * D, s))
             self._ok("add", L.bi_add(h, o, h, T * H, s))
             self._ok("rmsnorm", L.bi_rmsnorm(h, H, lw["mlp_norm"].data_ptr(), x, H, T, H, c["eps"], s))
