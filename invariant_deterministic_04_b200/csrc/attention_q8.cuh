@@ -355,12 +355,10 @@ __device__ __forceinline__ uint32_t chunk_at(int t, int i) {
   return (uint32_t)(t * D + ((i ^ (D == 128 ? (t & 7) : ((t >> 1) & 3))) << 4));
 }
 
-// Folds a page. masked: `seen` of its tokens exist, query row (n, r) sees nv(n, r).
-template <int KIND, int D, int NT, typename Nv>
-__device__ __forceinline__ void fold_page(const Query<D, NT>& Q, uint32_t page, uint32_t scales, bool masked, Nv nv, int seen,
-                                          int live, int lane, State<D, NT>& S) {
+// Scores of a page: tokens g and g + 8 of query rows 8 n + 2c and + 1, before any scale.
+template <int KIND, int D, int NT>
+__device__ __forceinline__ void page_scores(const Query<D, NT>& Q, uint32_t page, int lane, float (&s)[NT][4]) {
   const int g = lane >> 2, c = lane & 3;
-  float s[NT][4];
   const uint32_t k0 = page + chunk_at<D>(g, c);  // chunk c + 4 of a 128-byte row: bit 6 flipped
 #pragma unroll
   for (int v = 0; v < D / 64; ++v) {
@@ -377,6 +375,13 @@ __device__ __forceinline__ void fold_page(const Query<D, NT>& Q, uint32_t page, 
       }
     }
   }
+}
+
+// Folds a page whose scores are s. masked: `seen` of its tokens exist, query row (n, r) sees nv(n, r).
+template <int KIND, int D, int NT, typename Nv>
+__device__ __forceinline__ void fold_page(const Query<D, NT>& Q, float (&s)[NT][4], uint32_t page, uint32_t scales,
+                                          bool masked, Nv nv, int seen, int live, int lane, State<D, NT>& S) {
+  const int g = lane >> 2, c = lane & 3;
   Tokens T;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -589,22 +594,38 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT == 256 ? 3 : 4)
     }
     State<D, NT> S;
     S.clear();
-    for (int j = 0; j * PAGE < cur.seen; ++j) {
-      const uint32_t st = used % kStages;
-      if (!__all_sync(kFullMask, mbar_wait(bars + 8 * st, (used / kStages) & 1u))) {
+    const uint32_t usable = __ballot_sync(kFullMask, cur.page >= 0);
+    // Two pages at a time: the second's scores are under way during the first's weights. A page that
+    // is not there, or unusable, is one of whose tokens none is seen (whatever its stage holds).
+    for (int j = 0; j * PAGE < cur.seen; j += 2) {
+      const bool second = (j + 1) * PAGE < cur.seen;
+      bool ok = mbar_wait(bars + 8 * (used % kStages), (used / kStages) & 1u);
+      if (second) ok = ok && mbar_wait(bars + 8 * ((used + 1) % kStages), ((used + 1) / kStages) & 1u);
+      if (!__all_sync(kFullMask, ok)) {
         // a copy never landed (recorded): let the others land, then leave
         if (lane == 0) drain_copies(bars, 8, filled, ph_bits);
         __syncwarp();
         return;
       }
-      if (__shfl_sync(kFullMask, cur.page, j) >= 0) {  // the tokens of an unusable page are not seen
-        const int seen = cur.seen - j * PAGE;
-        fold_page<KIND, D, NT>(Q, ring + st * kPageBytes<D>, scales + st * kScaleBytes, seen < PAGE,
-                               [&](int, int) { return seen; }, seen, NT, lane, S);
+      float s[2][NT][4];
+      int seen[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        seen[u] = (usable >> (j + u)) & 1u ? cur.seen - (j + u) * PAGE : 0;
+        if (NT == 1 || u == 0) page_scores<KIND, D, NT>(Q, ring + ((used + u) % kStages) * kPageBytes<D>, lane, s[u]);
       }
-      ++used;
-      __syncwarp();  // every lane has read this page: its stage may be refilled
+      const bool masked = seen[0] < PAGE || seen[1] < PAGE;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t st = (used + u) % kStages;
+        if (NT > 1 && u == 1) page_scores<KIND, D, NT>(Q, ring + st * kPageBytes<D>, lane, s[u]);  // (no registers for both)
+        fold_page<KIND, D, NT>(Q, s[u], ring + st * kPageBytes<D>, scales + st * kScaleBytes, masked,
+                               [&](int, int) { return seen[u]; }, seen[u], NT, lane, S);
+      }
+      __syncwarp();  // every lane has read these pages: their stages may be refilled
+      used += second ? 2 : 1;
       issue();
+      if (second) issue();
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -1307,8 +1328,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3)
         __syncwarp();
         if (__shfl_sync(kFullMask, page, j) >= 0) {
           const int tp = t0 + j * PAGE;
-          const uint32_t st = (uint32_t)(j % kFewStages);
-          fold_page<KIND, D, kFewNT>(Q, ring + st * kPageBytes<D>, scales + st * kScaleBytes, tp + PAGE > shortest,
+          const uint32_t st = (uint32_t)(j % kFewStages), pg = ring + st * kPageBytes<D>;
+          float s[kFewNT][4];
+          page_scores<KIND, D, kFewNT>(Q, pg, lane, s);
+          fold_page<KIND, D, kFewNT>(Q, s, pg, scales + st * kScaleBytes, tp + PAGE > shortest,
                                      [&](int n, int r) { return len[n][r] - tp; }, longest - tp, live, lane, S);
         }
         __syncwarp();
