@@ -658,14 +658,14 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT == 256 ? 3 : 4)
 // Folds a row's splits in ascending order; one warp per (row, query head, 32 * DPL output dims).
 // The lanes take the splits' maxima 32 at a time: the running maximum before and after each
 // split (a maximum is exact in any order) gives the weights of both sides of its fold step, and
-// the fold itself is one chain per output dim in split order whatever DPL is. Partials are
-// loaded U at a time.
+// the fold itself is one chain per output dim in split order whatever DPL is. The partial
+// outputs come U at a time, the next U and the next 32 maxima asked for before these are folded.
 template <int D, int DPL>
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ po, const float2* __restrict__ pml,
                                                       Rows R, int nrows, int max_splits, int Hq,
                                                       uint16_t* __restrict__ out) {
   constexpr int NG = D / (32 * DPL);  // warps per (row, head)
-  constexpr int U = DPL == 1 ? 16 : 8;
+  constexpr int U = DPL == 1 ? 16 : 4;
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   pdl_wait();  // the split partials are complete from here on
@@ -680,46 +680,61 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
   float M = kLowest, L = 0.f, O[DPL];
 #pragma unroll
   for (int d = 0; d < DPL; ++d) O[d] = 0.f;
-  for (int s0 = 0; s0 < n; s0 += 32) {
-    const float2 ml = s0 + lane < n ? pml[slot0 + (int64_t)(s0 + lane) * Hq] : make_float2(kLowest, 0.f);
-    float top = ml.x;  // the running maximum up to and with this lane's split
+  auto load = [&](int s0, float (&v)[U][DPL]) {  // splits s0 .. s0 + U - 1 (past n: the last again, unused)
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const float y = __shfl_up_sync(kFullMask, top, d);
-      if (lane >= d) top = fmaxf(top, y);
-    }
-    top = fmaxf(top, M);
-    float prev = __shfl_up_sync(kFullMask, top, 1);
-    if (lane == 0) prev = M;
-    float a, b;
-    join(prev, ml.x, a, b);
-    M = __shfl_sync(kFullMask, top, 31);
-    const int cnt = min(32, n - s0);
-    for (int u0 = 0; u0 < cnt; u0 += U) {
-      float v[U][DPL];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float* p = src + (int64_t)(s0 + min(u0 + u, cnt - 1)) * Hq * D;
-        if constexpr (DPL == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(p);
-          v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
-        } else if constexpr (DPL == 2) {
-          const float2 x = *reinterpret_cast<const float2*>(p);
-          v[u][0] = x.x; v[u][1] = x.y;
-        } else {
-          v[u][0] = *p;
-        }
+    for (int u = 0; u < U; ++u) {
+      const float* p = src + (int64_t)min(s0 + u, n - 1) * Hq * D;
+      if constexpr (DPL == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+      } else if constexpr (DPL == 2) {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        v[u][0] = x.x; v[u][1] = x.y;
+      } else {
+        v[u][0] = *p;
       }
+    }
+  };
+  auto load_ml = [&](int s0) {
+    return s0 + lane < n ? pml[slot0 + (int64_t)(s0 + lane) * Hq] : make_float2(kLowest, 0.f);
+  };
+  if (n > 0) {
+    float va[U][DPL], vb[U][DPL];
+    float2 ml = load_ml(0), next = load_ml(32);
+    load(0, va);
+    float a = 0.f, b = 0.f;
+    auto fold = [&](int s0, const float (&v)[U][DPL]) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const float ak = __shfl_sync(kFullMask, a, (u0 + u) & 31), bk = __shfl_sync(kFullMask, b, (u0 + u) & 31);
-        const float lk = __shfl_sync(kFullMask, ml.y, (u0 + u) & 31);
-        if (u0 + u < cnt) {
+        const int at = (s0 + u) & 31;
+        const float ak = __shfl_sync(kFullMask, a, at), bk = __shfl_sync(kFullMask, b, at);
+        const float lk = __shfl_sync(kFullMask, ml.y, at);
+        if (s0 + u < n) {
           L = __fmaf_rn(lk, bk, __fmul_rn(L, ak));
 #pragma unroll
           for (int d = 0; d < DPL; ++d) O[d] = __fmaf_rn(v[u][d], bk, __fmul_rn(O[d], ak));
         }
       }
+    };
+    for (int s0 = 0; s0 < n; s0 += 2 * U) {
+      if (s0 + U < n) load(s0 + U, vb);
+      if (s0 % 32 == 0) {
+        if (s0) ml = next, next = load_ml(s0 + 32);
+        float top = ml.x;  // the running maximum up to and with this lane's split
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const float y = __shfl_up_sync(kFullMask, top, d);
+          if (lane >= d) top = fmaxf(top, y);
+        }
+        top = fmaxf(top, M);
+        float prev = __shfl_up_sync(kFullMask, top, 1);
+        if (lane == 0) prev = M;
+        join(prev, ml.x, a, b);
+        M = __shfl_sync(kFullMask, top, 31);
+      }
+      fold(s0, va);
+      if (s0 + 2 * U < n) load(s0 + 2 * U, va);
+      if (s0 + U < n) fold(s0 + U, vb);
     }
   }
   float y[DPL];
