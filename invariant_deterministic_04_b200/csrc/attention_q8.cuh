@@ -1086,7 +1086,7 @@ __device__ __forceinline__ void fold_tile(const TileArgs& A, uint8_t* smem, uint
   const int g = lane >> 2, c = lane & 3;
   constexpr int CHUNK = M::PAGES * PAGE;
   Query<D, LIVE> Q;
-  int shortest = INT_MAX, longest = 0;
+  int shortest = INT_MAX;
   // visible tokens of the lane's query rows, and running totals over splits, in places of this lane's own
   int2* lens = reinterpret_cast<int2*>(smem + M::LENS) + warp * 32 * kNT + lane;               // entry n at [32 n]
   float* tot = reinterpret_cast<float*>(smem + M::TOTALS) + warp * (kNT * 8) * D + lane;       // entry i at [32 i]
@@ -1104,12 +1104,10 @@ __device__ __forceinline__ void fold_tile(const TileArgs& A, uint8_t* smem, uint
       if (k >= A.rows) continue;
       int pt_row;
       len[r] = attn::row_len(A.R, A.first + k / A.G, pt_row);
-      longest = max(longest, len[r]);
       shortest = min(shortest, len[r]);
     }
     lens[32 * n] = make_int2(len[0], len[1]);
   }
-  longest = __reduce_max_sync(kFullMask, longest);
   shortest = __reduce_min_sync(kFullMask, shortest);
 #pragma unroll
   for (int n = 0; n < LIVE; ++n) stats[32 * n] = make_float4(kLowest, kLowest, 0.f, 0.f);
@@ -1123,10 +1121,9 @@ __device__ __forceinline__ void fold_tile(const TileArgs& A, uint8_t* smem, uint
     for (int tp = t0; tp < min(t0 + SPLIT, A.len); tp += CHUNK, ++it) {
       const uint32_t stage = base + (it % kRing) * M::STAGE, full = bars + (it % kRing) * 16;
       ring_wait(full, (it / kRing) & 1u, dead);
-#pragma unroll 1
-      for (int p = 0; p < M::PAGES; p += 2) {
+#pragma unroll
+      for (int p = 0; p < M::PAGES; p += 2) {  // (pages that none of its rows sees too: a way round them costs more)
         const int at = tp + p * PAGE;
-        if (at >= longest) break;
         fold_wide<D, LIVE>(Q, stage, p, at + 2 * PAGE > shortest,
                            [&](int n, int r) {
                              const int2 len = lens[32 * n];
