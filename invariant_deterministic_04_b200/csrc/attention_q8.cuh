@@ -774,28 +774,30 @@ struct Counts {
 // owning a contiguous stretch of rows. A tile whose run ends within `few` tokens is a few-row tile.
 __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ q_seq, int T, int per, int few,
                                                     int32_t* __restrict__ list, Counts* __restrict__ counts) {
-  __shared__ int32_t start[1024];
-  __shared__ int32_t sums[2][1024];
-  const int tid = threadIdx.x;
+  __shared__ int32_t warp_last[32];
+  __shared__ int2 warp_count[32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_trigger();
   const int each = (T + 1023) / 1024;
   const int r0 = (int)min((int64_t)tid * each, (int64_t)T), r1 = min(r0 + each, T);
   auto starts = [&](int r) { return r == 0 || q_seq[r] != q_seq[r - 1]; };
   auto is_few = [&](int r) { return r + few >= T || q_seq[r + few] != q_seq[r]; };
-  // the start of the run that row r0 - 1 lies in, from the running maximum of run starts
+  // the start of the run that row r0 - 1 lies in: the running maximum of run starts before this thread
   int last = -1;
   for (int r = r0; r < r1; ++r)
     if (starts(r)) last = r;
-  start[tid] = last;
-  __syncthreads();
-  for (int d = 1; d < 1024; d <<= 1) {
-    const int v = tid >= d ? start[tid - d] : -1;
-    __syncthreads();
-    start[tid] = max(start[tid], v);
-    __syncthreads();
+  int upto = last;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(kFullMask, upto, d);
+    if (lane >= d) upto = max(upto, v);
   }
-  const int before = tid ? start[tid - 1] : -1;
+  if (lane == 31) warp_last[warp] = upto;
+  __syncthreads();
+  int before = __shfl_up_sync(kFullMask, upto, 1);
+  if (lane == 0) before = -1;
+  before = max(before, __reduce_max_sync(kFullMask, lane < warp ? warp_last[lane] : -1));
   int run = before, n0 = 0, n1 = 0;
   for (int r = r0; r < r1; ++r) {
     if (starts(r)) run = r;
@@ -803,17 +805,18 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
     if (is_few(r)) ++n1;
     else ++n0;
   }
-  sums[0][tid] = n0;
-  sums[1][tid] = n1;
-  __syncthreads();
-  for (int d = 1; d < 1024; d <<= 1) {
-    const int a = tid >= d ? sums[0][tid - d] : 0, b = tid >= d ? sums[1][tid - d] : 0;
-    __syncthreads();
-    sums[0][tid] += a;
-    sums[1][tid] += b;
-    __syncthreads();
+  int2 sum = make_int2(n0, n1);  // up to and with this thread, first in its warp
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(kFullMask, sum.x, d), y = __shfl_up_sync(kFullMask, sum.y, d);
+    if (lane >= d) sum.x += x, sum.y += y;
   }
-  int at0 = sums[0][tid] - n0, at1 = T - (sums[1][tid] - n1) - 1;
+  if (lane == 31) warp_count[warp] = sum;
+  __syncthreads();
+  const int2 w = lane < warp ? warp_count[lane] : make_int2(0, 0);
+  sum.x += __reduce_add_sync(kFullMask, w.x);
+  sum.y += __reduce_add_sync(kFullMask, w.y);
+  int at0 = sum.x - n0, at1 = T - (sum.y - n1) - 1;
   run = before;
   for (int r = r0; r < r1; ++r) {
     if (starts(r)) run = r;
@@ -821,7 +824,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
     if (is_few(r)) list[at1--] = r;
     else list[at0++] = r;
   }
-  if (tid == 1023) *counts = Counts{sums[0][1023], sums[1][1023], 0};
+  if (tid == 1023) *counts = Counts{sum.x, sum.y, 0};
 }
 
 // Tokens of the tile that starts at row `first`: rows of its sequence that follow it, `per` at most.
@@ -1254,7 +1257,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 constexpr int kFewWarps = 4;
 constexpr int kFewStages = 3;
-constexpr int kFewNT = kFewRows / 8;
 
 template <int D>
 struct FewSmem {
@@ -1265,130 +1267,138 @@ struct FewSmem {
   static constexpr int BYTES = OVER + kFewWarps * kFewRows * 8 + kFewRows * D * 4;
 };
 
+// One tile of up to 8 NT query rows.
+template <int KIND, int D, int NT>
+__device__ __forceinline__ void few_tile(const uint16_t* __restrict__ q, int64_t ldq, int Hq, int Hkv, int G, const Cache& C,
+                                         const Rows& R, int first, int rows, int kh, uint16_t* __restrict__ out,
+                                         float scale_log2, uint8_t* smem, int warp, int lane) {
+  using M = FewSmem<D>;
+  const int g = lane >> 2, c = lane & 3;
+  const uint32_t base = smem_u32(smem);
+  const int live = (rows + 7) / 8;
+  Query<D, NT> Q;
+  int len[NT][2], longest = 0, shortest = INT_MAX / 2, pt_row = 0;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int i = 8 * n + g;
+    load_query<D, NT>(Q, n, i < rows ? q + (int64_t)(first + i / G) * ldq + (int64_t)(kh * G + i % G) * D : nullptr,
+                          lane, scale_log2);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int k = 8 * n + 2 * c + r;
+      len[n][r] = INT_MAX / 2;  // no row: nothing to mask
+      if (k < rows) {
+        int row;
+        len[n][r] = attn::row_len(R, first + k / G, row);
+        longest = max(longest, len[n][r]);
+        pt_row = max(pt_row, row);
+      }
+      shortest = min(shortest, len[n][r]);
+    }
+  }
+  longest = __reduce_max_sync(kFullMask, longest);
+  shortest = __reduce_min_sync(kFullMask, shortest);
+  pt_row = __reduce_max_sync(kFullMask, pt_row);  // rows that see anything share it; the others gave 0
+  const int32_t* prow = C.pt + (int64_t)pt_row * R.max_pages;
+  // four splits at a time, one a warp; then row k's thread group folds them in order
+  const uint32_t ring = base + (uint32_t)(warp * kFewStages * kPageBytes<D>);
+  const uint32_t scales = base + (uint32_t)(kFewWarps * kFewStages * kPageBytes<D> + warp * kFewStages * kScaleBytes);
+  float* part = reinterpret_cast<float*>(smem);                                  // [warp][row][D]
+  float2* pml = reinterpret_cast<float2*>(smem + M::OVER);                          // [warp][row]
+  float* tot = reinterpret_cast<float*>(smem + M::OVER + kFewWarps * kFewRows * 8);      // [row][D]
+  for (int i = threadIdx.x; i < rows * D; i += kFewWarps * 32) tot[i] = 0.f;
+  // thread -> (row, quarter of D) for the folds
+  const int frow = threadIdx.x >> 2, fd = (threadIdx.x & 3) * (D / 4);
+  float FM = kLowest, FL = 0.f;
+  for (int r0 = 0; r0 < longest; r0 += kFewWarps * SPLIT) {
+    const int t0 = r0 + warp * SPLIT, seen = min(SPLIT, longest - t0);
+    State<D, NT> S;
+    S.clear();
+    const int np = seen > 0 ? (seen + PAGE - 1) / PAGE : 0;
+    int page = -1;
+    if (lane < np) page = page_id(C, prow, t0 / PAGE + lane, longest);
+    auto issue = [&](int j) {
+      if (j < np) {
+        const int pg = __shfl_sync(kFullMask, page, j);
+        const uint32_t st = (uint32_t)(j % kFewStages);
+        if (pg >= 0)
+          copy_page<D>(ring + st * kPageBytes<D>, scales + st * kScaleBytes, C, ((int64_t)pg * Hkv + kh) * PAGE, lane);
+      }
+      cp_commit();
+    };
+    for (int j = 0; j < kFewStages; ++j) issue(j);
+    for (int j = 0; j < np; ++j) {
+      cp_wait<kFewStages - 1>();
+      __syncwarp();
+      if (__shfl_sync(kFullMask, page, j) >= 0) {
+        const int tp = t0 + j * PAGE;
+        const uint32_t st = (uint32_t)(j % kFewStages), pg = ring + st * kPageBytes<D>;
+        float s[NT][4];
+        page_scores<KIND, D, NT>(Q, pg, lane, s);
+        fold_page<KIND, D, NT>(Q, s, pg, scales + st * kScaleBytes, tp + PAGE > shortest,
+                                   [&](int n, int r) { return len[n][r] - tp; }, longest - tp, live, lane, S);
+      }
+      __syncwarp();
+      issue(j + kFewStages);
+    }
+    cp_wait<0>();
+    __syncthreads();  // the rings are free (and the totals cleared, or the last fold done)
+    if (np > 0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float l = row_sum(r ? S.l[n].y : S.l[n].x);
+          const int k = 8 * n + 2 * c + r;
+          if (k >= rows) continue;
+          float* dst = part + (warp * kFewRows + k) * D + (D / 8) * g;
+#pragma unroll
+          for (int i = 0; i < D / 16; i += 2)
+            *reinterpret_cast<float4*>(dst + 2 * i) =
+                make_float4(S.o[n][i][r], S.o[n][i][2 + r], S.o[n][i + 1][r], S.o[n][i + 1][2 + r]);
+          if (g == 0) pml[warp * kFewRows + k] = make_float2(r ? S.m[n].y : S.m[n].x, l);
+        }
+    }
+    __syncthreads();
+    if (frow < rows)
+      for (int w = 0; w < kFewWarps && r0 + w * SPLIT < longest; ++w) {
+        const float2 ml = pml[w * kFewRows + frow];
+        float fa, fb;
+        join(FM, ml.x, fa, fb);
+        FL = __fmaf_rn(ml.y, fb, __fmul_rn(FL, fa));
+        for (int d = fd; d < fd + D / 4; ++d)
+          tot[frow * D + d] = __fmaf_rn(part[(w * kFewRows + frow) * D + d], fb, __fmul_rn(tot[frow * D + d], fa));
+      }
+    __syncthreads();  // the partial results are read: the rings may be refilled
+  }
+  __syncthreads();
+  if (frow < rows) {
+    uint16_t* dst = out + ((int64_t)(first + frow / G) * Hq + kh * G + frow % G) * D + fd;
+    for (int d = 0; d < D / 4; d += D / 8) {
+      float x[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) x[i] = tot[frow * D + fd + d + i];
+      store_row<D>(dst + d, x, FL);
+    }
+  }
+}
+
 template <int KIND, int D>
 __global__ void __launch_bounds__(kFewWarps * 32, 3)
     few_kernel(const uint16_t* __restrict__ q, int64_t ldq, int Hq, int Hkv, Cache C, Rows R, int T, int few,
                const int32_t* __restrict__ list, const Counts* __restrict__ counts, uint16_t* __restrict__ out,
                float scale_log2) {
-  using M = FewSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem_few[];  // pages' swizzle counts from 128-byte boundaries
-  uint8_t* smem = smem_few;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, c = lane & 3;
   const int G = Hq / Hkv;
-  const uint32_t base = smem_u32(smem);
   pdl_wait();  // the plan (and the caller's q and store) are complete from here on
   pdl_trigger();
   const int total = counts->few * Hkv;
   for (int item = blockIdx.x; item < total; item += gridDim.x) {
     const int first = list[T - 1 - item / Hkv], kh = item % Hkv;
-    const int n_tok = tile_tokens(R.q_seq, first, T, few, lane);
-    const int rows = n_tok * G, live = (rows + 7) / 8;
-    Query<D, kFewNT> Q;
-    int len[kFewNT][2], longest = 0, shortest = INT_MAX / 2, pt_row = 0;
-#pragma unroll
-    for (int n = 0; n < kFewNT; ++n) {
-      const int i = 8 * n + g;
-      load_query<D, kFewNT>(Q, n, i < rows ? q + (int64_t)(first + i / G) * ldq + (int64_t)(kh * G + i % G) * D : nullptr,
-                            lane, scale_log2);
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int k = 8 * n + 2 * c + r;
-        len[n][r] = INT_MAX / 2;  // no row: nothing to mask
-        if (k < rows) {
-          int row;
-          len[n][r] = attn::row_len(R, first + k / G, row);
-          longest = max(longest, len[n][r]);
-          pt_row = max(pt_row, row);
-        }
-        shortest = min(shortest, len[n][r]);
-      }
-    }
-    longest = __reduce_max_sync(kFullMask, longest);
-    shortest = __reduce_min_sync(kFullMask, shortest);
-    pt_row = __reduce_max_sync(kFullMask, pt_row);  // rows that see anything share it; the others gave 0
-    const int32_t* prow = C.pt + (int64_t)pt_row * R.max_pages;
-    // four splits at a time, one a warp; then row k's thread group folds them in order
-    const uint32_t ring = base + (uint32_t)(warp * kFewStages * kPageBytes<D>);
-    const uint32_t scales = base + (uint32_t)(kFewWarps * kFewStages * kPageBytes<D> + warp * kFewStages * kScaleBytes);
-    float* part = reinterpret_cast<float*>(smem);                                  // [warp][row][D]
-    float2* pml = reinterpret_cast<float2*>(smem + M::OVER);                          // [warp][row]
-    float* tot = reinterpret_cast<float*>(smem + M::OVER + kFewWarps * kFewRows * 8);      // [row][D]
-    for (int i = threadIdx.x; i < rows * D; i += kFewWarps * 32) tot[i] = 0.f;
-    // thread -> (row, quarter of D) for the folds
-    const int frow = threadIdx.x >> 2, fd = (threadIdx.x & 3) * (D / 4);
-    float FM = kLowest, FL = 0.f;
-    for (int r0 = 0; r0 < longest; r0 += kFewWarps * SPLIT) {
-      const int t0 = r0 + warp * SPLIT, seen = min(SPLIT, longest - t0);
-      State<D, kFewNT> S;
-      S.clear();
-      const int np = seen > 0 ? (seen + PAGE - 1) / PAGE : 0;
-      int page = -1;
-      if (lane < np) page = page_id(C, prow, t0 / PAGE + lane, longest);
-      auto issue = [&](int j) {
-        if (j < np) {
-          const int pg = __shfl_sync(kFullMask, page, j);
-          const uint32_t st = (uint32_t)(j % kFewStages);
-          if (pg >= 0)
-            copy_page<D>(ring + st * kPageBytes<D>, scales + st * kScaleBytes, C, ((int64_t)pg * Hkv + kh) * PAGE, lane);
-        }
-        cp_commit();
-      };
-      for (int j = 0; j < kFewStages; ++j) issue(j);
-      for (int j = 0; j < np; ++j) {
-        cp_wait<kFewStages - 1>();
-        __syncwarp();
-        if (__shfl_sync(kFullMask, page, j) >= 0) {
-          const int tp = t0 + j * PAGE;
-          const uint32_t st = (uint32_t)(j % kFewStages), pg = ring + st * kPageBytes<D>;
-          float s[kFewNT][4];
-          page_scores<KIND, D, kFewNT>(Q, pg, lane, s);
-          fold_page<KIND, D, kFewNT>(Q, s, pg, scales + st * kScaleBytes, tp + PAGE > shortest,
-                                     [&](int n, int r) { return len[n][r] - tp; }, longest - tp, live, lane, S);
-        }
-        __syncwarp();
-        issue(j + kFewStages);
-      }
-      cp_wait<0>();
-      __syncthreads();  // the rings are free (and the totals cleared, or the last fold done)
-      if (np > 0) {
-#pragma unroll
-        for (int n = 0; n < kFewNT; ++n)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float l = row_sum(r ? S.l[n].y : S.l[n].x);
-            const int k = 8 * n + 2 * c + r;
-            if (k >= rows) continue;
-            float* dst = part + (warp * kFewRows + k) * D + (D / 8) * g;
-#pragma unroll
-            for (int i = 0; i < D / 16; i += 2)
-              *reinterpret_cast<float4*>(dst + 2 * i) =
-                  make_float4(S.o[n][i][r], S.o[n][i][2 + r], S.o[n][i + 1][r], S.o[n][i + 1][2 + r]);
-            if (g == 0) pml[warp * kFewRows + k] = make_float2(r ? S.m[n].y : S.m[n].x, l);
-          }
-      }
-      __syncthreads();
-      if (frow < rows)
-        for (int w = 0; w < kFewWarps && r0 + w * SPLIT < longest; ++w) {
-          const float2 ml = pml[w * kFewRows + frow];
-          float fa, fb;
-          join(FM, ml.x, fa, fb);
-          FL = __fmaf_rn(ml.y, fb, __fmul_rn(FL, fa));
-          for (int d = fd; d < fd + D / 4; ++d)
-            tot[frow * D + d] = __fmaf_rn(part[(w * kFewRows + frow) * D + d], fb, __fmul_rn(tot[frow * D + d], fa));
-        }
-      __syncthreads();  // the partial results are read: the rings may be refilled
-    }
-    __syncthreads();
-    if (frow < rows) {
-      uint16_t* dst = out + ((int64_t)(first + frow / G) * Hq + kh * G + frow % G) * D + fd;
-      for (int d = 0; d < D / 4; d += D / 8) {
-        float x[D / 8];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = tot[frow * D + fd + d + i];
-        store_row<D>(dst + d, x, FL);
-      }
-    }
+    const int rows = tile_tokens(R.q_seq, first, T, few, lane) * G;
+    if (rows <= 8) few_tile<KIND, D, 1>(q, ldq, Hq, Hkv, G, C, R, first, rows, kh, out, scale_log2, smem_few, warp, lane);
+    else few_tile<KIND, D, 2>(q, ldq, Hq, Hkv, G, C, R, first, rows, kh, out, scale_log2, smem_few, warp, lane);
     __syncthreads();  // shared memory is free for the next tile
   }
 }
