@@ -925,8 +925,8 @@ struct TileSmem {
   static constexpr int STATS = TOTALS + kTileRows * D * 4;   // M and L, lane by lane
   static constexpr int LENS = STATS + kFoldWarps * 32 * kNT * 16;  // visible lengths, lane by lane
   static constexpr int BARS = LENS + kFoldWarps * 32 * kNT * 8;
-  static constexpr int ARGS = BARS + kRing * 16;                   // the item, and what its tile is
-  static constexpr int BYTES = ARGS + 16 + 256;
+  static constexpr int ARGS = BARS + kRing * 16;                   // two TileArgs
+  static constexpr int BYTES = ARGS + 512;
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -1212,41 +1212,44 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   pdl_trigger();
   uint32_t it = 0;
   bool dead = false;
-  volatile int* item_at = reinterpret_cast<int*>(smem + M::ARGS);
-  TileArgs& A = *reinterpret_cast<TileArgs*>(smem + M::ARGS + 16);
-  // Takes the next tile (by the last warp, for all), or says that there is none. Later rows of a
-  // prompt see more keys: longest first.
-  auto next_tile = [&] {
-    tile_sync();  // every warp is done with the last tile's arguments (and the barriers are set up)
-    if (warp == kFoldWarps + kWidenWarps - 1) {
-      int item = 0;
-      if (lane == 0) item = counts->tiles * Hkv - 1 - atomicAdd(&counts->next, 1);  // all that this decides is who
-      item = __shfl_sync(kFullMask, item, 0);
-      if (item >= 0) {
-        const int first = list[item / Hkv], n = tile_tokens(R.q_seq, first, T, per, lane);
-        int len = 0, pt_row = 0;
-        for (int i = lane; i < n; i += 32) {
-          int row;
-          const int x = attn::row_len(R, first + i, row);
-          if (x > len) len = x, pt_row = row;
-        }
-        len = __reduce_max_sync(kFullMask, len);
-        pt_row = __reduce_max_sync(kFullMask, pt_row);  // rows that see anything share it; the others gave 0
-        if (lane == 0)
-          A = TileArgs{q, ldq, out, C, R, C.pt + (int64_t)pt_row * R.max_pages, Hq, Hkv, Hq / Hkv, first, n * (Hq / Hkv),
-                       item % Hkv, len, scale_log2};
-      }
-      if (lane == 0) *item_at = item;
+  // What the tile in hand is, and the next one: the last warp looks the next one up once it has
+  // widened this one's last stage, while the others still fold. rows < 0: there is none. Later rows
+  // of a prompt see more keys: longest first.
+  TileArgs* args = reinterpret_cast<TileArgs*>(smem + M::ARGS);
+  auto look_up = [&](TileArgs& A) {
+    int item = 0;
+    if (lane == 0) item = counts->tiles * Hkv - 1 - atomicAdd(&counts->next, 1);  // all that this decides is who
+    item = __shfl_sync(kFullMask, item, 0);
+    if (item < 0) {
+      if (lane == 0) A.rows = -1;
+      return;
     }
-    tile_sync();
-    return *item_at >= 0;
+    const int first = list[item / Hkv], n = tile_tokens(R.q_seq, first, T, per, lane);
+    int len = 0, pt_row = 0;
+    for (int i = lane; i < n; i += 32) {
+      int row;
+      const int x = attn::row_len(R, first + i, row);
+      if (x > len) len = x, pt_row = row;
+    }
+    len = __reduce_max_sync(kFullMask, len);
+    pt_row = __reduce_max_sync(kFullMask, pt_row);  // rows that see anything share it; the others gave 0
+    if (lane == 0)
+      A = TileArgs{q, ldq, out, C, R, C.pt + (int64_t)pt_row * R.max_pages, Hq, Hkv, Hq / Hkv, first, n * (Hq / Hkv),
+                   item % Hkv, len, scale_log2};
   };
+  int b = 0;
   if (warp >= kFoldWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWidenRegs));
-    while (next_tile()) widen_tile<KIND, D>(A, base, bars, it, dead, warp - kFoldWarps, lane);
+    const bool looks = warp == kFoldWarps + kWidenWarps - 1;
+    if (looks) look_up(args[0]);
+    for (tile_sync(); args[b].rows >= 0; b ^= 1, tile_sync()) {
+      widen_tile<KIND, D>(args[b], base, bars, it, dead, warp - kFoldWarps, lane);
+      if (looks) look_up(args[b ^ 1]);
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFoldRegs));
-    while (next_tile()) {
+    for (tile_sync(); args[b].rows >= 0; b ^= 1, tile_sync()) {
+      const TileArgs& A = args[b];
       const int tiles = (A.rows + 7) / 8;  // of 8 query rows
       if (tiles > 2 * kFoldWarps + warp) fold_tile<KIND, D, 3>(A, smem, base, bars, it, dead, warp, lane);
       else if (tiles > kFoldWarps + warp) fold_tile<KIND, D, 2>(A, smem, base, bars, it, dead, warp, lane);
