@@ -53,7 +53,7 @@ struct Cache {
   const int32_t* pt;
 };
 
-// 2^x with results below 2^-126 flushed to 0 (they are under 2^-112 of the largest weight's 2^14).
+// 2^x with results below 2^-126 flushed to 0 (of 2^7 w: under 2^-133, where a row's largest w is at least 1).
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -64,19 +64,11 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Value scales are at least 2^-109, so neither they nor their reciprocals are flushed.
+// Value scales lie in 2^-109 .. 2^121, so neither they nor their reciprocals are flushed.
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
 }
 
 // d += A B with A 16 x 16 (keys or values), B 16 x 8 (columns = query rows), f16 operands.
@@ -198,7 +190,7 @@ __device__ __forceinline__ void load_query(Query<D, NT>& Q, int n, const uint16_
   }
 }
 
-// Running state of a split: per query row the reference m, 2^7 sum w / sv over the lane's
+// Running state of a split: per query row the reference m, 2^-9 sum w / sv over the lane's
 // tokens, and 2^7 sum w v over the lane's output dims (o[n][i]: dims 2i | 2i + 1 of rows 2c, 2c+1).
 template <int D, int NT>
 struct State {
@@ -219,14 +211,13 @@ struct State {
 
 // What the fold needs of the lane's tokens g and g + 8.
 struct Tokens {
-  float ks[2], lg[2], ri[2];  // key scale; log2 and reciprocal of the value scale
+  float ks[2], lg[2], ri[2];  // key scale; log2 of the value scale, and 2^-16 over it
 };
-
 
 // Weights of one page from its scores s (which become z): moves m (and l and o with it) where it
 // must, adds to l, and gives 2^7 w as the operand of the value product. masked (the same for the
 // whole warp): the lane's query row (n, r) sees the first nv(n, r) tokens only; otherwise all 16
-// are seen. live: tiles that hold query rows.
+// are seen.
 // A row whose largest f16 weight exceeds 2^15 moves its reference to its largest score of the
 // page; weights are taken with the reference in hand first, which most pages keep.
 // There is one line of code through the accumulators, with small blocks beside it for what is
@@ -234,7 +225,7 @@ struct Tokens {
 // accumulators by register moves, which cost a third of the time of pages that never ran it.
 template <int D, int NT, typename Nv>
 __device__ __forceinline__ void page_weights(const Query<D, NT>& Q, float (&s)[NT][4], const Tokens& T, bool masked, Nv nv,
-                                             int g, int live, State<D, NT>& S, uint32_t (&w)[NT][2]) {
+                                             int g, State<D, NT>& S, uint32_t (&w)[NT][2]) {
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -268,8 +259,7 @@ __device__ __forceinline__ void page_weights(const Query<D, NT>& Q, float (&s)[N
       l[n] = __ffma2_rn(p, make_float2(T.ri[t], T.ri[t]), l[n]);
     }
     const __half2 top = __hmax2(*reinterpret_cast<__half2*>(&w[n][0]), *reinterpret_cast<__half2*>(&w[n][1]));
-    const bool up = !__hble2(top, __halves2half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800)));  // 2^15
-    over |= up && (NT == 1 || n < live);
+    over |= !__hble2(top, __halves2half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800)));  // 2^15
   }
   if (__any_sync(kFullMask, over)) {
 #pragma unroll
@@ -323,6 +313,13 @@ __device__ __forceinline__ void page_weights(const Query<D, NT>& Q, float (&s)[N
     w[n][1] = transpose8x8(w[n][1]);
   }
 }
+
+// 2^-16 / sv: what a token adds to l per 2^7 w. Unscaled, l would pass the fp32 range for long rows whose
+// values are all near 2^-100; scaled, 2^15 w / sv sums up to 2^19 such tokens, and the reciprocals of
+// scales above 2^110 keep 12 bits or more (fp32 subnormals).
+__device__ __forceinline__ float weight_per_scale(float vs) { return __fmul_rn(rcp(vs), 0x1p-16f); }
+// The output of a row from its sums of w v and of weight_per_scale w.
+__device__ __forceinline__ float row_out(float o, float l) { return l == 0.f ? 0.f : __fdiv_rn(__fmul_rn(o, 0x1p-16f), l); }
 
 // The xor tree over a query row's 8 lanes that ends a split.
 __device__ __forceinline__ float row_sum(float l) {
@@ -380,7 +377,7 @@ __device__ __forceinline__ void page_scores(const Query<D, NT>& Q, uint32_t page
 // Folds a page whose scores are s. masked: `seen` of its tokens exist, query row (n, r) sees nv(n, r).
 template <int KIND, int D, int NT, typename Nv>
 __device__ __forceinline__ void fold_page(const Query<D, NT>& Q, float (&s)[NT][4], uint32_t page, uint32_t scales,
-                                          bool masked, Nv nv, int seen, int live, int lane, State<D, NT>& S) {
+                                          bool masked, Nv nv, int seen, int lane, State<D, NT>& S) {
   const int g = lane >> 2, c = lane & 3;
   Tokens T;
 #pragma unroll
@@ -388,10 +385,10 @@ __device__ __forceinline__ void fold_page(const Query<D, NT>& Q, float (&s)[NT][
     const float vs = ld_shared_f32(scales + 64 + 4 * g + 32 * t);
     T.ks[t] = ld_shared_f32(scales + 4 * g + 32 * t);
     T.lg[t] = lg2(vs);
-    T.ri[t] = rcp(vs);
+    T.ri[t] = weight_per_scale(vs);
   }
   uint32_t w[NT][2];
-  page_weights<D, NT>(Q, s, T, masked, nv, g, live, S, w);
+  page_weights<D, NT>(Q, s, T, masked, nv, g, S, w);
   uint32_t x[4][D / 32];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -620,7 +617,7 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT == 256 ? 3 : 4)
         const uint32_t st = (used + u) % kStages;
         if (NT > 1 && u == 1) page_scores<KIND, D, NT>(Q, ring + st * kPageBytes<D>, lane, s[u]);  // (no registers for both)
         fold_page<KIND, D, NT>(Q, s[u], ring + st * kPageBytes<D>, scales + st * kScaleBytes, masked,
-                               [&](int, int) { return seen[u]; }, seen[u], NT, lane, S);
+                               [&](int, int) { return seen[u]; }, seen[u], lane, S);
       }
       __syncwarp();  // every lane has read these pages: their stages may be refilled
       used += second ? 2 : 1;
@@ -739,7 +736,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
   }
   float y[DPL];
 #pragma unroll
-  for (int d = 0; d < DPL; ++d) y[d] = L == 0.f ? 0.f : __fdiv_rn(O[d], L);
+  for (int d = 0; d < DPL; ++d) y[d] = row_out(O[d], L);
   uint16_t* dst = out + rh * D + d0;
   if constexpr (DPL == 1) {
     *dst = to_bf16_bits(y[0]);
@@ -900,7 +897,7 @@ __device__ __forceinline__ void store_row(uint16_t* dst, const float (&x)[D / 8]
   for (int i = 0; i < D / 8; i += 8) {
     float y[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) y[u] = L == 0.f ? 0.f : __fdiv_rn(x[i + u], L);
+    for (int u = 0; u < 8; ++u) y[u] = row_out(x[i + u], L);
     *reinterpret_cast<uint4*>(dst + i) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
                                                     pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
   }
@@ -920,7 +917,7 @@ template <int D>
 struct TileSmem {
   static constexpr int PAGES = 256 / D;                      // pages a stage: one part of each kind per widening warp
   static constexpr int OPERANDS = PAGES * 2 * PAGE * D * 2;  // f16 keys, then values
-  static constexpr int STAGE = OPERANDS + PAGES * PAGE * 16;  // and {ks, log2 vs, 1 / vs, -} per token
+  static constexpr int STAGE = OPERANDS + PAGES * PAGE * 16;  // and {ks, log2 vs, 2^-16 / vs, -} per token
   static constexpr int TOTALS = kRing * STAGE;               // fp32 totals [row][D], lane by lane
   static constexpr int STATS = TOTALS + kTileRows * D * 4;   // M and L, lane by lane
   static constexpr int LENS = STATS + kFoldWarps * 32 * kNT * 16;  // visible lengths, lane by lane
@@ -995,7 +992,7 @@ __device__ __forceinline__ void widen_raw(const Raw& X, uint32_t stage, int warp
     st_shared_v4(vb + (2 * u + 1) * 512, b);
   }
   if (warp * 32 < M::PAGES * PAGE) {
-    const float4 t = make_float4(X.ks, lg2(X.vs), X.vs == 0.f ? 0.f : rcp(X.vs), 0.f);
+    const float4 t = make_float4(X.ks, lg2(X.vs), X.vs == 0.f ? 0.f : weight_per_scale(X.vs), 0.f);
     st_shared_v4(stage + M::OPERANDS + (warp * 32 + lane) * 16, *reinterpret_cast<const uint4*>(&t));
   }
 }
@@ -1061,7 +1058,7 @@ __device__ __forceinline__ void fold_wide(const Query<D, LIVE>& Q, uint32_t stag
     if (u == (AHEAD ? 0 : 1)) wide_scores<D, LIVE>(Q, stage, page + 1, lane, s[1]);
     const Tokens T = wide_tokens<D>(stage, page + u, lane);
     uint32_t w[LIVE][2];
-    page_weights<D, LIVE>(Q, s[u], T, masked, [&](int n, int r) { return nv(n, r) - u * PAGE; }, lane >> 2, LIVE, S, w);
+    page_weights<D, LIVE>(Q, s[u], T, masked, [&](int n, int r) { return nv(n, r) - u * PAGE; }, lane >> 2, S, w);
     wide_values<D, LIVE>(stage, page + u, lane, w, S);
   }
 }
@@ -1278,7 +1275,6 @@ __device__ __forceinline__ void few_tile(const uint16_t* __restrict__ q, int64_t
   using M = FewSmem<D>;
   const int g = lane >> 2, c = lane & 3;
   const uint32_t base = smem_u32(smem);
-  const int live = (rows + 7) / 8;
   Query<D, NT> Q;
   int len[NT][2], longest = 0, shortest = INT_MAX / 2, pt_row = 0;
 #pragma unroll
@@ -1339,7 +1335,7 @@ __device__ __forceinline__ void few_tile(const uint16_t* __restrict__ q, int64_t
         float s[NT][4];
         page_scores<KIND, D, NT>(Q, pg, lane, s);
         fold_page<KIND, D, NT>(Q, s, pg, scales + st * kScaleBytes, tp + PAGE > shortest,
-                                   [&](int n, int r) { return len[n][r] - tp; }, longest - tp, live, lane, S);
+                               [&](int n, int r) { return len[n][r] - tp; }, longest - tp, lane, S);
       }
       __syncwarp();
       issue(j + kFewStages);

@@ -192,7 +192,7 @@ bi_status attention_common(const uint16_t* q, int64_t ldq, const uint16_t* kc, c
 bi_status store_check(const void* kc, const void* vc, const float* ks, const float* vs, int kind, int64_t num_pages,
                       int max_pages, int Hkv, int D) {
   if (num_pages <= 0 || max_pages <= 0 || Hkv <= 0 || D <= 0) return BI_ERR_SHAPE;
-  if (max_pages > INT_MAX / BI_PAGE_TOKENS) return BI_ERR_SHAPE;
+  if (max_pages > INT_MAX / BI_PAGE_TOKENS / 2) return BI_ERR_SHAPE;  // positions, and a walk's next ones, in 31 bits
   // store rows are counted in 31 bits (a TMA coordinate)
   if (num_pages > INT_MAX / BI_PAGE_TOKENS / (int64_t)Hkv) return BI_ERR_SHAPE;
   if ((kind != BI_KV_INT8 && kind != BI_KV_E4M3) || (D != 64 && D != 128)) return BI_ERR_UNSUPPORTED;
@@ -201,14 +201,12 @@ bi_status store_check(const void* kc, const void* vc, const float* ks, const flo
 }
 
 bi_status attention_q8_check(const uint16_t* q, int64_t ldq, int nrows, const uint16_t* out, int Hq, int Hkv, int D,
-                             int max_pages, float scale) {
+                             float scale) {
   if (Hq <= 0 || Hq % Hkv != 0) return BI_ERR_SHAPE;
   if (Hq / Hkv > 16) return BI_ERR_UNSUPPORTED;
   if (!std::isfinite(scale) || ldq < (int64_t)Hq * D) return BI_ERR_SHAPE;
   if (ldq % 8 || !aligned16(q) || !aligned16(out)) return BI_ERR_ALIGN;
-  // index arithmetic of the work lists is 32-bit
-  if ((int64_t)nrows * max_splits(max_pages) * Hkv >= INT_MAX / 2 || (int64_t)nrows * Hq >= INT_MAX / 16)
-    return BI_ERR_SHAPE;
+  if ((int64_t)nrows * Hq >= INT_MAX / 16) return BI_ERR_SHAPE;  // work items are counted in 31 bits
   if (ranges_overlap(q, span_bytes(nrows, (int64_t)Hq * D, ldq, 2), out, span_bytes(nrows, (int64_t)Hq * D, (int64_t)Hq * D, 2)))
     return BI_ERR_SHAPE;
   return BI_OK;
@@ -660,7 +658,8 @@ bi_status bi_attention_decode_q8(const bi_bf16* q, const void* k_cache, const vo
   if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !page_table || !seq_lens || !out) return BI_ERR_NULL;
   if (B < 0) return BI_ERR_SHAPE;
   if (bi_status e = store_check(k_cache, v_cache, k_scale, v_scale, kind, num_pages, max_pages_per_seq, Hkv, D)) return e;
-  if (bi_status e = attention_q8_check(q, (int64_t)Hq * D, B, out, Hq, Hkv, D, max_pages_per_seq, scale)) return e;
+  if (bi_status e = attention_q8_check(q, (int64_t)Hq * D, B, out, Hq, Hkv, D, scale)) return e;
+  if ((int64_t)B * max_splits(max_pages_per_seq) * Hkv >= INT_MAX / 2) return BI_ERR_SHAPE;  // so are splits
   if (B == 0) return BI_OK;
   if (!workspace) return BI_ERR_WORKSPACE;
   if (!aligned16(workspace)) return BI_ERR_ALIGN;
@@ -691,7 +690,7 @@ bi_status bi_attention_prefill_q8(const bi_bf16* q, int64_t ldq, const int32_t* 
   if (!q || !q_seq || !q_pos || !k_cache || !v_cache || !k_scale || !v_scale || !page_table || !out) return BI_ERR_NULL;
   if (T < 0 || num_seqs <= 0) return BI_ERR_SHAPE;
   if (bi_status e = store_check(k_cache, v_cache, k_scale, v_scale, kind, num_pages, max_pages_per_seq, Hkv, D)) return e;
-  if (bi_status e = attention_q8_check(q, ldq, T, out, Hq, Hkv, D, max_pages_per_seq, scale)) return e;
+  if (bi_status e = attention_q8_check(q, ldq, T, out, Hq, Hkv, D, scale)) return e;
   if (T == 0) return BI_OK;
   if (!workspace || workspace_bytes < bi_attention_prefill_q8_workspace_size(T)) return BI_ERR_WORKSPACE;
   if (!aligned16(workspace)) return BI_ERR_ALIGN;

@@ -477,3 +477,60 @@ def test_streams_and_captured_graphs():
             streams[0].synchronize()
             assert same_bits(s.od, od) and same_bits(s.op, op) and torch.equal(raw(s.S.k), k)
     assert bi.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [2.0 ** -97, 2.0 ** 120])
+def test_value_rows_at_both_ends_of_the_range(kind, size):
+    """Sums over 8192 tokens whose value rows are all near the least or the largest stored size. The
+    first page of every 256 tokens scores 0 and all others 7.89 (base 2): just under the step that
+    moves the softmax's reference, so the sums are as large as they get. |z| < 128 here: the fp32
+    scores move a weight by less than 128 * 8 * 2^-24 = 2^-14, and the reciprocal of a value scale
+    keeps 12 bits (2^-13); together, for numerator and denominator, under the 2^-11 of the tolerance."""
+    n, Hq, D = 8192, 4, 64
+    k = torch.zeros(n, 1, D)
+    k[torch.arange(n) % 256 >= 16, :, 0] = 1
+    v = (synth.normal_bf16((n, 1, D), 70).float().abs().clamp(0.25, 2.0) * size).bfloat16()
+    S, pt = fill(kind, [n], 1, D, n // 16, seed=71, k=k.bfloat16(), v=v)
+    q = torch.zeros(1, Hq, D, dtype=torch.bfloat16)
+    q[..., 0] = 5.46875
+    ref, mag = reference(S, pt, q[0], 0, n, scale=1.0)
+    out = bi.attention_decode_q8(q.to(dev()), *S.args, torch.tensor([n], dtype=torch.int32, device=dev()), scale=1.0)
+    q8_ref.assert_attention_close(out[0].double() / size, ref / size, mag / size)
+    T = 40                                            # rows enough for a wide tile and its last rows
+    pre = bi.attention_prefill_q8(q.repeat(T, 1, 1).to(dev()), torch.zeros(T, dtype=torch.int32, device=dev()),
+                                  torch.full((T,), n - 1, dtype=torch.int32, device=dev()), *S.args, scale=1.0)
+    assert bi.get_device_error() == 0 and same_bits(pre, out.expand_as(pre).contiguous())
+
+
+def test_a_captured_chunk_replays_with_the_eager_bits():
+    """A prompt chunk, its last rows and a decode row of another sequence in one captured prefill
+    call: the work list and its ticket are rebuilt by every replay, on one stream after the other."""
+    Hq, Hkv, D, n = 8, 8, 128, 700
+    S, _ = fill("e4m3", [n, 90], Hkv, D, 50, seed=310)
+    rows = list(range(n - 401, n)) + [89]
+    seq = torch.tensor([0] * 401 + [1], dtype=torch.int32, device=dev())
+    pos = torch.tensor(rows, dtype=torch.int32, device=dev())
+    q = synth.normal_bf16((402, Hq, D), 311).to(dev())
+    ws = torch.empty(bi.attention_prefill_q8_workspace_size(402), dtype=torch.uint8, device=dev())
+    out = torch.empty_like(q)
+    bi.attention_prefill_q8(q, seq, pos, *S.args, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        bi.attention_prefill_q8(q, seq, pos, *S.args, out=out, workspace=ws)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for rnd in range(4):
+        q.copy_(synth.normal_bf16((402, Hq, D), 320 + rnd).to(dev()))
+        pos[:401] -= 60 * rnd                         # other lengths, and in the end rows that see nothing
+        torch.cuda.synchronize()
+        want = bi.attention_prefill_q8(q, seq, pos.clamp(min=-1), *S.args)
+        out.fill_(float("nan"))
+        pos.clamp_(min=-1)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(streams[rnd % 2]):
+            g.replay()
+            g.replay()
+        torch.cuda.synchronize()
+        assert same_bits(out, want)
+    assert int((pos == -1).sum()) > 0 and bi.get_device_error() == 0

@@ -179,3 +179,14 @@ def test_binding_refuses_before_any_call(fake):
             f()
             pytest.fail(f"case {i} was accepted")
     assert not [c for c in fake.calls if not c.endswith("workspace_size")]
+
+
+def test_long_prefill_batches_of_long_contexts_are_not_refused(L):
+    """A prefill keeps no splits in its workspace: rows times splits may pass 31 bits (a decode's may not)."""
+    f, T = L.bi_attention_prefill_q8, 1 << 18
+    a = dict(q=Q, ldq=4096, seq=P, pos=P, kc=P, vc=P, ks=P, vs=P, kind=0, pages=100, pt=P, seqs=2, maxp=1 << 14,
+             out=1 << 44, T=T, Hq=32, Hkv=8, D=128, scale=0.088, ws=P, wsb=16, st=None)
+    assert call(f, a) == WS
+    d = dict(decode_args(L), B=T, maxp=1 << 14, out=1 << 44, wsb=16)
+    assert call(L.bi_attention_decode_q8, d) == SHAPE
+    assert call(f, a, maxp=1 << 27) == SHAPE            # positions past 31 bits
