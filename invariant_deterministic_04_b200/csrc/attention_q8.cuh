@@ -27,6 +27,7 @@
 //     tokens of each page in order, and the 8 lanes are added by an xor tree at the split's end;
 //   * whether m moves at a page depends on the row's own scores;
 //   * splits are folded in ascending order: M' = max(M, m_s), X = X 2^(M-M') + x_s 2^(m_s-M').
+// m and M are held as 7 - m, which is added to z for 2^7 w.
 // An MMA's output column depends on its own column of query rows only, so it does not matter
 // which rows share a tile. Tokens a row does not see get w = 0 exactly and stale value bytes are
 // replaced by zeros; rows that see nothing give zeros.
@@ -148,7 +149,7 @@ __device__ __forceinline__ void value_operands(const uint32_t (&x)[4], uint4& a,
   widen<KIND>(__byte_perm(x[2], x[3], 0x7362), b.z, b.w);
 }
 
-constexpr float kLowest = -0x1p127f;  // the reference of a row that has seen nothing: below its scores
+constexpr float kUnseen = 0x1p127f;  // 7 - m of a row that has seen nothing: m is below its scores
 
 // NT tiles of 8 query rows.
 template <int D, int NT>
@@ -190,7 +191,7 @@ __device__ __forceinline__ void load_query(Query<D, NT>& Q, int n, const uint16_
   }
 }
 
-// Running state of a split: per query row the reference m, 2^-9 sum w / sv over the lane's
+// Running state of a split: per query row 7 - m (m the reference), 2^-9 sum w / sv over the lane's
 // tokens, and 2^7 sum w v over the lane's output dims (o[n][i]: dims 2i | 2i + 1 of rows 2c, 2c+1).
 template <int D, int NT>
 struct State {
@@ -199,7 +200,7 @@ struct State {
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      m[n] = make_float2(kLowest, kLowest);
+      m[n] = make_float2(kUnseen, kUnseen);
       l[n] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -243,12 +244,11 @@ __device__ __forceinline__ void page_weights(const Query<D, NT>& Q, float (&s)[N
         if (g + 8 * (e >> 1) >= nv(n, e & 1)) s[n][e] = -INFINITY;
   }
   auto weight = [&](int n, int t) {  // pairs of query rows 2c, 2c + 1
-    const float2 x = __fadd2_rn(make_float2(s[n][2 * t], s[n][2 * t + 1]),
-                                make_float2(__fsub_rn(7.f, S.m[n].x), __fsub_rn(7.f, S.m[n].y)));
+    const float2 x = __fadd2_rn(make_float2(s[n][2 * t], s[n][2 * t + 1]), S.m[n]);
     return make_float2(ex2(x.x), ex2(x.y));
   };
   float2 l[NT];
-  bool over = false;
+  __half2 top;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     l[n] = S.l[n];
@@ -258,14 +258,15 @@ __device__ __forceinline__ void page_weights(const Query<D, NT>& Q, float (&s)[N
       w[n][t] = pack_f16x2(p.x, p.y);
       l[n] = __ffma2_rn(p, make_float2(T.ri[t], T.ri[t]), l[n]);
     }
-    const __half2 top = __hmax2(*reinterpret_cast<__half2*>(&w[n][0]), *reinterpret_cast<__half2*>(&w[n][1]));
-    over |= !__hble2(top, __halves2half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800)));  // 2^15
+    const __half2 most = __hmax2(*reinterpret_cast<__half2*>(&w[n][0]), *reinterpret_cast<__half2*>(&w[n][1]));
+    top = n ? __hmax2(top, most) : most;  // (a NaN is passed over: it moves no reference)
   }
-  if (__any_sync(kFullMask, over)) {
+  const __half2 limit = __halves2half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800));  // 2^15
+  if (__any_sync(kFullMask, !__hble2(top, limit))) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const __half2 top = __hmax2(*reinterpret_cast<__half2*>(&w[n][0]), *reinterpret_cast<__half2*>(&w[n][1]));
-      float pm[2] = {__low2float(top), __high2float(top)};
+      const __half2 most = __hmax2(*reinterpret_cast<__half2*>(&w[n][0]), *reinterpret_cast<__half2*>(&w[n][1]));
+      float pm[2] = {__low2float(most), __high2float(most)};
       float mx[2] = {fmaxf(s[n][0], s[n][2]), fmaxf(s[n][1], s[n][3])};
       float al[2];
 #pragma unroll
@@ -277,8 +278,9 @@ __device__ __forceinline__ void page_weights(const Query<D, NT>& Q, float (&s)[N
         }
         float& m = r ? S.m[n].y : S.m[n].x;
         const bool up = pm[r] > 32768.f;
-        al[r] = up ? ex2(__fsub_rn(m, mx[r])) : 1.f;  // x * 1 == x: the other rows keep their bits
-        if (up) m = mx[r];
+        const float to = __fsub_rn(7.f, mx[r]);
+        al[r] = up ? ex2(__fsub_rn(to, m)) : 1.f;  // x * 1 == x: the other rows keep their bits
+        if (up) m = to;
       }
       S.l[n] = __fmul2_rn(S.l[n], make_float2(al[0], al[1]));
       l[n] = S.l[n];
@@ -328,11 +330,11 @@ __device__ __forceinline__ float row_sum(float l) {
   return l;
 }
 
-// One step of the fold over splits: M and a split's m (kLowest at the least) -> the factors of both sides.
+// One step of the fold over splits: 7 - M and a split's 7 - m -> the factors of both sides.
 __device__ __forceinline__ void join(float& M, float m, float& a, float& b) {
-  const float mn = fmaxf(M, m);
-  a = ex2(__fsub_rn(M, mn));
-  b = ex2(__fsub_rn(m, mn));
+  const float mn = fminf(M, m);
+  a = ex2(__fsub_rn(mn, M));
+  b = ex2(__fsub_rn(mn, m));
   M = mn;
 }
 
@@ -653,10 +655,10 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT == 256 ? 3 : 4)
 }
 
 // Folds a row's splits in ascending order; one warp per (row, query head, 32 * DPL output dims).
-// The lanes take the splits' maxima 32 at a time: the running maximum before and after each
-// split (a maximum is exact in any order) gives the weights of both sides of its fold step, and
+// The lanes take the splits' 7 - m 32 at a time: the running minimum before and after each
+// split (a minimum is exact in any order) gives the weights of both sides of its fold step, and
 // the fold itself is one chain per output dim in split order whatever DPL is. The partial
-// outputs come U at a time, the next U and the next 32 maxima asked for before these are folded.
+// outputs come U at a time, the next U and the next 32 references asked for before these are folded.
 template <int D, int DPL>
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ po, const float2* __restrict__ pml,
                                                       Rows R, int nrows, int max_splits, int Hq,
@@ -674,7 +676,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
   const int n = attn::num_splits(R, r);
   const int64_t slot0 = (int64_t)r * max_splits * Hq + h;
   const float* src = po + slot0 * D + d0;
-  float M = kLowest, L = 0.f, O[DPL];
+  float M = kUnseen, L = 0.f, O[DPL];
 #pragma unroll
   for (int d = 0; d < DPL; ++d) O[d] = 0.f;
   auto load = [&](int s0, float (&v)[U][DPL]) {  // splits s0 .. s0 + U - 1 (past n: the last again, unused)
@@ -693,7 +695,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
     }
   };
   auto load_ml = [&](int s0) {
-    return s0 + lane < n ? pml[slot0 + (int64_t)(s0 + lane) * Hq] : make_float2(kLowest, 0.f);
+    return s0 + lane < n ? pml[slot0 + (int64_t)(s0 + lane) * Hq] : make_float2(kUnseen, 0.f);
   };
   if (n > 0) {
     float va[U][DPL], vb[U][DPL];
@@ -717,13 +719,13 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
       if (s0 + U < n) load(s0 + U, vb);
       if (s0 % 32 == 0) {
         if (s0) ml = next, next = load_ml(s0 + 32);
-        float top = ml.x;  // the running maximum up to and with this lane's split
+        float top = ml.x;  // the running minimum up to and with this lane's split
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const float y = __shfl_up_sync(kFullMask, top, d);
-          if (lane >= d) top = fmaxf(top, y);
+          if (lane >= d) top = fminf(top, y);
         }
-        top = fmaxf(top, M);
+        top = fminf(top, M);
         float prev = __shfl_up_sync(kFullMask, top, 1);
         if (lane == 0) prev = M;
         join(prev, ml.x, a, b);
@@ -749,15 +751,25 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
 // ---------------------------------------------------------------------------
 // Prefill: rows of one sequence that follow one another in the batch are taken in tiles, and a
 // tile and one kv-head run on one CTA. Query row i of a tile is query head i % G of token i / G.
-//   * tile_kernel, tiles of up to 192 query rows: eight warps share out the tiles of 8 query rows
-//     (three each at most), and four more widen keys and values once for all of them into a ring of
-//     stages in shared memory, in fragment order (every access is 16 contiguous bytes a lane).
+//   * tile_kernel, tiles of up to 192 query rows: eight warps (twelve for D = 64) share out the
+//     tiles of 8 query rows (three each at most; two), and four more widen keys and values once for
+//     all of them into a ring of stages in shared memory, in fragment order (every access is 16
+//     contiguous bytes a lane).
 //   * few_kernel, tiles of up to kFewRows query rows (decode rows in a mixed batch, ends of
 //     chunks): every warp takes all the rows and every fourth split, reading pages as decode does,
 //     and the CTA folds four splits at a time.
 // Either way a split is folded by one warp in the order above, and splits in ascending order.
-// Bound: the tensor cores' mma.sync rate (509 TFLOP/s measured on operands in registers), with
-// the reads of the widened operands from shared memory next.
+// Bound: the latency of a folding warp's instructions. One prompt of 4096 tokens (32 heads over 8,
+// D = 128, int8; 137 GFLOP) takes 0.556 ms, 247 TFLOP/s, where mma.sync itself gave 509 TFLOP/s on
+// operands in registers; the schedulers issue in a quarter of the cycles, and what is left is the
+// wait for one result after another with two (D = 64: three) folding warps on a scheduler, as
+// many as the accumulators leave room for.
+//   * D = 128: 3 tiles on 8 warps; 2 on 12 spills the accumulators (695 us against 600 then).
+//   * D = 64: 2 tiles on 12 warps (322 us for that prompt); 3 on 8 took 358, 3 on 12 403.
+//   * A third tile's queries are read from shared memory for each page: the registers that this
+//     frees are worth more than the reads (600 -> 583 us).
+//   * The scores of a page are not issued ahead of the weights of the one before, which takes
+//     registers for both (D = 64: 340 us with, 322 without; D = 128: no difference).
 
 constexpr int kFewRows = 16;
 
@@ -903,27 +915,35 @@ __device__ __forceinline__ void store_row(uint16_t* dst, const float (&x)[D / 8]
   }
 }
 
-constexpr int kNT = 3;          // tiles of 8 query rows per folding warp, at most
-constexpr int kFoldWarps = 8;
 constexpr int kWidenWarps = 4;
-constexpr int kTileThreads = (kFoldWarps + kWidenWarps) * 32;
-constexpr int kTileRows = kFoldWarps * kNT * 8;
 constexpr int kRing = 4;
-// Registers: 384 threads start with 168 each; the widening warps keep 56 and the folding warps
-// take 224 (128 * 56 + 256 * 224 = 384 * 168).
-constexpr int kWidenRegs = 56, kFoldRegs = 224;
+
+// Registers: the CTA starts with the SM's shared out evenly; the widening warps keep 56 each and
+// the folding warps take the rest (D = 128: 128 * 56 + 256 * 224 = 384 * 168; D = 64:
+// 128 * 56 + 384 * 152 = 512 * 128).
+template <int D>
+struct TileShape {
+  static constexpr int NT = D == 128 ? 3 : 2;     // tiles of 8 query rows per folding warp, at most
+  static constexpr int FOLD = D == 128 ? 8 : 12;  // folding warps
+  static constexpr int WARPS = FOLD + kWidenWarps, THREADS = WARPS * 32;
+  static constexpr int ROWS = FOLD * NT * 8;
+  static constexpr int WIDEN_REGS = 56, FOLD_REGS = D == 128 ? 224 : 152, START_REGS = D == 128 ? 168 : 128;
+  static_assert(kWidenWarps * WIDEN_REGS + FOLD * FOLD_REGS <= WARPS * START_REGS, "registers at launch");
+};
 
 template <int D>
 struct TileSmem {
+  using P = TileShape<D>;
   static constexpr int PAGES = 256 / D;                      // pages a stage: one part of each kind per widening warp
   static constexpr int OPERANDS = PAGES * 2 * PAGE * D * 2;  // f16 keys, then values
   static constexpr int STAGE = OPERANDS + PAGES * PAGE * 16;  // and {ks, log2 vs, 2^-16 / vs, -} per token
   static constexpr int TOTALS = kRing * STAGE;               // fp32 totals [row][D], lane by lane
-  static constexpr int STATS = TOTALS + kTileRows * D * 4;   // M and L, lane by lane
-  static constexpr int LENS = STATS + kFoldWarps * 32 * kNT * 16;  // visible lengths, lane by lane
-  static constexpr int BARS = LENS + kFoldWarps * 32 * kNT * 8;
+  static constexpr int STATS = TOTALS + P::ROWS * D * 4;     // M and L, lane by lane
+  static constexpr int LENS = STATS + P::FOLD * 32 * P::NT * 16;  // visible lengths, lane by lane
+  static constexpr int BARS = LENS + P::FOLD * 32 * P::NT * 8;
   static constexpr int ARGS = BARS + kRing * 16;                   // two TileArgs
-  static constexpr int BYTES = ARGS + 512;
+  static constexpr int QUERY = ARGS + 512;                         // a third tile's queries, lane by lane
+  static constexpr int BYTES = QUERY + (P::NT == 3 ? P::FOLD * (D / 32) * 512 : 0);
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -998,7 +1018,7 @@ __device__ __forceinline__ void widen_raw(const Raw& X, uint32_t stage, int warp
 }
 
 // The CTA's barrier; its warps meet it in different places.
-__device__ __forceinline__ void tile_sync() { asm volatile("barrier.cta.sync 0, %0;" ::"n"(kTileThreads) : "memory"); }
+__device__ __forceinline__ void tile_sync() { asm volatile("barrier.cta.sync 0;" ::: "memory"); }
 
 // A wait that, once one of this thread's has given up (recorded), is skipped: the CTA then runs to
 // its end with wrong numbers instead of waiting again at every stage.
@@ -1008,15 +1028,19 @@ __device__ __forceinline__ void ring_wait(uint32_t bar, uint32_t parity, bool& d
 
 // Scores of one page of a buffer for the warp's LIVE tiles, and a page's tokens.
 template <int D, int LIVE>
-__device__ __forceinline__ void wide_scores(const Query<D, LIVE>& Q, uint32_t buf, int page, int lane, float (&s)[LIVE][4]) {
+__device__ __forceinline__ void wide_scores(const Query<D, LIVE>& Q, uint32_t buf, uint32_t third, int page, int lane,
+                                            float (&s)[LIVE][4]) {
   const uint32_t kb = buf + (page * (D / 16) * 32 + lane) * 16;
+  uint4 b;
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) {
     const uint4 a = ld_shared_v4(kb + j * 512);
 #pragma unroll
     for (int n = 0; n < LIVE; ++n) {
-      if (j == 0) mma16816_first(s[n], a, Q.b[n][0][0], Q.b[n][0][1]);
-      else mma16816(s[n], a, Q.b[n][j][0], Q.b[n][j][1]);
+      if (n == 2 && j % 2 == 0) b = ld_shared_v4(third + j * 256);
+      const uint32_t b0 = n < 2 ? Q.b[n][j][0] : j % 2 ? b.z : b.x, b1 = n < 2 ? Q.b[n][j][1] : j % 2 ? b.w : b.y;
+      if (j == 0) mma16816_first(s[n], a, b0, b1);
+      else mma16816(s[n], a, b0, b1);
     }
   }
 }
@@ -1044,23 +1068,16 @@ __device__ __forceinline__ void wide_values(uint32_t buf, int page, int lane, co
   }
 }
 
-// Folds two pages of a stage from `page` on. The scores of the second are issued before the
-// weights of the first (of up to two tiles; three leave no registers for that), so that the
-// tensor cores work through the softmax. masked: query row (n, r) sees the first nv(n, r) tokens.
+// Folds a page of a stage. masked: query row (n, r) sees the first nv(n, r) tokens.
 template <int D, int LIVE, typename Nv>
-__device__ __forceinline__ void fold_wide(const Query<D, LIVE>& Q, uint32_t stage, int page, bool masked, Nv nv, int lane,
-                                          State<D, LIVE>& S) {
-  constexpr bool AHEAD = LIVE < 3;
-  float s[2][LIVE][4];
-  wide_scores<D, LIVE>(Q, stage, page, lane, s[0]);
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    if (u == (AHEAD ? 0 : 1)) wide_scores<D, LIVE>(Q, stage, page + 1, lane, s[1]);
-    const Tokens T = wide_tokens<D>(stage, page + u, lane);
-    uint32_t w[LIVE][2];
-    page_weights<D, LIVE>(Q, s[u], T, masked, [&](int n, int r) { return nv(n, r) - u * PAGE; }, lane >> 2, S, w);
-    wide_values<D, LIVE>(stage, page + u, lane, w, S);
-  }
+__device__ __forceinline__ void fold_wide(const Query<D, LIVE>& Q, uint32_t stage, uint32_t third, int page, bool masked, Nv nv,
+                                          int lane, State<D, LIVE>& S) {
+  float s[LIVE][4];
+  wide_scores<D, LIVE>(Q, stage, third, page, lane, s);
+  const Tokens T = wide_tokens<D>(stage, page, lane);
+  uint32_t w[LIVE][2];
+  page_weights<D, LIVE>(Q, s, T, masked, nv, lane >> 2, S, w);
+  wide_values<D, LIVE>(stage, page, lane, w, S);
 }
 
 // What a warp needs of its tile.
@@ -1083,24 +1100,25 @@ template <int KIND, int D, int LIVE>
 __device__ __forceinline__ void fold_tile(const TileArgs& A, uint8_t* smem, uint32_t base, uint32_t bars, uint32_t& it,
                                           bool& dead, int warp, int lane) {
   using M = TileSmem<D>;
+  using P = TileShape<D>;
   const int g = lane >> 2, c = lane & 3;
   constexpr int CHUNK = M::PAGES * PAGE;
   Query<D, LIVE> Q;
   int shortest = INT_MAX;
   // visible tokens of the lane's query rows, and running totals over splits, in places of this lane's own
-  int2* lens = reinterpret_cast<int2*>(smem + M::LENS) + warp * 32 * kNT + lane;               // entry n at [32 n]
-  float* tot = reinterpret_cast<float*>(smem + M::TOTALS) + warp * (kNT * 8) * D + lane;       // entry i at [32 i]
-  float4* stats = reinterpret_cast<float4*>(smem + M::STATS) + warp * 32 * kNT + lane;         // M and L, entry n at [32 n]
+  int2* lens = reinterpret_cast<int2*>(smem + M::LENS) + warp * 32 * P::NT + lane;               // entry n at [32 n]
+  float* tot = reinterpret_cast<float*>(smem + M::TOTALS) + warp * (P::NT * 8) * D + lane;       // entry i at [32 i]
+  float4* stats = reinterpret_cast<float4*>(smem + M::STATS) + warp * 32 * P::NT + lane;         // M and L, entry n at [32 n]
 #pragma unroll
   for (int n = 0; n < LIVE; ++n) {
-    const int i = (n * kFoldWarps + warp) * 8 + g;
+    const int i = (n * P::FOLD + warp) * 8 + g;
     load_query<D, LIVE>(Q, n,
                         i < A.rows ? A.q + (int64_t)(A.first + i / A.G) * A.ldq + (int64_t)(A.kh * A.G + i % A.G) * D : nullptr,
                         lane, A.scale_log2);
     int len[2] = {0, 0};
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int k = (n * kFoldWarps + warp) * 8 + 2 * c + r;
+      const int k = (n * P::FOLD + warp) * 8 + 2 * c + r;
       if (k >= A.rows) continue;
       int pt_row;
       len[r] = attn::row_len(A.R, A.first + k / A.G, pt_row);
@@ -1108,9 +1126,15 @@ __device__ __forceinline__ void fold_tile(const TileArgs& A, uint8_t* smem, uint
     }
     lens[32 * n] = make_int2(len[0], len[1]);
   }
+  const uint32_t third = base + M::QUERY + (warp * (D / 32) * 32 + lane) * 16;
+  if constexpr (LIVE == 3) {
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j)
+      st_shared_v4(third + j * 512, make_uint4(Q.b[2][2 * j][0], Q.b[2][2 * j][1], Q.b[2][2 * j + 1][0], Q.b[2][2 * j + 1][1]));
+  }
   shortest = __reduce_min_sync(kFullMask, shortest);
 #pragma unroll
-  for (int n = 0; n < LIVE; ++n) stats[32 * n] = make_float4(kLowest, kLowest, 0.f, 0.f);
+  for (int n = 0; n < LIVE; ++n) stats[32 * n] = make_float4(kUnseen, kUnseen, 0.f, 0.f);
 #pragma unroll 8
   for (int i = 0; i < LIVE * D / 4; ++i) tot[32 * i] = 0.f;
 #pragma unroll 1
@@ -1122,9 +1146,9 @@ __device__ __forceinline__ void fold_tile(const TileArgs& A, uint8_t* smem, uint
       const uint32_t stage = base + (it % kRing) * M::STAGE, full = bars + (it % kRing) * 16;
       ring_wait(full, (it / kRing) & 1u, dead);
 #pragma unroll
-      for (int p = 0; p < M::PAGES; p += 2) {  // (pages that none of its rows sees too: a way round them costs more)
+      for (int p = 0; p < M::PAGES; ++p) {  // (pages that none of its rows sees too: a way round them costs more)
         const int at = tp + p * PAGE;
-        fold_wide<D, LIVE>(Q, stage, p, at + 2 * PAGE > shortest,
+        fold_wide<D, LIVE>(Q, stage, third, p, at + PAGE > shortest,
                            [&](int n, int r) {
                              const int2 len = lens[32 * n];
                              return (r ? len.y : len.x) - at;
@@ -1157,7 +1181,7 @@ __device__ __forceinline__ void fold_tile(const TileArgs& A, uint8_t* smem, uint
   for (int n = 0; n < LIVE; ++n)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int k = (n * kFoldWarps + warp) * 8 + 2 * c + r;
+      const int k = (n * P::FOLD + warp) * 8 + 2 * c + r;
       if (k >= A.rows) continue;
       const float4 st = stats[32 * n];
       float x[D / 8];
@@ -1190,18 +1214,19 @@ __device__ __forceinline__ void widen_tile(const TileArgs& A, uint32_t base, uin
 }
 
 template <int KIND, int D>
-__global__ void __launch_bounds__(kTileThreads, 1)
+__global__ void __launch_bounds__(TileShape<D>::THREADS, 1)
     tile_kernel(const uint16_t* __restrict__ q, int64_t ldq, int Hq, int Hkv, Cache C, Rows R, int T, int per,
                 const int32_t* __restrict__ list, Counts* __restrict__ counts, uint16_t* __restrict__ out,
                 float scale_log2) {
   using M = TileSmem<D>;
+  using P = TileShape<D>;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem), bars = base + M::BARS;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(bars + 16 * i, kWidenWarps);     // a stage is complete
-      mbar_init(bars + 16 * i + 8, kFoldWarps);  // a stage has been read
+      mbar_init(bars + 16 * i + 8, P::FOLD);  // a stage has been read
     }
     fence_mbar_init();
   }
@@ -1235,21 +1260,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                    item % Hkv, len, scale_log2};
   };
   int b = 0;
-  if (warp >= kFoldWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWidenRegs));
-    const bool looks = warp == kFoldWarps + kWidenWarps - 1;
+  if (warp >= P::FOLD) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::WIDEN_REGS));
+    const bool looks = warp == P::FOLD + kWidenWarps - 1;
     if (looks) look_up(args[0]);
     for (tile_sync(); args[b].rows >= 0; b ^= 1, tile_sync()) {
-      widen_tile<KIND, D>(args[b], base, bars, it, dead, warp - kFoldWarps, lane);
+      widen_tile<KIND, D>(args[b], base, bars, it, dead, warp - P::FOLD, lane);
       if (looks) look_up(args[b ^ 1]);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFoldRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P::FOLD_REGS));
     for (tile_sync(); args[b].rows >= 0; b ^= 1, tile_sync()) {
       const TileArgs& A = args[b];
       const int tiles = (A.rows + 7) / 8;  // of 8 query rows
-      if (tiles > 2 * kFoldWarps + warp) fold_tile<KIND, D, 3>(A, smem, base, bars, it, dead, warp, lane);
-      else if (tiles > kFoldWarps + warp) fold_tile<KIND, D, 2>(A, smem, base, bars, it, dead, warp, lane);
+      if (tiles > (P::NT - 1) * P::FOLD + warp) fold_tile<KIND, D, P::NT>(A, smem, base, bars, it, dead, warp, lane);
+      else if (P::NT > 2 && tiles > P::FOLD + warp) fold_tile<KIND, D, 2>(A, smem, base, bars, it, dead, warp, lane);
       else fold_tile<KIND, D, 1>(A, smem, base, bars, it, dead, warp, lane);
     }
   }
@@ -1308,7 +1333,7 @@ __device__ __forceinline__ void few_tile(const uint16_t* __restrict__ q, int64_t
   for (int i = threadIdx.x; i < rows * D; i += kFewWarps * 32) tot[i] = 0.f;
   // thread -> (row, quarter of D) for the folds
   const int frow = threadIdx.x >> 2, fd = (threadIdx.x & 3) * (D / 4);
-  float FM = kLowest, FL = 0.f;
+  float FM = kUnseen, FL = 0.f;
   for (int r0 = 0; r0 < longest; r0 += kFewWarps * SPLIT) {
     const int t0 = r0 + warp * SPLIT, seen = min(SPLIT, longest - t0);
     State<D, NT> S;

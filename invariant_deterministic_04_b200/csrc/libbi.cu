@@ -279,10 +279,10 @@ cudaError_t q8_decode(const Q8Call& a, const AttnWs& ws) {
 // the tiles of 8 query rows a scheduler has (1 to 6), and about one more for the work that a chunk of
 // keys takes whatever the rows; take what makes the CTAs' rounds over T rows (as if they were one
 // chunk) cheapest, the larger tile among equals.
-int q8_tile_tokens(int64_t T, int G, int Hkv, int sms) {
+int q8_tile_tokens(int64_t T, int G, int Hkv, int most, int sms) {
   int best = 1;
   int64_t least = 0;
-  for (int k = 1; k <= bi::attnq8::kTileRows / 32; ++k) {
+  for (int k = 1; k <= most / 32; ++k) {
     const int per = 32 * k / G;
     const int64_t rounds = ((T + per - 1) / per * Hkv + sms - 1) / sms;
     if (k == 1 || rounds * (k + 1) <= least) best = per, least = rounds * (k + 1);
@@ -298,16 +298,16 @@ cudaError_t q8_prefill(const Q8Call& a, int32_t* list, bi::attnq8::Counts* count
   struct TileTag {};  // one set of once-flags per instantiation
   struct FewTag {};
   int tile_sm = 0, few_sm = 0;
-  cudaError_t e = resident_ctas<TileTag>(tile, a8::kTileThreads, a8::TileSmem<D>::BYTES, a.dev, &tile_sm);
+  cudaError_t e = resident_ctas<TileTag>(tile, a8::TileShape<D>::THREADS, a8::TileSmem<D>::BYTES, a.dev, &tile_sm);
   if (e == cudaSuccess) e = resident_ctas<FewTag>(rest, a8::kFewWarps * 32, a8::FewSmem<D>::BYTES, a.dev, &few_sm);
   if (e != cudaSuccess) return e;
-  const int G = a.Hq / a.Hkv, few = a8::kFewRows / G, per = q8_tile_tokens(a.rows, G, a.Hkv, a.sms);
+  const int G = a.Hq / a.Hkv, few = a8::kFewRows / G, per = q8_tile_tokens(a.rows, G, a.Hkv, a8::TileShape<D>::ROWS, a.sms);
   e = bi::launch_pdl(a8::plan_kernel, dim3(1), dim3(1024), 0, a.st, a.R.q_seq, a.rows, per, few, list, counts);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)a.rows * a.Hkv;
   if (a.rows > few) {  // else there are few-row tiles only
     const int64_t full = (int64_t)a.sms * tile_sm;
-    e = bi::launch_pdl(tile, dim3((unsigned)(most < full ? most : full)), dim3(a8::kTileThreads),
+    e = bi::launch_pdl(tile, dim3((unsigned)(most < full ? most : full)), dim3(a8::TileShape<D>::THREADS),
                        (size_t)a8::TileSmem<D>::BYTES, a.st, a.q, a.ldq, a.Hq, a.Hkv, a.C, a.R, a.rows, per,
                        (const int32_t*)list, counts, a.out, a.c);
     if (e != cudaSuccess) return e;
