@@ -428,22 +428,30 @@ __device__ __forceinline__ void fold_page(const Query<D, NT>& Q, float (&s)[NT][
 // ---------------------------------------------------------------------------
 // Decode: one warp per (row, kv-head, split); the split's partial result goes to the workspace.
 //
-// Bound: HBM (Hkv (2 D + 8) bytes per token against 4 Hq D flops). Each warp has a ring of
-// kStages pages that one lane fills by TMA (two tiles and two 64-byte scale rows a page), ahead
-// across item boundaries, and widens pages from it. The same ring filled by cp.async, lane by
-// lane, took 0.50 ms for 2.2 GB without any arithmetic; TMA takes that off the warps.
+// Bound: HBM (Hkv (2 D + 8) bytes per token against 4 Hq D flops) where there are splits enough to
+// go round: 64 int8 sequences of up to 32768 tokens (2.2 GB) take 384 us, 5.76 TB/s. A single
+// short round is bound by one warp's 16 pages one after another (one sequence of 16921 tokens: 21 us).
+// Each warp has a ring of kStages pages that one lane fills by TMA (two tiles and two 64-byte scale
+// rows a page), ahead across item boundaries, and widens pages from it. The same ring filled by
+// cp.async, lane by lane, took 0.50 ms for those 2.2 GB without any arithmetic; TMA takes that off
+// the warps. Three stages: two took 406 us and four 415 where three took 394; deeper rings for the
+// fewer warps of a short round gained nothing.
 
-constexpr int kWarps = 4;
 constexpr int kStages = 3;
 constexpr int kCoarse = 512;  // entries of the split-count prefix that a CTA keeps
 
-template <int D>
+// W warps a CTA.
+template <int D, int W>
 struct Ring {
-  static constexpr int SCALES = kWarps * kStages * kPageBytes<D>;
-  static constexpr int BARS = SCALES + kWarps * kStages * kScaleBytes;
-  static constexpr int PREFIX = BARS + kWarps * kStages * 8;
+  static constexpr int SCALES = W * kStages * kPageBytes<D>;
+  static constexpr int BARS = SCALES + W * kStages * kScaleBytes;
+  static constexpr int PREFIX = BARS + W * kStages * 8;
   static constexpr int SMEM = 1024 + PREFIX + kCoarse * 4;  // pages start on a 1024-byte boundary
+  static_assert(SMEM <= 227 * 1024, "shared memory");
 };
+// Warps that an SM's registers hold: 168 a thread with 16 query rows of 128 dims, else 128.
+template <int D, int NT>
+constexpr int kSmWarps = D * NT == 256 ? 12 : 16;
 
 // Tensor map of a cache's rows [rows, D] of bytes, loaded a page (16 rows) at a time.
 template <int D>
@@ -464,15 +472,15 @@ struct Item {
   int r, s, kh, seen, page;
 };
 
-template <int KIND, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, D * NT == 256 ? 3 : 4)
+template <int KIND, int D, int NT, int W>
+__global__ void __launch_bounds__(W * 32, kSmWarps<D, NT> / W)
     split_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
                  const uint16_t* __restrict__ q, int Hq, int Hkv, Cache C, Rows R, int nrows, int max_splits,
                  float* __restrict__ po, float2* __restrict__ pml, float scale_log2) {
-  using T = Ring<D>;
+  using T = Ring<D, W>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  __shared__ int32_t warp_sum[kWarps];
+  __shared__ int32_t warp_sum[W];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int G = Hq / Hkv;
@@ -492,7 +500,7 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT == 256 ? 3 : 4)
   // the prefix of split counts, `per` rows an entry (1 up to kCoarse rows)
   const int per = (nrows + kCoarse - 1) / kCoarse, entries = (nrows + per - 1) / per;
   int base = 0;
-  for (int e0 = 0; e0 < entries; e0 += kWarps * 32) {
+  for (int e0 = 0; e0 < entries; e0 += W * 32) {
     const int e = e0 + (int)threadIdx.x;
     int n = 0;
     if (e < entries)
@@ -507,7 +515,7 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT == 256 ? 3 : 4)
     __syncthreads();
     int before = base;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       if (w < warp) before += warp_sum[w];
       base += warp_sum[w];
     }
@@ -515,7 +523,7 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT == 256 ? 3 : 4)
     __syncthreads();
   }
   const int total = base * Hkv;
-  const int step = (int)gridDim.x * kWarps;
+  const int step = (int)gridDim.x * W;
 
   auto fetch = [&](int item) {
     Item I;

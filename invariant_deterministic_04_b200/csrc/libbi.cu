@@ -242,32 +242,42 @@ struct Q8Call {
   cudaStream_t st;
 };
 
-template <int KIND, int D, int NT>
+template <int KIND, int D, int NT, int W>
 cudaError_t q8_split(const Q8Call& a, const AttnWs& ws) {
-  namespace a8 = bi::attnq8;
-  auto kernel = a8::split_kernel<KIND, D, NT>;
+  using T = bi::attnq8::Ring<D, W>;
+  auto kernel = bi::attnq8::split_kernel<KIND, D, NT, W>;
   struct Tag {};  // one set of once-flags per instantiation
   int per_sm = 0;
-  const cudaError_t e = resident_ctas<Tag>(kernel, a8::kWarps * 32, a8::Ring<D>::SMEM, a.dev, &per_sm);
+  const cudaError_t e = resident_ctas<Tag>(kernel, W * 32, T::SMEM, a.dev, &per_sm);
   if (e != cudaSuccess) return e;
   CUtensorMap km, vm;
   const int64_t store_rows = a.C.num_pages * a.Hkv * BI_PAGE_TOKENS;
-  if (!a8::make_page_map<D>(&km, a.C.k, store_rows) || !a8::make_page_map<D>(&vm, a.C.v, store_rows))
+  if (!bi::attnq8::make_page_map<D>(&km, a.C.k, store_rows) || !bi::attnq8::make_page_map<D>(&vm, a.C.v, store_rows))
     return cudaErrorInvalidValue;
   // no more CTAs than there can be items
   const int ms = max_splits(a.R.max_pages);
-  const int64_t ctas = ((int64_t)a.rows * ms * a.Hkv + a8::kWarps - 1) / a8::kWarps;
-  const int64_t full = (int64_t)a.sms * per_sm;
-  return bi::launch_pdl(kernel, dim3((unsigned)(ctas < full ? ctas : full)), dim3(a8::kWarps * 32),
-                        (size_t)a8::Ring<D>::SMEM, a.st, km, vm, a.q, a.Hq, a.Hkv, a.C, a.R, a.rows, ms, ws.po, ws.pml, a.c);
+  const int64_t ctas = ((int64_t)a.rows * ms * a.Hkv + W - 1) / W, full = (int64_t)a.sms * per_sm;
+  return bi::launch_pdl(kernel, dim3((unsigned)(ctas < full ? ctas : full)), dim3(W * 32), (size_t)T::SMEM, a.st, km, vm, a.q,
+                        a.Hq, a.Hkv, a.C, a.R, a.rows, ms, ws.po, ws.pml, a.c);
+}
+
+// One CTA an SM where there can be more than two rounds of splits: their prefix is counted once an SM
+// (16 sequences, 599 MB: 144 -> 125 us; 64, 2.2 GB: 392 -> 384). CTAs of four warps otherwise, which
+// leave room for the launches before and after them (one sequence 29 -> 21 us, 37 short ones 49 -> 47).
+template <int KIND, int D, int NT>
+cudaError_t q8_split_any(const Q8Call& a, const AttnWs& ws) {
+  constexpr int SM = bi::attnq8::kSmWarps<D, NT>;
+  return (int64_t)a.rows * max_splits(a.R.max_pages) * a.Hkv > (int64_t)a.sms * SM * 2 ? q8_split<KIND, D, NT, SM>(a, ws)
+                                                                                   : q8_split<KIND, D, NT, 4>(a, ws);
 }
 
 template <int KIND, int D>
 cudaError_t q8_decode(const Q8Call& a, const AttnWs& ws) {
   namespace a8 = bi::attnq8;
-  const cudaError_t e = a.Hq / a.Hkv <= 8 ? q8_split<KIND, D, 1>(a, ws) : q8_split<KIND, D, 2>(a, ws);
+  const cudaError_t e = a.Hq / a.Hkv <= 8 ? q8_split_any<KIND, D, 1>(a, ws) : q8_split_any<KIND, D, 2>(a, ws);
   if (e != cudaSuccess) return e;
-  // one dim per lane while that leaves at most 32 warps per SM, else D / 32 (fewer, wider loads)
+  // One dim per lane while that leaves at most 32 warps per SM, else D / 32 (fewer, wider loads): 37
+  // sequences of 32 heads 47.1 us one way and 48.1 the other, 128 of them 121.9 and 117.6 (the whole call).
   const int64_t heads = (int64_t)a.rows * a.Hq;
   const bool narrow = heads * (D / 32) <= (int64_t)a.sms * 32;
   auto kernel = narrow ? a8::combine_kernel<D, 1> : a8::combine_kernel<D, D / 32>;
@@ -275,8 +285,8 @@ cudaError_t q8_decode(const Q8Call& a, const AttnWs& ws) {
                         (const float*)ws.po, (const float2*)ws.pml, a.R, a.rows, max_splits(a.R.max_pages), a.Hq, a.out);
 }
 
-// Tokens a prefill tile takes. A CTA's eight folding warps sit on four schedulers, so its time goes by
-// the tiles of 8 query rows a scheduler has (1 to 6), and about one more for the work that a chunk of
+// Tokens a prefill tile takes. A CTA's folding warps sit on four schedulers, so its time goes by the
+// tiles of 8 query rows a scheduler has (1 to 6), and about one more for the work that a chunk of
 // keys takes whatever the rows; take what makes the CTAs' rounds over T rows (as if they were one
 // chunk) cheapest, the larger tile among equals.
 int q8_tile_tokens(int64_t T, int G, int Hkv, int most, int sms) {

@@ -104,7 +104,9 @@ inline cudaError_t launch_hpg(const Part& q, const Part& k, int64_t T, int Hq, i
 }
 
 // Four heads a group of lanes once one head each would give the SMs more than twice the threads
-// they hold; below that more, shorter threads finish sooner.
+// they hold; below that more, shorter threads finish as soon or sooner. 32 + 8 heads of 128, one
+// head against four: 64 rows 2.7 us and 3.4, 577 rows 4.6 and 4.4, 4096 rows 19.4 and 13.8, 32768
+// rows 164 and 117 (671 MB: 5.7 TB/s).
 template <int D>
 inline cudaError_t launch_d(const Part& q, const Part& k, int64_t T, int Hq, int H, const int32_t* pos, const float2* table,
                             int max_pos, float eps, int sms, cudaStream_t st) {
