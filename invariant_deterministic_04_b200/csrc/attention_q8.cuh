@@ -764,8 +764,9 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
 //     all of them into a ring of stages in shared memory, in fragment order (every access is 16
 //     contiguous bytes a lane).
 //   * few_kernel, tiles of up to kFewRows query rows (decode rows in a mixed batch, ends of
-//     chunks): every warp takes all the rows and every fourth split, reading pages as decode does,
-//     and the CTA folds four splits at a time.
+//     chunks, short chunks): every warp takes all the rows and one split at a time, reading pages as
+//     decode does; a CTA, or a cluster of kFewCluster where there are few tiles, folds as many splits
+//     as it has warps at a time.
 // Either way a split is folded by one warp in the order above, and splits in ascending order.
 // Bound: the latency of a folding warp's instructions. One prompt of 4096 tokens (32 heads over 8,
 // D = 128, int8; 137 GFLOP) takes 0.556 ms, 247 TFLOP/s, where mma.sync itself gave 509 TFLOP/s on
@@ -788,7 +789,8 @@ struct Counts {
 };
 
 // Cuts the runs of rows of one sequence into tiles of `per` tokens. One CTA of 1024 threads, each
-// owning a contiguous stretch of rows. A tile whose run ends within `few` tokens is a few-row tile.
+// owning a contiguous stretch of rows. A tile whose run ends within `few` tokens is a few-row tile,
+// and so is every tile if per == few.
 __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ q_seq, int T, int per, int few,
                                                     int32_t* __restrict__ list, Counts* __restrict__ counts) {
   __shared__ int32_t warp_last[32];
@@ -799,7 +801,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
   const int each = (T + 1023) / 1024;
   const int r0 = (int)min((int64_t)tid * each, (int64_t)T), r1 = min(r0 + each, T);
   auto starts = [&](int r) { return r == 0 || q_seq[r] != q_seq[r - 1]; };
-  auto is_few = [&](int r) { return r + few >= T || q_seq[r + few] != q_seq[r]; };
+  auto is_few = [&](int r) { return per == few || r + few >= T || q_seq[r + few] != q_seq[r]; };
   // the start of the run that row r0 - 1 lies in: the running maximum of run starts before this thread
   int last = -1;
   for (int r = r0; r < r1; ++r)
@@ -1290,6 +1292,7 @@ __global__ void __launch_bounds__(TileShape<D>::THREADS, 1)
 
 constexpr int kFewWarps = 4;
 constexpr int kFewStages = 3;
+constexpr int kFewCluster = 8;
 
 template <int D>
 struct FewSmem {
@@ -1300,12 +1303,18 @@ struct FewSmem {
   static constexpr int BYTES = OVER + kFewWarps * kFewRows * 8 + kFewRows * D * 4;
 };
 
-// One tile of up to 8 NT query rows.
-template <int KIND, int D, int NT>
+// One tile of up to 8 NT query rows, by the CTAS CTAs of a cluster (1: this CTA alone).
+template <int KIND, int D, int NT, int CTAS>
 __device__ __forceinline__ void few_tile(const uint16_t* __restrict__ q, int64_t ldq, int Hq, int Hkv, int G, const Cache& C,
                                          const Rows& R, int first, int rows, int kh, uint16_t* __restrict__ out,
                                          float scale_log2, uint8_t* smem, int warp, int lane) {
   using M = FewSmem<D>;
+  const int rank = CTAS > 1 ? (int)cluster_rank() : 0;
+  auto sync = [&] {  // all that share the tile
+    __syncwarp();
+    if (CTAS > 1) cluster_barrier();
+    else __syncthreads();
+  };
   const int g = lane >> 2, c = lane & 3;
   const uint32_t base = smem_u32(smem);
   Query<D, NT> Q;
@@ -1332,18 +1341,18 @@ __device__ __forceinline__ void few_tile(const uint16_t* __restrict__ q, int64_t
   shortest = __reduce_min_sync(kFullMask, shortest);
   pt_row = __reduce_max_sync(kFullMask, pt_row);  // rows that see anything share it; the others gave 0
   const int32_t* prow = C.pt + (int64_t)pt_row * R.max_pages;
-  // four splits at a time, one a warp; then row k's thread group folds them in order
+  // a split a warp at a time; then row k's four threads of each CTA fold them in order, D / CTAS dims a CTA
   const uint32_t ring = base + (uint32_t)(warp * kFewStages * kPageBytes<D>);
   const uint32_t scales = base + (uint32_t)(kFewWarps * kFewStages * kPageBytes<D> + warp * kFewStages * kScaleBytes);
   float* part = reinterpret_cast<float*>(smem);                                  // [warp][row][D]
   float2* pml = reinterpret_cast<float2*>(smem + M::OVER);                          // [warp][row]
   float* tot = reinterpret_cast<float*>(smem + M::OVER + kFewWarps * kFewRows * 8);      // [row][D]
   for (int i = threadIdx.x; i < rows * D; i += kFewWarps * 32) tot[i] = 0.f;
-  // thread -> (row, quarter of D) for the folds
-  const int frow = threadIdx.x >> 2, fd = (threadIdx.x & 3) * (D / 4);
+  constexpr int dims = D / 4 / CTAS;  // even
+  const int frow = threadIdx.x >> 2, fd = (threadIdx.x & 3) * (D / 4) + rank * dims;
   float FM = kUnseen, FL = 0.f;
-  for (int r0 = 0; r0 < longest; r0 += kFewWarps * SPLIT) {
-    const int t0 = r0 + warp * SPLIT, seen = min(SPLIT, longest - t0);
+  for (int r0 = 0; r0 < longest; r0 += CTAS * kFewWarps * SPLIT) {
+    const int t0 = r0 + (rank * kFewWarps + warp) * SPLIT, seen = min(SPLIT, longest - t0);
     State<D, NT> S;
     S.clear();
     const int np = seen > 0 ? (seen + PAGE - 1) / PAGE : 0;
@@ -1391,27 +1400,54 @@ __device__ __forceinline__ void few_tile(const uint16_t* __restrict__ q, int64_t
           if (g == 0) pml[warp * kFewRows + k] = make_float2(r ? S.m[n].y : S.m[n].x, l);
         }
     }
-    __syncthreads();
-    if (frow < rows)
-      for (int w = 0; w < kFewWarps && r0 + w * SPLIT < longest; ++w) {
-        const float2 ml = pml[w * kFewRows + frow];
-        float fa, fb;
-        join(FM, ml.x, fa, fb);
-        FL = __fmaf_rn(ml.y, fb, __fmul_rn(FL, fa));
-        for (int d = fd; d < fd + D / 4; ++d)
-          tot[frow * D + d] = __fmaf_rn(part[(w * kFewRows + frow) * D + d], fb, __fmul_rn(tot[frow * D + d], fa));
+    sync();
+    if (frow < rows) {
+      for (int o = 0; o < CTAS && r0 + o * kFewWarps * SPLIT < longest; ++o) {  // the CTAs' splits, in order
+        const int n = min(kFewWarps, (longest - r0 + SPLIT - 1) / SPLIT - o * kFewWarps);
+        float fa[kFewWarps], fb[kFewWarps];
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) {
+          fa[w] = 1.f;
+          fb[w] = 0.f;
+          if (w >= n) continue;
+          const uint32_t at = base + M::OVER + (uint32_t)(w * kFewRows + frow) * 8;
+          float m, l;
+          if (CTAS > 1) {
+            const uint32_t far = map_to_rank(at, (uint32_t)o);
+            m = ld_cluster_f32(far);
+            l = ld_cluster_f32(far + 4);
+          } else {
+            m = ld_shared_f32(at);
+            l = ld_shared_f32(at + 4);
+          }
+          join(FM, m, fa[w], fb[w]);
+          FL = __fmaf_rn(l, fb[w], __fmul_rn(FL, fa[w]));
+        }
+#pragma unroll 2
+        for (int d = fd; d < fd + dims; ++d) {
+          const uint32_t at = base + (uint32_t)(frow * D + d) * 4;
+          const uint32_t far = CTAS > 1 ? map_to_rank(at, (uint32_t)o) : at;
+          float v[kFewWarps];
+#pragma unroll
+          for (int w = 0; w < kFewWarps; ++w) {
+            v[w] = 0.f;
+            if (w < n) v[w] = CTAS > 1 ? ld_cluster_f32(far + w * kFewRows * D * 4) : ld_shared_f32(far + w * kFewRows * D * 4);
+          }
+          float x = tot[frow * D + d];
+#pragma unroll
+          for (int w = 0; w < kFewWarps; ++w)
+            if (w < n) x = __fmaf_rn(v[w], fb[w], __fmul_rn(x, fa[w]));
+          tot[frow * D + d] = x;
+        }
       }
-    __syncthreads();  // the partial results are read: the rings may be refilled
+    }
+    sync();  // the partial results are read: the rings may be refilled
   }
   __syncthreads();
   if (frow < rows) {
-    uint16_t* dst = out + ((int64_t)(first + frow / G) * Hq + kh * G + frow % G) * D + fd;
-    for (int d = 0; d < D / 4; d += D / 8) {
-      float x[D / 8];
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) x[i] = tot[frow * D + fd + d + i];
-      store_row<D>(dst + d, x, FL);
-    }
+    uint16_t* dst = out + ((int64_t)(first + frow / G) * Hq + kh * G + frow % G) * D;
+    for (int d = fd; d < fd + dims; d += 2)
+      *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16x2(row_out(tot[frow * D + d], FL), row_out(tot[frow * D + d + 1], FL));
   }
 }
 
@@ -1419,18 +1455,31 @@ template <int KIND, int D>
 __global__ void __launch_bounds__(kFewWarps * 32, 3)
     few_kernel(const uint16_t* __restrict__ q, int64_t ldq, int Hq, int Hkv, Cache C, Rows R, int T, int few,
                const int32_t* __restrict__ list, const Counts* __restrict__ counts, uint16_t* __restrict__ out,
-               float scale_log2) {
+               float scale_log2, bool clusters) {
   extern __shared__ __align__(1024) uint8_t smem_few[];  // pages' swizzle counts from 128-byte boundaries
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = Hq / Hkv;
   pdl_wait();  // the plan (and the caller's q and store) are complete from here on
   pdl_trigger();
   const int total = counts->few * Hkv;
-  for (int item = blockIdx.x; item < total; item += gridDim.x) {
+  // A cluster a tile where that takes two rounds of clusters at most (a few rows of long contexts);
+  // a CTA a tile otherwise, and where no row can have more splits than a CTA has warps. One decode row
+  // at 32000 tokens 520 -> 102 us, 16 rows at 4000 151 -> 63 us (8 kv-heads of 128, e4m3).
+  const bool together = clusters && total <= 2 * (int)gridDim.x / kFewCluster;
+  const int ctas = together ? kFewCluster : 1;
+  for (int item = (int)blockIdx.x / ctas; item < total; item += (int)gridDim.x / ctas) {
     const int first = list[T - 1 - item / Hkv], kh = item % Hkv;
     const int rows = tile_tokens(R.q_seq, first, T, few, lane) * G;
-    if (rows <= 8) few_tile<KIND, D, 1>(q, ldq, Hq, Hkv, G, C, R, first, rows, kh, out, scale_log2, smem_few, warp, lane);
-    else few_tile<KIND, D, 2>(q, ldq, Hq, Hkv, G, C, R, first, rows, kh, out, scale_log2, smem_few, warp, lane);
+#define BI_FEW_TILE(NT, CTAS) \
+  few_tile<KIND, D, NT, CTAS>(q, ldq, Hq, Hkv, G, C, R, first, rows, kh, out, scale_log2, smem_few, warp, lane)
+    if (together) {
+      if (rows <= 8) BI_FEW_TILE(1, kFewCluster);
+      else BI_FEW_TILE(2, kFewCluster);
+    } else {
+      if (rows <= 8) BI_FEW_TILE(1, 1);
+      else BI_FEW_TILE(2, 1);
+    }
+#undef BI_FEW_TILE
     __syncthreads();  // shared memory is free for the next tile
   }
 }

@@ -311,21 +311,34 @@ cudaError_t q8_prefill(const Q8Call& a, int32_t* list, bi::attnq8::Counts* count
   cudaError_t e = resident_ctas<TileTag>(tile, a8::TileShape<D>::THREADS, a8::TileSmem<D>::BYTES, a.dev, &tile_sm);
   if (e == cudaSuccess) e = resident_ctas<FewTag>(rest, a8::kFewWarps * 32, a8::FewSmem<D>::BYTES, a.dev, &few_sm);
   if (e != cudaSuccess) return e;
-  const int G = a.Hq / a.Hkv, few = a8::kFewRows / G, per = q8_tile_tokens(a.rows, G, a.Hkv, a8::TileShape<D>::ROWS, a.sms);
+  const int G = a.Hq / a.Hkv, few = a8::kFewRows / G;
+  const int64_t few_full = (int64_t)a.sms * few_sm / a8::kFewCluster * a8::kFewCluster;
+  // Clusters where a row can have more splits than a CTA's warps take at a time; then short chunks go
+  // as few-row tiles too, where the clusters take them in one round: a CTA of the wide tiles would walk
+  // the whole context (16 rows at 4000 tokens 151 us, 63 in clusters; 48 rows, two rounds, 154 and 156).
+  const bool clusters = max_splits(a.R.max_pages) > a8::kFewWarps;
+  const bool all_few = clusters && ((int64_t)a.rows + few - 1) / few * a.Hkv <= few_full / a8::kFewCluster;
+  const int per = all_few ? few : q8_tile_tokens(a.rows, G, a.Hkv, a8::TileShape<D>::ROWS, a.sms);
   e = bi::launch_pdl(a8::plan_kernel, dim3(1), dim3(1024), 0, a.st, a.R.q_seq, a.rows, per, few, list, counts);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)a.rows * a.Hkv;
-  if (a.rows > few) {  // else there are few-row tiles only
+  if (a.rows > few && !all_few) {  // else there are few-row tiles only
     const int64_t full = (int64_t)a.sms * tile_sm;
     e = bi::launch_pdl(tile, dim3((unsigned)(most < full ? most : full)), dim3(a8::TileShape<D>::THREADS),
                        (size_t)a8::TileSmem<D>::BYTES, a.st, a.q, a.ldq, a.Hq, a.Hkv, a.C, a.R, a.rows, per,
                        (const int32_t*)list, counts, a.out, a.c);
     if (e != cudaSuccess) return e;
   }
+  if (clusters) {
+    const int64_t ctas = most * a8::kFewCluster;
+    return bi::launch_pdl_clusters(a8::kFewCluster, rest, dim3((unsigned)(ctas < few_full ? ctas : few_full)),
+                                   dim3(a8::kFewWarps * 32), (size_t)a8::FewSmem<D>::BYTES, a.st, a.q, a.ldq, a.Hq, a.Hkv,
+                                   a.C, a.R, a.rows, few, (const int32_t*)list, (const a8::Counts*)counts, a.out, a.c, true);
+  }
   const int64_t full = (int64_t)a.sms * few_sm;
   return bi::launch_pdl(rest, dim3((unsigned)(most < full ? most : full)), dim3(a8::kFewWarps * 32),
                         (size_t)a8::FewSmem<D>::BYTES, a.st, a.q, a.ldq, a.Hq, a.Hkv, a.C, a.R, a.rows, few,
-                        (const int32_t*)list, (const a8::Counts*)counts, a.out, a.c);
+                        (const int32_t*)list, (const a8::Counts*)counts, a.out, a.c, false);
 }
 
 // ---- LM head workspace: bf16 logits [M, V], fp32 logits [M, V], flagged list [M + 1],

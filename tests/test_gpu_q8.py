@@ -534,3 +534,22 @@ def test_a_captured_chunk_replays_with_the_eager_bits():
         torch.cuda.synchronize()
         assert same_bits(out, want)
     assert int((pos == -1).sum()) > 0 and bi.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind,Hq,Hkv,D", [("int8", 16, 2, 128), ("e4m3", 14, 2, 64), ("int8", 16, 1, 64),
+                                           ("e4m3", 32, 8, 128)])
+def test_few_rows_of_long_contexts_have_the_decode_bits(kind, Hq, Hkv, D):
+    """Short chunks and decode rows over up to 37 splits (more than a cluster's warps take at a time),
+    alone and beside a chunk of many rows or many decode rows, and rows that see nothing."""
+    lens = [9300, 1024, 1025, 8193, 40, 0]
+    S, _ = fill(kind, lens, Hkv, D, 600, seed=330)
+    chunks = [(0, range(9290, 9300)), (5, [-1]), (1, [1023]), (2, range(1020, 1025)), (3, [8192, 8191, 3]), (4, range(30, 40))]
+    wide = chunks + [(0, range(9000, 9280))]
+    many = [(b, [n - 1]) for b, n in enumerate(lens)] * 30
+    for parts in (chunks, wide, many):
+        seq = torch.tensor([b for b, r in parts for _ in r], dtype=torch.int32, device=dev())
+        pos = torch.tensor([x for _, r in parts for x in r], dtype=torch.int32, device=dev())
+        q = synth.normal_bf16((len(seq), Hq, D), 331).to(dev())
+        pre = bi.attention_prefill_q8(q, seq, pos, *S.args)
+        dec = bi.attention_decode_q8(q, *S.args[:4], S.pt[seq.long()].contiguous(), pos + 1)
+        assert bi.get_device_error() == 0 and same_bits(pre, dec)
