@@ -293,13 +293,15 @@ bi_status bi_kv_read_q8(bi_bf16* k_out, bi_bf16* v_out, int64_t ld_out, const in
 /*
  * Attention over the 8-bit store: bi_attention_decode and bi_attention_prefill with the store
  * above in place of the bf16 one. Keys and values are the exact v * s; with
- * z_t = scale log2(e) q.(k_t sk_t) + log2 sv_t and w_t = 2^(z_t - m),
- *   out = sum_t w_t v_t / sum_t (w_t / sv_t)    (= softmax(scale q.k) v for any m),
- * m following the running maximum of z (it moves when that has risen by more than 8). The
- * products run on tensor cores in f16 with fp32 sums (8-bit values are exact in f16; a query
- * row is scaled by a power of two; 2^7 w_t is rounded to f16: 2^-11 relative, and 2^-32 of the
- * largest weight for the faintest ones), everything else in fp32, one rounding to bf16. Splits of 256 tokens at absolute positions, pages in order, splits folded
- * in ascending order: a row's bits depend on its own length and slots only, and a prefill row
+ * z_t = scale log2(e) q.(k_t sk_t), p_t = 2^(z_t - m) and w_t = p_t F sv_t,
+ *   out = sum_t w_t v_t / (F sum_t p_t)    (= softmax(scale q.k) v for any m and F),
+ * m following the running maximum of z and F that of 2^7 / (p sv) (they move when a w_t passes
+ * 2^15). The products run on tensor cores in f16 with fp32 sums (8-bit values are exact in f16;
+ * a query row is scaled by a power of two; w_t is rounded to f16: 2^-11 relative, and 2^-32 of
+ * the largest w for the faintest), everything else in fp32, one rounding to bf16. Weights p_t
+ * below 2^-126 of a row's largest are zeros; scores have to be finite in fp32.
+ * Splits of 256 tokens at absolute positions, pages in order, splits folded in ascending order:
+ * a row's bits depend on its own length and slots only, and a prefill row
  * equals the decode row at its position bit for bit (they are not the bits of the bf16 store's
  * calls). Slots past a row's length are never folded in, whatever bytes and scales they hold;
  * a row that sees nothing (length 0, q_pos -1) yields zeros; a page id outside the store sets

@@ -2,32 +2,38 @@
 //
 // For a query row (one token, one head) with visible keys 0 .. L-1 of its sequence:
 //   s_t = scale q . (k_t sk_t),  out = sum_t e^(s_t) v_t sv_t / sum_t e^(s_t).
-// In the base-2 domain with z_t = s_t log2 e + log2 sv_t, any m and w_t = 2^(z_t - m):
-//   out = sum_t w_t v_t / sum_t (w_t / sv_t),
-// so the value scale rides in the exponent, the weights share one range however far apart the
-// rows' scales are, and both sums use the same w_t (an error of log2 sv_t is a common factor of
-// a token's two terms). m follows the running maximum of z lazily: it moves, to the maximum,
-// when that has risen by more than 8, so w_t <= 2^8 and most pages need neither a reduction
-// over lanes nor a rescaling of the sums.
+// In the base-2 domain with z_t = s_t log2 e, any m and any F > 0:
+//   p_t = 2^(z_t - m),  l = sum_t p_t,  w_t = p_t F sv_t,  out = sum_t w_t v_t / (F l).
+// m is the softmax's reference and follows the running maximum of z; F is the value product's and
+// follows 2^7 / max (p_t sv_t), so the largest weight is near 2^7 whatever the rows' scales are. The two
+// are apart because the token that carries the softmax and the one whose w is largest need not be the
+// same: with one reference over z_t + log2 sv_t (and l summing w_t / sv_t) a faint row's share of l
+// left fp32's range beside a loud row's w. Both follow lazily: they move, m to the maximum and F to
+// 2^7 over it, when a w passes 2^15 or a lane's l 2^24, so most pages need neither a reduction over
+// lanes nor a rescaling of the sums. Weights below 2^-126 of the row's largest p are zeros, and
+// so are weights whose p_t sv_t is below 2^-146 times that.
 //
 // The products run on mma.sync m16n8k16 (f16 operands, fp32 sums), keys and values as the
 // 16-row operand, 8 query rows as the other: scores^T = K Q^T, out^T = V^T W^T. Decode has 1 to
 // 16 query rows per kv-head, so this wastes the least of the MMA, and the operands come from
 // registers: the 8-bit bytes go from HBM to the lane that widens them. 8-bit keys and values
 // are exact in f16. A query row is brought to |q| < 2^15 by a power of two (exact but for dims
-// 2^28 below the row's largest, which lose bits below 2^-39 of it). 2^7 w_t <= 2^15 is rounded
-// to f16: half a step 2^-12 relative (finer than the bf16 output's 2^-9), and 2^-32 of the
-// largest weight for weights 2^-21 below it. All sums and the softmax statistics are fp32.
+// 2^28 below the row's largest, which lose bits below 2^-39 of it). w_t <= 2^15 is rounded
+// to f16: half a step 2^-11 relative (the bf16 output's is 2^-8), and 2^-32 of the largest for
+// weights 2^-21 below it. All sums and the softmax statistics are fp32.
 //
 // Per-row schedule (a function of the row's own L only, so decode, whole and chunked prefill,
 // and any batch give the same bits):
 //   * keys are cut into splits at absolute positions 0, 256, 512, ...; a split is folded page
 //     by page (16 tokens, one MMA k-step of weights x values);
-//   * s_t is one chain of D/16 MMAs, dims in a fixed order; lane t mod 8 sums w / sv over its two
+//   * s_t is one chain of D/16 MMAs, dims in a fixed order; lane t mod 8 sums p over its two
 //     tokens of each page in order, and the 8 lanes are added by an xor tree at the split's end;
-//   * whether m moves at a page depends on the row's own scores;
+//   * whether m and F move at a page, and to what, depends on the row's own scores and value scales;
+//   * a split ends with l brought into [1, 2) by a power of two that goes to m, and its sum of w v divided
+//     by F and multiplied by that power and 2^-h, h = 2 + ceil(log2(the row's splits)), which keeps the
+//     sum over splits below 2^127 for value rows of any size;
 //   * splits are folded in ascending order: M' = max(M, m_s), X = X 2^(M-M') + x_s 2^(m_s-M').
-// m and M are held as 7 - m, which is added to z for 2^7 w.
+// m and M are held as -m, which is added to z.
 // An MMA's output column depends on its own column of query rows only, so it does not matter
 // which rows share a tile. Tokens a row does not see get w = 0 exactly and stale value bytes are
 // replaced by zeros; rows that see nothing give zeros.
@@ -54,23 +60,20 @@ struct Cache {
   const int32_t* pt;
 };
 
-// 2^x with results below 2^-126 flushed to 0 (of 2^7 w: under 2^-133, where a row's largest w is at least 1).
+// 2^x with results below 2^-126 flushed to 0 (of a p: where the row's largest so far is at least 1).
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// Value scales lie in 2^-109 .. 2^121, so neither they nor their reciprocals are flushed.
+// 1 / x of a normal number (of a smaller one: infinity).
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// 2^e for e <= 127, and 2^-126 below that.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(max(e, -126) + 127) << 23); }
 
 // d += A B with A 16 x 16 (keys or values), B 16 x 8 (columns = query rows), f16 operands.
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
@@ -149,7 +152,9 @@ __device__ __forceinline__ void value_operands(const uint32_t (&x)[4], uint4& a,
   widen<KIND>(__byte_perm(x[2], x[3], 0x7362), b.z, b.w);
 }
 
-constexpr float kUnseen = 0x1p127f;  // 7 - m of a row that has seen nothing: m is below its scores
+constexpr float kUnseen = 0x1p127f;  // -m of a row that has seen nothing: m is below its scores
+constexpr float kMostL = 0x1p24f;    // a lane's l that moves the references
+constexpr float kMostF = 0x1p120f;
 
 // NT tiles of 8 query rows.
 template <int D, int NT>
@@ -191,16 +196,17 @@ __device__ __forceinline__ void load_query(Query<D, NT>& Q, int n, const uint16_
   }
 }
 
-// Running state of a split: per query row 7 - m (m the reference), 2^-9 sum w / sv over the lane's
-// tokens, and 2^7 sum w v over the lane's output dims (o[n][i]: dims 2i | 2i + 1 of rows 2c, 2c+1).
+// Running state of a split: per query row -m, F and the sum of p over the lane's tokens, and
+// sum w v over the lane's output dims (o[n][i]: dims 2i | 2i + 1 of rows 2c, 2c+1).
 template <int D, int NT>
 struct State {
-  float2 m[NT], l[NT];
+  float2 m[NT], f[NT], l[NT];
   float o[NT][D / 16][4];
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       m[n] = make_float2(kUnseen, kUnseen);
+      f[n] = make_float2(1.f, 1.f);
       l[n] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -212,18 +218,19 @@ struct State {
 
 // What the fold needs of the lane's tokens g and g + 8.
 struct Tokens {
-  float ks[2], lg[2], ri[2];  // key scale; log2 of the value scale, and 2^-16 over it
+  float ks[2], sv[2], z0[2];  // key and value scale; added to z: 0, or -infinity for a token on a page that is not there
 };
 
-// Weights of one page from its scores s (which become z): moves m (and l and o with it) where it
-// must, adds to l, and gives 2^7 w as the operand of the value product. masked (the same for the
+// Weights of one page from its scores s (which become z): moves m and F (and l and o with them) where
+// it must, adds to l, and gives w as the operand of the value product. masked (the same for the
 // whole warp): the lane's query row (n, r) sees the first nv(n, r) tokens only; otherwise all 16
 // are seen.
-// A row whose largest f16 weight exceeds 2^15 moves its reference to its largest score of the
-// page; weights are taken with the reference in hand first, which most pages keep.
+// The weights are taken with the references in hand first, which most pages keep. A row that has one
+// above 2^15, or an l above kMostL in some lane (infinite on the first page that it sees), moves m to its
+// largest score and F to what the page then asks for, if that is less than F already is.
 // There is one line of code through the accumulators, with small blocks beside it for what is
-// rare: with a second, masked form of the whole page the compiler joined two sets of
-// accumulators by register moves, which cost a third of the time of pages that never ran it.
+// rare: a second, masked form of the whole page beside the plain one was slower for pages that never
+// ran it (prefill of 4096 tokens 695 us against 635).
 template <int D, int NT, typename Nv>
 __device__ __forceinline__ void page_weights(const Query<D, NT>& Q, float (&s)[NT][4], const Tokens& T, bool masked, Nv nv,
                                              int g, State<D, NT>& S, uint32_t (&w)[NT][2]) {
@@ -232,7 +239,7 @@ __device__ __forceinline__ void page_weights(const Query<D, NT>& Q, float (&s)[N
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const float2 z = __ffma2_rn(make_float2(s[n][2 * t], s[n][2 * t + 1]), __fmul2_rn(make_float2(T.ks[t], T.ks[t]), Q.c[n]),
-                                  make_float2(T.lg[t], T.lg[t]));
+                                  make_float2(T.z0[t], T.z0[t]));
       s[n][2 * t] = z.x;
       s[n][2 * t + 1] = z.y;
     }
@@ -243,70 +250,89 @@ __device__ __forceinline__ void page_weights(const Query<D, NT>& Q, float (&s)[N
       for (int e = 0; e < 4; ++e)
         if (g + 8 * (e >> 1) >= nv(n, e & 1)) s[n][e] = -INFINITY;
   }
-  auto weight = [&](int n, int t) {  // pairs of query rows 2c, 2c + 1
+  auto prob = [&](int n, int t) {  // p of query rows 2c, 2c + 1
     const float2 x = __fadd2_rn(make_float2(s[n][2 * t], s[n][2 * t + 1]), S.m[n]);
     return make_float2(ex2(x.x), ex2(x.y));
   };
   float2 l[NT];
-  __half2 top;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
+  auto weigh = [&](int n) {  // w and l of tile n. (p F before sv: it stays in range where F sv need not)
     l[n] = S.l[n];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const float2 p = weight(n, t);
-      w[n][t] = pack_f16x2(p.x, p.y);
-      l[n] = __ffma2_rn(p, make_float2(T.ri[t], T.ri[t]), l[n]);
+      const float2 p = prob(n, t);
+      l[n] = __fadd2_rn(l[n], p);
+      const float2 x = __fmul2_rn(__fmul2_rn(p, S.f[n]), make_float2(T.sv[t], T.sv[t]));
+      w[n][t] = pack_f16x2(x.x, x.y);
     }
-    const __half2 most = __hmax2(*reinterpret_cast<__half2*>(&w[n][0]), *reinterpret_cast<__half2*>(&w[n][1]));
-    top = n ? __hmax2(top, most) : most;  // (a NaN is passed over: it moves no reference)
+  };
+  auto most = [&](int n) { return __hmax2(*reinterpret_cast<__half2*>(&w[n][0]), *reinterpret_cast<__half2*>(&w[n][1])); };
+  __half2 top;
+  float sums = 0.f;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    weigh(n);
+    top = n ? __hmax2(top, most(n)) : most(n);  // (a NaN is passed over, here and below: it moves nothing)
+    sums = fmaxf(sums, fmaxf(l[n].x, l[n].y));
   }
   const __half2 limit = __halves2half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800));  // 2^15
-  if (__any_sync(kFullMask, !__hble2(top, limit))) {
+  if (__any_sync(kFullMask, !__hble2(top, limit) || sums > kMostL)) {
+    const uint32_t rows = 0x11111111u << (threadIdx.x & 3);  // the lanes of rows 2c, 2c + 1
+    float to[NT][2], q[NT][2];                               // -m once moved, and the page's largest p sv then
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const __half2 most = __hmax2(*reinterpret_cast<__half2*>(&w[n][0]), *reinterpret_cast<__half2*>(&w[n][1]));
-      float pm[2] = {__low2float(most), __high2float(most)};
-      float mx[2] = {fmaxf(s[n][0], s[n][2]), fmaxf(s[n][1], s[n][3])};
-      float al[2];
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) to[n][r] = fmaxf(s[n][r], s[n][2 + r]);
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i) to[i / 2][i % 2] = fmaxf(to[i / 2][i % 2], __shfl_xor_sync(kFullMask, to[i / 2][i % 2], d));
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
+        to[n][r] = fminf(r ? S.m[n].y : S.m[n].x, -to[n][r]);
+        q[n][r] = fmaxf(__fmul_rn(ex2(__fadd_rn(s[n][r], to[n][r])), T.sv[0]),
+                        __fmul_rn(ex2(__fadd_rn(s[n][2 + r], to[n][r])), T.sv[1]));
+      }
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFullMask, mx[r], d));
-          pm[r] = fmaxf(pm[r], __shfl_xor_sync(kFullMask, pm[r], d));
-        }
+    for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i) q[i / 2][i % 2] = fmaxf(q[i / 2][i % 2], __shfl_xor_sync(kFullMask, q[i / 2][i % 2], d));
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const __half2 mine = most(n);
+      float al[2], ao[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const bool up = __ballot_sync(kFullMask, (r ? __high2float(mine) : __low2float(mine)) > 32768.f ||
+                                                     (r ? l[n].y : l[n].x) > kMostL) & rows;
         float& m = r ? S.m[n].y : S.m[n].x;
-        const bool up = pm[r] > 32768.f;
-        const float to = __fsub_rn(7.f, mx[r]);
-        al[r] = up ? ex2(__fsub_rn(to, m)) : 1.f;  // x * 1 == x: the other rows keep their bits
-        if (up) m = to;
+        float& f = r ? S.f[n].y : S.f[n].x;
+        // o keeps its meaning, 2^m o / F: by 2^(m_old - m) and F / F_old. x * 1 == x: other rows keep their bits
+        const float down = ex2(__fsub_rn(to[n][r], m));
+        const float ft = fminf(fminf(__fmul_rn(f, ex2(__fsub_rn(m, to[n][r]))), __fmul_rn(128.f, rcp(q[n][r]))), kMostF);
+        al[r] = up ? down : 1.f;
+        ao[r] = up ? __fmul_rn(__fmul_rn(down, ft), rcp(f)) : 1.f;
+        if (up) m = to[n][r], f = ft;
       }
       S.l[n] = __fmul2_rn(S.l[n], make_float2(al[0], al[1]));
-      l[n] = S.l[n];
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S.o[n][i][e] = __fmul_rn(S.o[n][i][e], al[e & 1]);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float2 p = weight(n, t);
-        w[n][t] = pack_f16x2(p.x, p.y);
-        l[n] = __ffma2_rn(p, make_float2(T.ri[t], T.ri[t]), l[n]);
-      }
+        for (int e = 0; e < 4; e += 2) {
+          const float2 o = __fmul2_rn(make_float2(S.o[n][i][e], S.o[n][i][e + 1]), make_float2(ao[0], ao[1]));
+          S.o[n][i][e] = o.x;
+          S.o[n][i][e + 1] = o.y;
+        }
+      weigh(n);
     }
   }
-  if (masked) {  // tokens that a row does not see add nothing to its l, whatever their scales
+  if (masked) {  // tokens that a row does not see have no weight, whatever their scales (their p is 0, w may be NaN)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      l[n] = S.l[n];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float2 p = weight(n, t);
-        if (g + 8 * t < nv(n, 0)) l[n].x = __fmaf_rn(p.x, T.ri[t], l[n].x);
-        if (g + 8 * t < nv(n, 1)) l[n].y = __fmaf_rn(p.y, T.ri[t], l[n].y);
-      }
-    }
+      for (int t = 0; t < 2; ++t)
+        w[n][t] &= (g + 8 * t < nv(n, 0) ? 0xFFFFu : 0u) | (g + 8 * t < nv(n, 1) ? 0xFFFF0000u : 0u);
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -316,13 +342,6 @@ __device__ __forceinline__ void page_weights(const Query<D, NT>& Q, float (&s)[N
   }
 }
 
-// 2^-16 / sv: what a token adds to l per 2^7 w. Unscaled, l would pass the fp32 range for long rows whose
-// values are all near 2^-100; scaled, 2^15 w / sv sums up to 2^19 such tokens, and the reciprocals of
-// scales above 2^110 keep 12 bits or more (fp32 subnormals).
-__device__ __forceinline__ float weight_per_scale(float vs) { return __fmul_rn(rcp(vs), 0x1p-16f); }
-// The output of a row from its sums of w v and of weight_per_scale w.
-__device__ __forceinline__ float row_out(float o, float l) { return l == 0.f ? 0.f : __fdiv_rn(__fmul_rn(o, 0x1p-16f), l); }
-
 // The xor tree over a query row's 8 lanes that ends a split.
 __device__ __forceinline__ float row_sum(float l) {
 #pragma unroll
@@ -330,7 +349,30 @@ __device__ __forceinline__ float row_sum(float l) {
   return l;
 }
 
-// One step of the fold over splits: 7 - M and a split's 7 - m -> the factors of both sides.
+// h of a row of n splits.
+__device__ __forceinline__ int headroom(int n) { return 34 - __clz(n - 1); }
+
+// The end of a split for query row (n, r), of a row of `splits` splits: -m and l as the fold over splits
+// takes them, and the factor that its sums of w v are multiplied by (fp32 subnormal, with 18 bits or
+// more, where all its p sv are below 2^-90 or so).
+struct SplitEnd {
+  float m, l, c;
+  __device__ __forceinline__ float value(float o) const { return __fmul_rn(o, c); }
+};
+template <int D, int NT>
+__device__ __forceinline__ SplitEnd split_end(const State<D, NT>& S, int n, int r, int splits) {
+  const float l = row_sum(r ? S.l[n].y : S.l[n].x);
+  const int e = (int)(__float_as_uint(l) >> 23) - 127;  // l = 0: -127, which changes neither l nor kUnseen
+  return {__fsub_rn(r ? S.m[n].y : S.m[n].x, (float)e), __fmul_rn(l, pow2(-e)),
+          __fmul_rn(pow2(-e - headroom(splits)), rcp(r ? S.f[n].y : S.f[n].x))};
+}
+
+// The output of a row of n splits from its folded sums.
+__device__ __forceinline__ float row_out(float o, float l, int n) {
+  return l == 0.f ? 0.f : __fmul_rn(__fdiv_rn(o, l), pow2(headroom(n)));
+}
+
+// One step of the fold over splits: -M and a split's -m -> the factors of both sides.
 __device__ __forceinline__ void join(float& M, float m, float& a, float& b) {
   const float mn = fminf(M, m);
   a = ex2(__fsub_rn(mn, M));
@@ -384,10 +426,9 @@ __device__ __forceinline__ void fold_page(const Query<D, NT>& Q, float (&s)[NT][
   Tokens T;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const float vs = ld_shared_f32(scales + 64 + 4 * g + 32 * t);
     T.ks[t] = ld_shared_f32(scales + 4 * g + 32 * t);
-    T.lg[t] = lg2(vs);
-    T.ri[t] = weight_per_scale(vs);
+    T.sv[t] = ld_shared_f32(scales + 64 + 4 * g + 32 * t);
+    T.z0[t] = 0.f;
   }
   uint32_t w[NT][2];
   page_weights<D, NT>(Q, s, T, masked, nv, g, S, w);
@@ -467,9 +508,9 @@ inline bool make_page_map(CUtensorMap* map, const void* ptr, int64_t rows) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A work item: split s of row r for one kv-head; `page` is page `lane` of it (-1: unusable).
+// A work item: split s of row r (of `splits`) for one kv-head; `page` is page `lane` of it (-1: unusable).
 struct Item {
-  int r, s, kh, seen, page;
+  int r, s, kh, seen, page, splits;
 };
 
 template <int KIND, int D, int NT, int W>
@@ -546,6 +587,7 @@ __global__ void __launch_bounds__(W * 32, kSmWarps<D, NT> / W)
     int pt_row;
     const int len = attn::row_len(R, I.r, pt_row);
     I.seen = min(SPLIT, len - I.s * SPLIT);
+    I.splits = (len + SPLIT - 1) / SPLIT;
     I.page = -1;
     if (lane * PAGE < I.seen) {
       const int pg = C.pt[(int64_t)pt_row * R.max_pages + I.s * PAGES_PER_SPLIT + lane];
@@ -638,16 +680,16 @@ __global__ void __launch_bounds__(W * 32, kSmWarps<D, NT> / W)
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float l = row_sum(r ? S.l[n].y : S.l[n].x);
+        const SplitEnd E = split_end(S, n, r, cur.splits);
         const int head = 8 * n + 2 * c + r;
         if (head >= G) continue;
         const int64_t slot = ((int64_t)cur.r * max_splits + cur.s) * Hq + cur.kh * G + head;
         float* dst = po + slot * D + (D / 8) * g;
 #pragma unroll
         for (int i = 0; i < D / 16; i += 2)
-          *reinterpret_cast<float4*>(dst + 2 * i) =
-              make_float4(S.o[n][i][r], S.o[n][i][2 + r], S.o[n][i + 1][r], S.o[n][i + 1][2 + r]);
-        if (g == 0) pml[slot] = make_float2(r ? S.m[n].y : S.m[n].x, l);
+          *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(E.value(S.o[n][i][r]), E.value(S.o[n][i][2 + r]),
+                                                                E.value(S.o[n][i + 1][r]), E.value(S.o[n][i + 1][2 + r]));
+        if (g == 0) pml[slot] = make_float2(E.m, E.l);
       }
     if (item + step >= total) break;
     item += step;
@@ -663,7 +705,7 @@ __global__ void __launch_bounds__(W * 32, kSmWarps<D, NT> / W)
 }
 
 // Folds a row's splits in ascending order; one warp per (row, query head, 32 * DPL output dims).
-// The lanes take the splits' 7 - m 32 at a time: the running minimum before and after each
+// The lanes take the splits' -m 32 at a time: the running minimum before and after each
 // split (a minimum is exact in any order) gives the weights of both sides of its fold step, and
 // the fold itself is one chain per output dim in split order whatever DPL is. The partial
 // outputs come U at a time, the next U and the next 32 references asked for before these are folded.
@@ -746,7 +788,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
   }
   float y[DPL];
 #pragma unroll
-  for (int d = 0; d < DPL; ++d) y[d] = row_out(O[d], L);
+  for (int d = 0; d < DPL; ++d) y[d] = row_out(O[d], L, n);
   uint16_t* dst = out + rh * D + d0;
   if constexpr (DPL == 1) {
     *dst = to_bf16_bits(y[0]);
@@ -914,12 +956,12 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
 
 // Writes a query row's dims (D/8) g .. + D/8 - 1.
 template <int D>
-__device__ __forceinline__ void store_row(uint16_t* dst, const float (&x)[D / 8], float L) {
+__device__ __forceinline__ void store_row(uint16_t* dst, const float (&x)[D / 8], float L, int splits) {
 #pragma unroll
   for (int i = 0; i < D / 8; i += 8) {
     float y[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) y[u] = row_out(x[i + u], L);
+    for (int u = 0; u < 8; ++u) y[u] = row_out(x[i + u], L, splits);
     *reinterpret_cast<uint4*>(dst + i) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
                                                     pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
   }
@@ -946,7 +988,7 @@ struct TileSmem {
   using P = TileShape<D>;
   static constexpr int PAGES = 256 / D;                      // pages a stage: one part of each kind per widening warp
   static constexpr int OPERANDS = PAGES * 2 * PAGE * D * 2;  // f16 keys, then values
-  static constexpr int STAGE = OPERANDS + PAGES * PAGE * 16;  // and {ks, log2 vs, 2^-16 / vs, -} per token
+  static constexpr int STAGE = OPERANDS + PAGES * PAGE * 16;  // and {ks, vs, z0, -} per token
   static constexpr int TOTALS = kRing * STAGE;               // fp32 totals [row][D], lane by lane
   static constexpr int STATS = TOTALS + P::ROWS * D * 4;     // M and L, lane by lane
   static constexpr int LENS = STATS + P::FOLD * 32 * P::NT * 16;  // visible lengths, lane by lane
@@ -1001,7 +1043,7 @@ __device__ __forceinline__ void load_raw(Raw& X, const Cache& C, const int32_t* 
 }
 
 // Widens a loaded part into a stage: keys [page][step][lane], values [page][tile][lane], tokens. A
-// token without a value scale (0) has log2 -infinity: no weight.
+// token without a value scale (0) has no weight.
 template <int KIND, int D>
 __device__ __forceinline__ void widen_raw(const Raw& X, uint32_t stage, int warp, int lane) {
   using M = TileSmem<D>;
@@ -1022,7 +1064,7 @@ __device__ __forceinline__ void widen_raw(const Raw& X, uint32_t stage, int warp
     st_shared_v4(vb + (2 * u + 1) * 512, b);
   }
   if (warp * 32 < M::PAGES * PAGE) {
-    const float4 t = make_float4(X.ks, lg2(X.vs), X.vs == 0.f ? 0.f : weight_per_scale(X.vs), 0.f);
+    const float4 t = make_float4(X.ks, X.vs, X.vs == 0.f ? -INFINITY : 0.f, 0.f);
     st_shared_v4(stage + M::OPERANDS + (warp * 32 + lane) * 16, *reinterpret_cast<const uint4*>(&t));
   }
 }
@@ -1061,8 +1103,8 @@ __device__ __forceinline__ Tokens wide_tokens(uint32_t buf, int page, int lane) 
   for (int t = 0; t < 2; ++t) {
     const uint4 x = ld_shared_v4(buf + TileSmem<D>::OPERANDS + (page * PAGE + (lane >> 2) + 8 * t) * 16);
     T.ks[t] = __uint_as_float(x.x);
-    T.lg[t] = __uint_as_float(x.y);
-    T.ri[t] = __uint_as_float(x.z);
+    T.sv[t] = __uint_as_float(x.y);
+    T.z0[t] = __uint_as_float(x.z);
   }
   return T;
 }
@@ -1172,18 +1214,22 @@ __device__ __forceinline__ void fold_tile(const TileArgs& A, uint8_t* smem, uint
     for (int n = 0; n < LIVE; ++n) {
       float4 st = stats[32 * n];
       float a0, b0, a1, b1;
-      const float l0 = row_sum(S.l[n].x), l1 = row_sum(S.l[n].y);
-      join(st.x, S.m[n].x, a0, b0);
-      join(st.y, S.m[n].y, a1, b1);
-      st.z = __fmaf_rn(l0, b0, __fmul_rn(st.z, a0));
-      st.w = __fmaf_rn(l1, b1, __fmul_rn(st.w, a1));
+      const int2 len = lens[32 * n];
+      const SplitEnd E0 = split_end(S, n, 0, (len.x + SPLIT - 1) / SPLIT), E1 = split_end(S, n, 1, (len.y + SPLIT - 1) / SPLIT);
+      join(st.x, E0.m, a0, b0);
+      join(st.y, E1.m, a1, b1);
+      st.z = __fmaf_rn(E0.l, b0, __fmul_rn(st.z, a0));
+      st.w = __fmaf_rn(E1.l, b1, __fmul_rn(st.w, a1));
       stats[32 * n] = st;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float* x = tot + 32 * ((n * 2 + (e & 1)) * (D / 8) + 2 * i + (e >> 1));
-          *x = __fmaf_rn(S.o[n][i][e], e & 1 ? b1 : b0, __fmul_rn(*x, e & 1 ? a1 : a0));
+        for (int e = 0; e < 2; ++e) {
+          float* x = tot + 32 * (n * 2 * (D / 8) + 2 * i + e);  // and of row 2c + 1 at [32 (D / 8)]
+          const float2 v = __fmul2_rn(make_float2(S.o[n][i][2 * e], S.o[n][i][2 * e + 1]), make_float2(E0.c, E1.c));
+          const float2 y = __ffma2_rn(v, make_float2(b0, b1), __fmul2_rn(make_float2(x[0], x[32 * (D / 8)]), make_float2(a0, a1)));
+          x[0] = y.x;
+          x[32 * (D / 8)] = y.y;
         }
     }
   }
@@ -1197,7 +1243,9 @@ __device__ __forceinline__ void fold_tile(const TileArgs& A, uint8_t* smem, uint
       float x[D / 8];
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) x[i] = tot[32 * ((n * 2 + r) * (D / 8) + i)];
-      store_row<D>(A.out + ((int64_t)(A.first + k / A.G) * A.Hq + A.kh * A.G + k % A.G) * D + (D / 8) * g, x, r ? st.w : st.z);
+      const int len = r ? lens[32 * n].y : lens[32 * n].x;
+      store_row<D>(A.out + ((int64_t)(A.first + k / A.G) * A.Hq + A.kh * A.G + k % A.G) * D + (D / 8) * g, x, r ? st.w : st.z,
+                   (len + SPLIT - 1) / SPLIT);
     }
 }
 
@@ -1389,15 +1437,15 @@ __device__ __forceinline__ void few_tile(const uint16_t* __restrict__ q, int64_t
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float l = row_sum(r ? S.l[n].y : S.l[n].x);
+          const SplitEnd E = split_end(S, n, r, (len[n][r] + SPLIT - 1) / SPLIT);
           const int k = 8 * n + 2 * c + r;
           if (k >= rows) continue;
           float* dst = part + (warp * kFewRows + k) * D + (D / 8) * g;
 #pragma unroll
           for (int i = 0; i < D / 16; i += 2)
-            *reinterpret_cast<float4*>(dst + 2 * i) =
-                make_float4(S.o[n][i][r], S.o[n][i][2 + r], S.o[n][i + 1][r], S.o[n][i + 1][2 + r]);
-          if (g == 0) pml[warp * kFewRows + k] = make_float2(r ? S.m[n].y : S.m[n].x, l);
+            *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(E.value(S.o[n][i][r]), E.value(S.o[n][i][2 + r]),
+                                                                  E.value(S.o[n][i + 1][r]), E.value(S.o[n][i + 1][2 + r]));
+          if (g == 0) pml[warp * kFewRows + k] = make_float2(E.m, E.l);
         }
     }
     sync();
@@ -1446,8 +1494,10 @@ __device__ __forceinline__ void few_tile(const uint16_t* __restrict__ q, int64_t
   __syncthreads();
   if (frow < rows) {
     uint16_t* dst = out + ((int64_t)(first + frow / G) * Hq + kh * G + frow % G) * D;
+    const int splits = attn::num_splits(R, first + frow / G);
     for (int d = fd; d < fd + dims; d += 2)
-      *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16x2(row_out(tot[frow * D + d], FL), row_out(tot[frow * D + d + 1], FL));
+      *reinterpret_cast<uint32_t*>(dst + d) =
+          pack_bf16x2(row_out(tot[frow * D + d], FL, splits), row_out(tot[frow * D + d + 1], FL, splits));
   }
 }
 
