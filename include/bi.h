@@ -295,8 +295,8 @@ bi_status bi_kv_read_q8(bi_bf16* k_out, bi_bf16* v_out, int64_t ld_out, const in
  * above in place of the bf16 one. Keys and values are the exact v * s; with
  * z_t = scale log2(e) q.(k_t sk_t), p_t = 2^(z_t - m) and w_t = p_t F sv_t,
  *   out = sum_t w_t v_t / (F sum_t p_t)    (= softmax(scale q.k) v for any m and F),
- * m following the running maximum of z and F that of 2^7 / (p sv) (they move when a w_t passes
- * 2^15). The products run on tensor cores in f16 with fp32 sums (8-bit values are exact in f16;
+ * m following the running maximum of z and F 2^7 over that of p sv, value rows of zeros passed
+ * over (they move when a w_t passes 2^15). The products run on tensor cores in f16 with fp32 sums (8-bit values are exact in f16;
  * a query row is scaled by a power of two; w_t is rounded to f16: 2^-11 relative, and 2^-32 of
  * the largest w for the faintest), everything else in fp32, one rounding to bf16. Weights p_t
  * below 2^-126 of a row's largest are zeros; scores have to be finite in fp32.

@@ -10,7 +10,9 @@
 // same: with one reference over z_t + log2 sv_t (and l summing w_t / sv_t) a faint row's share of l
 // left fp32's range beside a loud row's w. Both follow lazily: they move, m to the maximum and F to
 // 2^7 over it, when a w passes 2^15 or a lane's l 2^24, so most pages need neither a reduction over
-// lanes nor a rescaling of the sums. Weights below 2^-126 of the row's largest p are zeros, and
+// lanes nor a rescaling of the sums. A value row of zeros is stored with scale 1 and gives nothing to the
+// value product: F passes it over (kNoScale), else a null token that holds much of the weight would
+// leave the other rows' weights f16's last bits. Weights below 2^-126 of the row's largest p are zeros, and
 // so are weights whose p_t sv_t is below 2^-146 times that.
 //
 // The products run on mma.sync m16n8k16 (f16 operands, fp32 sums), keys and values as the
@@ -155,6 +157,7 @@ __device__ __forceinline__ void value_operands(const uint32_t (&x)[4], uint4& a,
 constexpr float kUnseen = 0x1p127f;  // -m of a row that has seen nothing: m is below its scores
 constexpr float kMostL = 0x1p24f;    // a lane's l that moves the references
 constexpr float kMostF = 0x1p120f;
+constexpr float kNoScale = 0x1p-149f;  // value scale of a row of zeros, where F is found and after
 
 // NT tiles of 8 query rows.
 template <int D, int NT>
@@ -227,13 +230,15 @@ struct Tokens {
 // are seen.
 // The weights are taken with the references in hand first, which most pages keep. A row that has one
 // above 2^15, or an l above kMostL in some lane (infinite on the first page that it sees), moves m to its
-// largest score and F to what the page then asks for, if that is less than F already is.
+// largest score and F to what the page then asks for, if that is less than F already is. Rows of zeros
+// are found here: elsewhere their weights, 2^15 at most, meet zeros. set_tokens() gives the tokens
+// (bit i: token i) whose value rows are not zeros.
 // There is one line of code through the accumulators, with small blocks beside it for what is
 // rare: a second, masked form of the whole page beside the plain one was slower for pages that never
 // ran it (prefill of 4096 tokens 695 us against 635).
-template <int D, int NT, typename Nv>
-__device__ __forceinline__ void page_weights(const Query<D, NT>& Q, float (&s)[NT][4], const Tokens& T, bool masked, Nv nv,
-                                             int g, State<D, NT>& S, uint32_t (&w)[NT][2]) {
+template <int D, int NT, typename Nv, typename Set>
+__device__ __forceinline__ void page_weights(const Query<D, NT>& Q, float (&s)[NT][4], Tokens T, bool masked, Nv nv,
+                                             Set set_tokens, int g, State<D, NT>& S, uint32_t (&w)[NT][2]) {
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -276,6 +281,12 @@ __device__ __forceinline__ void page_weights(const Query<D, NT>& Q, float (&s)[N
   }
   const __half2 limit = __halves2half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800));  // 2^15
   if (__any_sync(kFullMask, !__hble2(top, limit) || sums > kMostL)) {
+    if (__any_sync(kFullMask, T.sv[0] == 1.f || T.sv[1] == 1.f)) {  // the scale of a row of zeros, and of few others
+      const uint32_t set = set_tokens();
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (T.sv[t] == 1.f && !(set >> (g + 8 * t) & 1u)) T.sv[t] = kNoScale;
+    }
     const uint32_t rows = 0x11111111u << (threadIdx.x & 3);  // the lanes of rows 2c, 2c + 1
     float to[NT][2], q[NT][2];                               // -m once moved, and the page's largest p sv then
 #pragma unroll
@@ -431,7 +442,21 @@ __device__ __forceinline__ void fold_page(const Query<D, NT>& Q, float (&s)[NT][
     T.z0[t] = 0.f;
   }
   uint32_t w[NT][2];
-  page_weights<D, NT>(Q, s, T, masked, nv, g, S, w);
+  auto set_tokens = [&] {  // lane c of four ORs its quarter of the rows of tokens g and g + 8
+    uint32_t mine = 0;
+#pragma unroll
+    for (int t = 0; t < 16; t += 8) {
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const uint4 y = ld_shared_v4(page + PAGE * D + chunk_at<D>(g + t, c * (D / 64) + i));
+        any |= y.x | y.y | y.z | y.w;
+      }
+      if (any) mine |= 1u << (g + t);
+    }
+    return __reduce_or_sync(kFullMask, mine);
+  };
+  page_weights<D, NT>(Q, s, T, masked, nv, set_tokens, g, S, w);
   uint32_t x[4][D / 32];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -1128,7 +1153,18 @@ __device__ __forceinline__ void fold_wide(const Query<D, LIVE>& Q, uint32_t stag
   wide_scores<D, LIVE>(Q, stage, third, page, lane, s);
   const Tokens T = wide_tokens<D>(stage, page, lane);
   uint32_t w[LIVE][2];
-  page_weights<D, LIVE>(Q, s, T, masked, nv, lane >> 2, S, w);
+  auto set_tokens = [&] {  // the lane ORs its dims of tokens 2c, 2c + 1, 2c + 8, 2c + 9, as f16 pairs
+    const uint32_t vb = stage + TileSmem<D>::OPERANDS / 2 + (page * (D / 16) * 32 + lane) * 16;
+    uint32_t lo = 0, hi = 0;
+    for (int i = 0; i < D / 16; ++i) {
+      const uint4 y = ld_shared_v4(vb + i * 512);
+      lo |= y.x | y.y;
+      hi |= y.z | y.w;
+    }
+    const uint32_t mine = (lo & 0xFFFFu ? 1u : 0u) | (lo >> 16 ? 2u : 0u) | (hi & 0xFFFFu ? 0x100u : 0u) | (hi >> 16 ? 0x200u : 0u);
+    return __reduce_or_sync(kFullMask, mine << (2 * (lane & 3)));
+  };
+  page_weights<D, LIVE>(Q, s, T, masked, nv, set_tokens, lane >> 2, S, w);
   wide_values<D, LIVE>(stage, page, lane, w, S);
 }
 

@@ -1,6 +1,7 @@
-"""Attention over the 8-bit store where value rows differ widely in size: the softmax's
-denominator keeps every token that carries weight, whatever its value scale, and each form of
-the calls (decode, wide tiles, few rows, clusters) gives the same bits."""
+"""Attention over the 8-bit store where value rows differ widely in size, or are zeros: the
+softmax's denominator keeps every token that carries weight, whatever its value scale, the other
+rows' weights keep their bits, and each form of the calls (decode, wide tiles, few rows,
+clusters) gives the same bits."""
 import numpy as np
 import pytest
 import torch
@@ -111,3 +112,107 @@ def test_scores_and_sizes_that_rise_and_fall_together(kind):
         z = up * 3.0 * page.float() - 48.0
         v = synth.normal_bf16((n, 2, D), 802).float() * torch.exp2(-up * 4.0 * (page.float() - 16))[:, None, None]
         check_all_forms(kind, scored(z, 2, D), v, first_axis(6, D), LN2)
+
+
+def zero_score(p, n):
+    """The base-2 score at which one token holds the share p beside n - 1 tokens of score 0."""
+    return float(np.log2(p / (1 - p) * (n - 1)))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [0.1, 0.02, 1e-4, 2.0 ** -60, 2.0 ** 60])
+@pytest.mark.parametrize("p", [0.5, 0.99, 0.9999])
+@pytest.mark.parametrize("at,D", [([0], 128), ([1023], 64), ([300, 301, 777], 128), (list(range(512, 528)), 64)])
+def test_zero_value_rows_with_most_of_the_weight(kind, size, p, at, D):
+    """A null token or a sink: rows of zeros take p of the softmax from the first, a middle and the last
+    place, and as a page of their own; what the other rows give must not lose bits to them."""
+    n = 1024
+    z = torch.linspace(-2, 2, n)
+    z[at] = zero_score(p, n) - float(np.log2(len(at)))
+    v = synth.normal_bf16((n, 2, D), 810).float() * size
+    v[at] = 0
+    check_all_forms(kind, scored(z, 2, D), v, first_axis(8, D), LN2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [1e-7, 1e-8, 2.0 ** -97])
+def test_small_values_beside_zero_rows_of_equal_weight(kind, size):
+    n, D = 256, 128
+    v = synth.normal_bf16((n, 1, D), 811).float().clamp(-4, 4) * size
+    v[100] = 0
+    check_all_forms(kind, scored(torch.zeros(n), 1, D), v, first_axis(3, D), LN2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_nothing_but_zero_value_rows(kind):
+    n, D = 300, 64
+    S, _ = fill(kind, [n], 2, D, 20, seed=901, v=torch.zeros(n, 2, D, dtype=torch.bfloat16))
+    q = synth.normal_bf16((1, 6, D), 812).to(dev())
+    dec = bi.attention_decode_q8(q, *S.args, torch.tensor([n], dtype=torch.int32, device=dev()))
+    assert bool((dec == 0).all())
+    pre = bi.attention_prefill_q8(q.repeat(40, 1, 1), torch.zeros(40, dtype=torch.int32, device=dev()),
+                                  torch.arange(n - 40, n, dtype=torch.int32, device=dev()), *S.args)
+    assert bool((pre == 0).all()) and bi.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind,one", [("int8", 127.0), ("e4m3", 448.0), ("e4m3", 225.0)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_whose_scale_is_one_are_not_taken_for_zero_rows(kind, one, D):
+    """A row with the scale of an empty one, 1, and a single value that is not zero, in each eighth of the
+    row; beside rows of zeros, with the weight spread evenly."""
+    n = 40
+    v = torch.zeros(n, 2, D)
+    for i, d in enumerate(range(0, D, D // 8)):
+        v[3 + 2 * i, 0, d + i % (D // 8)] = -one if i % 2 else one
+        v[4 + 2 * i, 1, D - 1 - d] = one
+    v[30:, :, :] = 1e-3 * synth.normal_bf16((10, 2, D), 813).float()
+    check_all_forms(kind, scored(torch.linspace(-1, 1, n), 2, D), v, first_axis(4, D), LN2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 118, 2.0 ** -92])
+def test_the_least_row_that_is_kept_beside_others(kind, size):
+    """A row whose largest value is 2^-100 is no zero row; it holds most of the weight here."""
+    n, D = 200, 64
+    z = torch.zeros(n)
+    z[33] = zero_score(0.999, n)
+    v = synth.normal_bf16((n, 1, D), 814).float().clamp(-4, 4) * size
+    v[33] = 2.0 ** -100
+    check_all_forms(kind, scored(z, 1, D), v, first_axis(4, D), LN2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_weights_beside_a_zero_row(kind, D):
+    """32768 weights of 2^-20.5 on rows near 2^-96 beside one of 1 on a row below 2^-100, which is empty."""
+    n = 32769
+    z = torch.full((n,), -20.5)
+    z[17] = 0.0
+    v = synth.normal_bf16((n, 1, D), 801).float().abs().clamp(0.5, 2.0) * 2.0 ** -96
+    v[17] *= -(2.0 ** -8)
+    check_all_forms(kind, scored(z, 1, D), v, first_axis(8, D), LN2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 128), (8, 1, 64), (16, 1, 128)])
+def test_prompts_over_mixed_value_rows_have_the_decode_bits(kind, Hq, Hkv, D):
+    """Value rows of 2^-40 to 2^40, every fifth one zeros, and one with a NaN that later rows see: a
+    whole prompt, whose tiles mix rows that see such tokens with rows that do not, against decode."""
+    n = 700
+    g = torch.Generator().manual_seed(820)
+    v = synth.normal_bf16((n, Hkv, D), 821).float() * torch.exp2(torch.randint(-40, 41, (n, Hkv, 1), generator=g).float())
+    v[torch.rand(n, Hkv, generator=g) < 0.2] = 0
+    v[649, 0, 3] = float("nan")
+    S, pt = fill(kind, [n], Hkv, D, 60, seed=902, v=v.bfloat16())
+    q = synth.normal_bf16((n, Hq, D), 822).to(dev())
+    seq, pos = torch.zeros(n, dtype=torch.int32, device=dev()), torch.arange(n, dtype=torch.int32, device=dev())
+    pre = bi.attention_prefill_q8(q, seq, pos, *S.args)
+    dec = bi.attention_decode_q8(q, *S.args[:4], S.pt.expand(n, -1).contiguous(), pos + 1)
+    assert same_bits(pre, dec) and bi.get_device_error() == 0
+    assert bool(torch.isnan(dec[649:, : Hq // Hkv]).all()) and not bool(torch.isnan(dec[:649]).any())
+    pages = pt[0, : -(-n // 16)].tolist()
+    k64, v64, sv = S.values("k", pages, n), S.values("v", pages, n), S.value_scales(pages, n)
+    for t in (0, 16, 255, 256, 600, 648):
+        ref, tol = attend(q[t].cpu().double().numpy(), k64[:, : t + 1], v64[:, : t + 1], sv[:, : t + 1], D ** -0.5)
+        err = np.abs(dec[t].cpu().double().numpy() - ref)
+        assert (err <= tol).all(), (t, float((err / tol).max()))
