@@ -868,7 +868,13 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
   const int each = (T + 1023) / 1024;
   const int r0 = (int)min((int64_t)tid * each, (int64_t)T), r1 = min(r0 + each, T);
   auto starts = [&](int r) { return r == 0 || q_seq[r] != q_seq[r - 1]; };
-  auto is_few = [&](int r) { return per == few || r + few >= T || q_seq[r + few] != q_seq[r]; };
+  // (every row up to r + few: with rows of sequences in turn, that one alone may be of the same sequence)
+  auto is_few = [&](int r) {
+    bool ends = per == few || r + few >= T;
+    const int seq = q_seq[r];
+    for (int i = 1; i <= few && !ends; ++i) ends = q_seq[r + i] != seq;
+    return ends;
+  };
   // the start of the run that row r0 - 1 lies in: the running maximum of run starts before this thread
   int last = -1;
   for (int r = r0; r < r1; ++r)
