@@ -144,3 +144,53 @@ def test_qk_norm_rope_of_many_rows(Hq, Hkv, D, in_place):
         # one rounding to bf16 (2^-8 of y), fp32 before it: 16 + 4 sums and 5 products, 2^-19 of the terms
         err = np.abs(got[one].cpu().double().numpy() - y)
         assert (err <= 2.0 ** -8 * np.abs(y) + 2.0 ** -19 * mag).all()
+
+
+def test_captured_clusters_and_large_decode_replay_with_the_eager_bits():
+    """Few rows of long contexts (clusters of CTAs) and a decode of more than two rounds of splits in one
+    captured graph, replayed on changed queries and lengths, beside a second graph on another stream."""
+    Hq, Hkv, D, B, max_pages = 16, 2, 128, 40, 1600
+    lens = [9000, 1, 0, 4000] + [300 + 7 * i for i in range(B - 4)]
+
+    class Side:
+        def __init__(self, seed, kind):
+            self.S, _ = fill(kind, lens, Hkv, D, max_pages, seed=seed)
+            self.n = torch.tensor(lens, dtype=torch.int32, device=dev())
+            self.q = synth.normal_bf16((B, Hq, D), seed).to(dev())
+            self.few = synth.normal_bf16((6, Hq, D), seed + 1).to(dev())
+            self.seq = torch.tensor([0, 0, 0, 3, 1, 2], dtype=torch.int32, device=dev())
+            self.pos = torch.tensor([8997, 8998, 8999, 3999, 0, -1], dtype=torch.int32, device=dev())
+
+        def step(self):
+            return (bi.attention_decode_q8(self.q, *self.S.args, self.n),
+                    bi.attention_prefill_q8(self.few, self.seq, self.pos, *self.S.args))
+
+    sides, streams = [Side(550, "int8"), Side(560, "e4m3")], [torch.cuda.Stream(), torch.cuda.Stream()]
+    graphs = []
+    for s in sides:
+        s.step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.out = s.step()
+        graphs.append(g)
+    for rnd in range(3):
+        for i, s in enumerate(sides):
+            s.q.copy_(synth.normal_bf16((B, Hq, D), 570 + 2 * rnd + i).to(dev()))
+            s.few.copy_(synth.normal_bf16((6, Hq, D), 580 + 2 * rnd + i).to(dev()))
+            s.n[4:] -= 40
+            s.pos[:4] -= 300 * rnd
+            for t in s.out:
+                t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+                g.replay()
+        torch.cuda.synchronize()
+        for s in sides:
+            dec, pre = s.step()
+            assert same_bits(s.out[0], dec) and same_bits(s.out[1], pre)
+    assert bi.get_device_error() == 0
+    for g in graphs:
+        g.reset()
