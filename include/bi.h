@@ -296,17 +296,17 @@ bi_status bi_kv_read_q8(bi_bf16* k_out, bi_bf16* v_out, int64_t ld_out, const in
  * z_t = scale log2(e) q.(k_t sk_t), p_t = 2^(z_t - m) and w_t = p_t F sv_t,
  *   out = sum_t w_t v_t / (F sum_t p_t)    (= softmax(scale q.k) v for any m and F),
  * m following the running maximum of z and F 2^7 over that of p sv, value rows of zeros passed
- * over (they move when a w_t passes 2^15). The products run on tensor cores in f16 with fp32 sums (8-bit values are exact in f16;
- * a query row is scaled by a power of two; w_t is rounded to f16: 2^-11 relative, and 2^-32 of
- * the largest w for the faintest), everything else in fp32, one rounding to bf16. Weights p_t
- * below 2^-126 of a row's largest are zeros; scores have to be finite in fp32.
- * Splits of 256 tokens at absolute positions, pages in order, splits folded in ascending order:
- * a row's bits depend on its own length and slots only, and a prefill row
- * equals the decode row at its position bit for bit (they are not the bits of the bf16 store's
- * calls). Slots past a row's length are never folded in, whatever bytes and scales they hold;
- * a row that sees nothing (length 0, q_pos -1) yields zeros; a page id outside the store sets
- * the device error word and its tokens are not seen. Every slot that a row sees was written by
- * bi_kv_append_q8 (its scale is a positive normal number, or NaN, which gives NaN).
+ * over (they move when a w_t passes 2^15). The products run on tensor cores in f16 with fp32
+ * sums (8-bit values are exact in f16; a query row is scaled by a power of two; w_t is rounded
+ * to f16: 2^-11 relative, and 2^-32 of the largest w for the faintest), everything else in
+ * fp32, one rounding to bf16. Weights p_t below 2^-126 of a row's largest are zeros; scores
+ * have to be finite in fp32. Splits of 256 tokens at absolute positions, pages in order, splits
+ * folded in ascending order: a row's bits depend on its own length and slots only, and a
+ * prefill row equals the decode row at its position bit for bit (they are not the bits of the
+ * bf16 store's calls). Slots past a row's length are never folded in, whatever bytes and scales
+ * they hold; a row that sees nothing (length 0, q_pos -1) yields zeros; a page id outside the
+ * store sets the device error word and its tokens are not seen. Every slot that a row sees was
+ * written by bi_kv_append_q8 (its scale is a positive normal number, or NaN, which gives NaN).
  * Hq % Hkv == 0 and Hq / Hkv in 1..16; D in {64, 128}. out must not overlap q.
  * bi_attention_decode_q8: workspace >= bi_attention_workspace_size(B, Hq, D, max_pages).
  * bi_attention_prefill_q8: q's rows ldq apart; rows of one sequence that follow one another

@@ -532,9 +532,9 @@ def kv_append_q8(k_new, v_new, q_seq, q_pos, k_cache, v_cache, k_scale, v_scale,
         return
     with _launch_on(device, stream):
         _check("bi_kv_append_q8", lib().bi_kv_append_q8(
-            k_new.data_ptr(), v_new.data_ptr(), ld, q_seq.data_ptr(), q_pos.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), kind, num_pages, page_table.data_ptr(), page_table.shape[0], page_table.shape[1], T, Hkv, D,
-            _stream_of(device)))
+            k_new.data_ptr(), v_new.data_ptr(), ld, q_seq.data_ptr(), q_pos.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), kind, num_pages, page_table.data_ptr(),
+            page_table.shape[0], page_table.shape[1], T, Hkv, D, _stream_of(device)))
 
 
 def kv_read_q8(q_seq, q_pos, k_cache, v_cache, k_scale, v_scale, page_table, k_out=None, v_out=None, stream=None):
@@ -562,9 +562,9 @@ def kv_read_q8(q_seq, q_pos, k_cache, v_cache, k_scale, v_scale, page_table, k_o
         if T == 0:
             return k_out, v_out
         _check("bi_kv_read_q8", lib().bi_kv_read_q8(
-            k_out.data_ptr(), v_out.data_ptr(), ld, q_seq.data_ptr(), q_pos.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), kind, num_pages, page_table.data_ptr(), page_table.shape[0], page_table.shape[1], T, Hkv, D,
-            _stream_of(device)))
+            k_out.data_ptr(), v_out.data_ptr(), ld, q_seq.data_ptr(), q_pos.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), kind, num_pages, page_table.data_ptr(),
+            page_table.shape[0], page_table.shape[1], T, Hkv, D, _stream_of(device)))
     return k_out, v_out
 
 
@@ -593,8 +593,9 @@ def attention_decode_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_l
             return out
         ws, nbytes = _workspace(attention_workspace_size(B, Hq, D, maxp), device, workspace)
         _check("bi_attention_decode_q8", lib().bi_attention_decode_q8(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), kind, num_pages, page_table.data_ptr(),
-            maxp, seq_lens.data_ptr(), out.data_ptr(), B, Hq, Hkv, D, scale, ws.data_ptr(), nbytes, _stream_of(device)))
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), kind,
+            num_pages, page_table.data_ptr(), maxp, seq_lens.data_ptr(), out.data_ptr(), B, Hq, Hkv, D, scale,
+            ws.data_ptr(), nbytes, _stream_of(device)))
     return out
 
 
@@ -628,9 +629,9 @@ def attention_prefill_q8(q, q_seq, q_pos, k_cache, v_cache, k_scale, v_scale, pa
             return out
         ws, nbytes = _workspace(attention_prefill_q8_workspace_size(T), device, workspace)
         _check("bi_attention_prefill_q8", lib().bi_attention_prefill_q8(
-            q.data_ptr(), ldq, q_seq.data_ptr(), q_pos.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), kind,
-            num_pages, page_table.data_ptr(), num_seqs, maxp, out.data_ptr(), T, Hq, Hkv, D, scale, ws.data_ptr(), nbytes,
-            _stream_of(device)))
+            q.data_ptr(), ldq, q_seq.data_ptr(), q_pos.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), kind, num_pages, page_table.data_ptr(), num_seqs, maxp,
+            out.data_ptr(), T, Hq, Hkv, D, scale, ws.data_ptr(), nbytes, _stream_of(device)))
     return out
 
 
@@ -665,9 +666,9 @@ def qk_norm_rope(q, k, q_weight, k_weight, pos, cos_sin, eps: float = 1e-6, q_ou
         return q_out, k_out
     with _launch_on(device, stream):
         _check("bi_qk_norm_rope", lib().bi_qk_norm_rope(
-            q.data_ptr(), _rows3(q, "q"), k.data_ptr(), _rows3(k, "k"), q_weight.data_ptr(), k_weight.data_ptr(), pos.data_ptr(),
-            cos_sin.data_ptr(), cos_sin.shape[0], eps, q_out.data_ptr(), _rows3(q_out, "q_out"), k_out.data_ptr(),
-            _rows3(k_out, "k_out"), T, Hq, Hkv, D, _stream_of(device)))
+            q.data_ptr(), _rows3(q, "q"), k.data_ptr(), _rows3(k, "k"), q_weight.data_ptr(), k_weight.data_ptr(),
+            pos.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], eps, q_out.data_ptr(), _rows3(q_out, "q_out"),
+            k_out.data_ptr(), _rows3(k_out, "k_out"), T, Hq, Hkv, D, _stream_of(device)))
     return q_out, k_out
 
 

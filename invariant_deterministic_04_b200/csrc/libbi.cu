@@ -315,7 +315,7 @@ cudaError_t q8_prefill(const Q8Call& a, int32_t* list, bi::attnq8::Counts* count
   const int64_t few_full = (int64_t)a.sms * few_sm / a8::kFewCluster * a8::kFewCluster;
   // Clusters where a row can have more splits than a CTA's warps take at a time; then short chunks go
   // as few-row tiles too, where the clusters take them in one round: a CTA of the wide tiles would walk
-  // the whole context (16 rows at 4000 tokens 151 us, 63 in clusters; 48 rows, two rounds, 154 and 156).
+  // the whole context (16 rows at 4000 tokens 151 us, 62 in clusters; 48 rows, two rounds, 154 and 156).
   const bool clusters = max_splits(a.R.max_pages) > a8::kFewWarps;
   const bool all_few = clusters && ((int64_t)a.rows + few - 1) / few * a.Hkv <= few_full / a8::kFewCluster;
   const int per = all_few ? few : q8_tile_tokens(a.rows, G, a.Hkv, a8::TileShape<D>::ROWS, a.sms);
