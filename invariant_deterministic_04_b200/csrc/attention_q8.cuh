@@ -221,7 +221,7 @@ struct State {
 
 // What the fold needs of the lane's tokens g and g + 8.
 struct Tokens {
-  float ks[2], sv[2], z0[2];  // key and value scale; added to z: 0, or -infinity for a token on a page that is not there
+  float ks[2], sv[2], z0[2];  // key and value scale; added to z: 0, or -infinity where there is no value scale (0)
 };
 
 // Weights of one page from its scores s (which become z): moves m and F (and l and o with them) where
@@ -439,7 +439,7 @@ __device__ __forceinline__ void fold_page(const Query<D, NT>& Q, float (&s)[NT][
   for (int t = 0; t < 2; ++t) {
     T.ks[t] = ld_shared_f32(scales + 4 * g + 32 * t);
     T.sv[t] = ld_shared_f32(scales + 64 + 4 * g + 32 * t);
-    T.z0[t] = 0.f;
+    T.z0[t] = T.sv[t] == 0.f ? -INFINITY : 0.f;
   }
   uint32_t w[NT][2];
   auto set_tokens = [&] {  // lane c of four ORs its quarter of the rows of tokens g and g + 8

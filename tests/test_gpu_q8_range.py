@@ -216,3 +216,25 @@ def test_prompts_over_mixed_value_rows_have_the_decode_bits(kind, Hq, Hkv, D):
         ref, tol = attend(q[t].cpu().double().numpy(), k64[:, : t + 1], v64[:, : t + 1], sv[:, : t + 1], D ** -0.5)
         err = np.abs(dec[t].cpu().double().numpy() - ref)
         assert (err <= tol).all(), (t, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_slots_without_a_value_scale_have_no_weight(kind):
+    """Slots of a store that was cleared to zeros and not written (no contract covers them): a value
+    scale of 0 takes the token out of the softmax, in decode and in prefill alike."""
+    n, D, Hkv = 300, 128, 2
+    S, pt = fill(kind, [n], Hkv, D, 20, seed=903)
+    hole = [0, 5, 17, 256, 290]
+    for i in hole:
+        for t in (S.k.view(torch.int8), S.v.view(torch.int8), S.ks, S.vs):
+            t[pt[0, i // 16], :, i % 16] = 0
+    q = synth.normal_bf16((n, 8, D), 830).to(dev())
+    seq, pos = torch.zeros(n, dtype=torch.int32, device=dev()), torch.arange(n, dtype=torch.int32, device=dev())
+    pre = bi.attention_prefill_q8(q, seq, pos, *S.args)
+    dec = bi.attention_decode_q8(q, *S.args[:4], S.pt.expand(n, -1).contiguous(), pos + 1)
+    assert same_bits(pre, dec) and bool((dec[0] == 0).all()) and bi.get_device_error() == 0
+    keep = [i for i in range(n) if i not in hole]
+    pages = pt[0, : -(-n // 16)].tolist()
+    ref, tol = attend(q[-1].cpu().double().numpy(), S.values("k", pages, n)[:, keep], S.values("v", pages, n)[:, keep],
+                      S.value_scales(pages, n)[:, keep], D ** -0.5)
+    assert (np.abs(dec[-1].cpu().double().numpy() - ref) <= tol).all()
