@@ -68,6 +68,7 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float nan() { return __uint_as_float(0x7FC00000u); }
 // 1 / x of a normal number (of a smaller one: infinity).
 __device__ __forceinline__ float rcp(float x) {
   float y;
@@ -159,11 +160,14 @@ constexpr float kMostL = 0x1p24f;    // a lane's l that moves the references
 constexpr float kMostF = 0x1p120f;
 constexpr float kNoScale = 0x1p-149f;  // value scale of a row of zeros, where F is found and after
 
-// NT tiles of 8 query rows.
+// NT tiles of 8 query rows. A row that is not finite is taken as zeros and marked: its sum l becomes NaN
+// if it saw a token. (A NaN in its scores would make pages that are not there count.)
 template <int D, int NT>
 struct Query {
   uint32_t b[NT][D / 16][2];
-  float2 c[NT];  // of rows 8 n + 2c, + 1: scale log2(e) / the row's power of two; NaN if the row is not finite
+  float2 c[NT];  // of rows 8 n + 2c, + 1: scale log2(e) / the row's power of two
+  uint32_t bad;  // bit 2 n + r: row 8 n + 2c + r is not finite
+  __device__ __forceinline__ bool marked(int n, int r) const { return bad >> (2 * n + r) & 1u; }
 };
 
 // Loads query row g of tile n (nullptr: zeros). All lanes of the warp call it.
@@ -187,13 +191,15 @@ __device__ __forceinline__ void load_query(Query<D, NT>& Q, int n, const uint16_
   const bool finite = m < kvq8::kNonFiniteBits;
   const float up = __uint_as_float((uint32_t)(127 + 14 - (finite ? e : 14)) << 23);
   const float down = __uint_as_float((uint32_t)(127 - 14 + (finite ? e : 14)) << 23);
-  const float mine = finite ? __fmul_rn(scale_log2, down) : __uint_as_float(0x7FC00000u);
-  Q.c[n] = make_float2(__shfl_sync(kFullMask, mine, 8 * c), __shfl_sync(kFullMask, mine, 8 * c + 4));
+  const float mine = finite ? __fmul_rn(scale_log2, down) : nan();
+  const float c0 = __shfl_sync(kFullMask, mine, 8 * c), c1 = __shfl_sync(kFullMask, mine, 8 * c + 4);
+  Q.bad = (n ? Q.bad : 0u) | (c0 != c0 ? 1u << (2 * n) : 0u) | (c1 != c1 ? 2u << (2 * n) : 0u);
+  Q.c[n] = make_float2(c0 != c0 ? 0.f : c0, c1 != c1 ? 0.f : c1);
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) {
     // 4 dims: elements 4 (j%4) .. + 3 of the 16 in x[j/4]
     const uint4 q = x[j / 4][(j % 4) / 2];
-    const uint32_t w0 = (j & 1) ? q.z : q.x, w1 = (j & 1) ? q.w : q.y;
+    const uint32_t w0 = finite ? (j & 1) ? q.z : q.x : 0u, w1 = finite ? (j & 1) ? q.w : q.y : 0u;
     Q.b[n][j][0] = pack_f16x2(__fmul_rn(bf16lo(w0), up), __fmul_rn(bf16hi(w0), up));
     Q.b[n][j][1] = pack_f16x2(__fmul_rn(bf16lo(w1), up), __fmul_rn(bf16hi(w1), up));
   }
@@ -714,7 +720,7 @@ __global__ void __launch_bounds__(W * 32, kSmWarps<D, NT> / W)
         for (int i = 0; i < D / 16; i += 2)
           *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(E.value(S.o[n][i][r]), E.value(S.o[n][i][2 + r]),
                                                                 E.value(S.o[n][i + 1][r]), E.value(S.o[n][i + 1][2 + r]));
-        if (g == 0) pml[slot] = make_float2(E.m, E.l);
+        if (g == 0) pml[slot] = make_float2(E.m, Q.marked(n, r) && E.l > 0.f ? nan() : E.l);
       }
     if (item + step >= total) break;
     item += step;
@@ -1026,7 +1032,8 @@ struct TileSmem {
   static constexpr int LENS = STATS + P::FOLD * 32 * P::NT * 16;  // visible lengths, lane by lane
   static constexpr int BARS = LENS + P::FOLD * 32 * P::NT * 8;
   static constexpr int ARGS = BARS + kRing * 16;                   // two TileArgs
-  static constexpr int QUERY = ARGS + 512;                         // a third tile's queries, lane by lane
+  static constexpr int MARKS = ARGS + 512;                         // the query rows that are not finite, lane by lane
+  static constexpr int QUERY = MARKS + P::FOLD * 128;              // a third tile's queries, lane by lane
   static constexpr int BYTES = QUERY + (P::NT == 3 ? P::FOLD * (D / 32) * 512 : 0);
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
@@ -1230,6 +1237,8 @@ __device__ __forceinline__ void fold_tile(const TileArgs& A, uint8_t* smem, uint
   shortest = __reduce_min_sync(kFullMask, shortest);
 #pragma unroll
   for (int n = 0; n < LIVE; ++n) stats[32 * n] = make_float4(kUnseen, kUnseen, 0.f, 0.f);
+  uint32_t* marks = reinterpret_cast<uint32_t*>(smem + M::MARKS) + warp * 32 + lane;  // (no register for them in the loop)
+  *marks = Q.bad;
 #pragma unroll 8
   for (int i = 0; i < LIVE * D / 4; ++i) tot[32 * i] = 0.f;
 #pragma unroll 1
@@ -1287,7 +1296,9 @@ __device__ __forceinline__ void fold_tile(const TileArgs& A, uint8_t* smem, uint
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) x[i] = tot[32 * ((n * 2 + r) * (D / 8) + i)];
       const int len = r ? lens[32 * n].y : lens[32 * n].x;
-      store_row<D>(A.out + ((int64_t)(A.first + k / A.G) * A.Hq + A.kh * A.G + k % A.G) * D + (D / 8) * g, x, r ? st.w : st.z,
+      float L = r ? st.w : st.z;
+      if (L > 0.f && *marks >> (2 * n + r) & 1u) L = nan();
+      store_row<D>(A.out + ((int64_t)(A.first + k / A.G) * A.Hq + A.kh * A.G + k % A.G) * D + (D / 8) * g, x, L,
                    (len + SPLIT - 1) / SPLIT);
     }
 }
@@ -1488,7 +1499,7 @@ __device__ __forceinline__ void few_tile(const uint16_t* __restrict__ q, int64_t
           for (int i = 0; i < D / 16; i += 2)
             *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(E.value(S.o[n][i][r]), E.value(S.o[n][i][2 + r]),
                                                                   E.value(S.o[n][i + 1][r]), E.value(S.o[n][i + 1][2 + r]));
-          if (g == 0) pml[warp * kFewRows + k] = make_float2(E.m, E.l);
+          if (g == 0) pml[warp * kFewRows + k] = make_float2(E.m, Q.marked(n, r) && E.l > 0.f ? nan() : E.l);
         }
     }
     sync();

@@ -238,3 +238,44 @@ def test_slots_without_a_value_scale_have_no_weight(kind):
     ref, tol = attend(q[-1].cpu().double().numpy(), S.values("k", pages, n)[:, keep], S.values("v", pages, n)[:, keep],
                       S.value_scales(pages, n)[:, keep], D ** -0.5)
     assert (np.abs(dec[-1].cpu().double().numpy() - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_non_finite_queries_over_pages_that_are_not_there(kind, D):
+    """A query with a NaN or an infinity that sees no page of the store reads zeros, one that sees some
+    reads NaN, in a wide tile as in decode."""
+    n, T = 300, 40
+    S, pt = fill(kind, [n], 2, D, 20, seed=904)
+    q = synth.normal_bf16((T, 8, D), 840)
+    q[::2, 0, 3], q[1::2, 5, D - 1] = float("nan"), float("inf")
+    q = q.to(dev())
+    pos = torch.arange(n - T, n, dtype=torch.int32, device=dev())
+    for gone in (range(20), range(0, 20, 2)):
+        S.pt[0] = pt[0].to(dev())
+        for i in gone:
+            S.pt[0, i] = S.k.shape[0] + i if i % 3 else -1
+        pre = bi.attention_prefill_q8(q, torch.zeros_like(pos), pos, *S.args)
+        assert bi.get_device_error() == 8
+        dec = bi.attention_decode_q8(q, *S.args[:4], S.pt.expand(T, -1).contiguous(), pos + 1)
+        assert bi.get_device_error() == 8 and same_bits(pre, dec)
+        bad = ~torch.isfinite(q.float()).all(-1)
+        assert torch.equal(torch.isnan(dec).all(-1), bad & (len(gone) < 20)) and (len(gone) < 20 or bool((dec == 0).all()))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_that_see_nothing_but_non_finite_tokens(kind, D):
+    """NaN keys, then NaN values, in all of the first 17 tokens: rows 0 to 16 see nothing else, and all
+    rows read NaN, with NaN and finite queries, in a wide tile as in decode."""
+    n = 60
+    for side in (0, 1):
+        kv = [synth.normal_bf16((n, 2, D), 850), synth.normal_bf16((n, 2, D), 851)]
+        kv[side][:17, :, 1] = float("nan")
+        S, _ = fill(kind, [n], 2, D, 8, seed=905, k=kv[0], v=kv[1])
+        q = synth.normal_bf16((n, 8, D), 852)
+        q[::3, 2, 0] = float("inf")
+        q, pos = q.to(dev()), torch.arange(n, dtype=torch.int32, device=dev())
+        pre = bi.attention_prefill_q8(q, torch.zeros_like(pos), pos, *S.args)
+        dec = bi.attention_decode_q8(q, *S.args[:4], S.pt.expand(n, -1).contiguous(), pos + 1)
+        assert same_bits(pre, dec) and bool(torch.isnan(dec).all()) and bi.get_device_error() == 0
