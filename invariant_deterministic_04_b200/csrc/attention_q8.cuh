@@ -501,7 +501,7 @@ __device__ __forceinline__ void fold_page(const Query<D, NT>& Q, float (&s)[NT][
 // Decode: one warp per (row, kv-head, split); the split's partial result goes to the workspace.
 //
 // Bound: HBM (Hkv (2 D + 8) bytes per token against 4 Hq D flops) where there are splits enough to
-// go round: 64 int8 sequences of up to 32768 tokens (2.2 GB) take 420 us, 5.3 TB/s. A single
+// go round: 64 int8 sequences of up to 32768 tokens (2.2 GB) take 424 us, 5.2 TB/s. A single
 // short round is bound by one warp's 16 pages one after another (one sequence of 16921 tokens: 21 us).
 // Each warp has a ring of kStages pages that one lane fills by TMA (two tiles and two 64-byte scale
 // rows a page), ahead across item boundaries, and widens pages from it. The same ring filled by
@@ -842,11 +842,11 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
 //     as it has warps at a time.
 // Either way a split is folded by one warp in the order above, and splits in ascending order.
 // Bound: the latency of a folding warp's instructions. One prompt of 4096 tokens (32 heads over 8,
-// D = 128, int8; 137 GFLOP) takes 0.584 ms, 235 TFLOP/s, where mma.sync itself gave 509 TFLOP/s on
+// D = 128, int8; 137 GFLOP) takes 0.593 ms, 232 TFLOP/s, where mma.sync itself gave 509 TFLOP/s on
 // operands in registers; the schedulers issue in a third of the cycles, and what is left is the
 // wait for one result after another with two (D = 64: three) folding warps on a scheduler, as
 // many as the accumulators leave room for.
-// (The figures below are from before the denominator had a reference of its own, which takes 6 %.)
+// (The figures below are from before the denominator had a reference of its own, which takes 6 to 8 %.)
 //   * D = 128: 3 tiles on 8 warps; 2 on 12 has no room for the accumulators (695 us against 600 then).
 //   * D = 64: 2 tiles on 12 warps (322 us for that prompt); 3 on 8 took 358, 3 on 12 403.
 //   * A third tile's queries are read from shared memory for each page: the registers that this
